@@ -44,7 +44,8 @@ HBM_GBS = 8000.0
 METRIC = "qlinear TFLOP/s (act-quant+GEMM) and % of FP8/FP4 MFMA peak, M=4608"
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_gemm_nvfp4_4608x3072x12288.md")
 # sources of the kernel the traffic counters were taken on; a changed source voids them
-TRAFFIC_SOURCES = ("precision_quantized_linear_amd/csrc/gemm_kernels.hip", "precision_quantized_linear_amd/csrc/qpl_dma.h",
+TRAFFIC_SOURCES = ("precision_quantized_linear_amd/csrc/gemm_kernels.hip", "precision_quantized_linear_amd/csrc/qpl_gemm.h",
+                   "precision_quantized_linear_amd/csrc/qpl_dma.h",
                    "precision_quantized_linear_amd/csrc/qpl_device.h", "precision_quantized_linear_amd/csrc/qpl_nvfp4.h")
 COPY_PROBE_BYTES = 256 << 20
 

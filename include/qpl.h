@@ -26,7 +26,8 @@
  *   and > 0, workspace large enough, and a current HIP device that is gfx950.
  * - Size limits of the linears (QPL_ERR_SHAPE beyond them): the GEMMs address a
  *   256-row tile of an operand with 32-bit offsets below 2^30, so K < 2^22 for
- *   fp8r and INT4 (K-byte rows) and K < 2^23 for nvfp4 (K/2-byte rows); with a
+ *   fp8r and INT4 (K-byte rows) and K < 2^23 for nvfp4 (K/2-byte rows); INT8 has
+ *   K <= 2^17, which keeps its int32 sums exact; with a
  *   low-rank branch (R > 0) K <= 2^21 and the activation's scales (8 M ceil(K/128)
  *   bytes for nvfp4, 4 M K/64 for INT4) below 2^31 bytes.
  * - Inputs must be finite: NaN or infinity in x or W is outside the contract.
@@ -53,7 +54,7 @@ typedef enum {
   QPL_ERR_LAUNCH = 7     /* the HIP runtime rejected a kernel launch */
 } qpl_status;
 
-typedef enum { QPL_FP8R = 0, QPL_NVFP4 = 1, QPL_INT4 = 2 } qpl_scheme;
+typedef enum { QPL_FP8R = 0, QPL_NVFP4 = 1, QPL_INT4 = 2, QPL_INT8 = 3 } qpl_scheme;
 
 /*
  * Row-wise FP8 quantization (guide "BFL (fp8r / nvfp4)", intro bullet on fp8r:
@@ -303,6 +304,90 @@ qpl_status qlinear_mlp_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t H,
                              uint16_t* y, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * 8-bit integer linear (W8A8): int8 codes with one fp32 scale per row of x (token)
+ * and one per row of W (output channel).
+ *   rule   a = max_k |x[m,k]|, s[m] = a / 127 (fp32, correctly rounded),
+ *          q[m,k] = rint(127 x[m,k] / a) of the exact quotient, ties to even (so a code
+ *          does not depend on how s was rounded); an all-zero row has s = 0 and
+ *          codes 0.  The same rule quantizes a weight [N,K].
+ * quant_act_int8: x bf16 [M,K] -> x_q int8 [M,K], x_scale float [M]; with smooth
+ *   (float [K] or NULL, as in quant_act_nvfp4) the quantized activation is
+ *   bf16_rne(x / smooth).
+ * qlinear_int8: y[m,n] = bf16_rne((sum_k q_x q_w) s_x[m] weight_scale[n]), the sum
+ *   exact in int32, with q_x, s_x from quant_act_int8(x, smooth).
+ *   weight int8 [N,K], any codes in [-128, 127]; weight_scale float [N]; ws of at
+ *   least qlinear_workspace_bytes(QPL_INT8, M, K, N, 0), which after the call holds
+ *   the quantized activation: x_q, then (from byte 256 ceil(M K / 256)) x_scale.
+ * qlinear_int8_ex: the same with an epilogue (see qlinear_fp8r_ex).
+ * All pointers 16-byte aligned.  K <= 2^17 for the linears (QPL_ERR_SHAPE beyond).
+ */
+qpl_status quant_act_int8(const uint16_t* x, int64_t M, int64_t K, const float* smooth,
+                          int8_t* x_q, float* x_scale, void* stream);
+qpl_status qlinear_int8(const uint16_t* x, int64_t M, int64_t K, int64_t N,
+                        const int8_t* weight, const float* weight_scale, const float* smooth,
+                        uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N,
+                           const int8_t* weight, const float* weight_scale, const float* smooth,
+                           const qpl_epilogue* epi, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Mixture-of-experts linears on the 8-bit integer scheme.  E experts (1..65536), each
+ * with its own weight; every token goes to topk of them (1..256).  Sizes: M, R, T topk
+ * below 2^31 - 2^16.  Index and offset arrays are device data that the calls do not check:
+ * whatever they hold, no call reads or writes outside the arrays it was given.
+ *
+ * expert_plan: sorts the router's choices by expert.
+ *   expert_ids  int32 [T, topk]  expert of each choice; an id outside [0, E) (say -1)
+ *                                means no expert
+ *   row_index   int32 [T topk]   out: the token of each place in expert order; -1 behind the last
+ *   slot        int32 [T, topk]  out: the place of each choice, -1 for no expert
+ *   offsets     int32 [E + 1]    out: expert e has the places offsets[e] .. offsets[e+1] - 1
+ *   Places of one expert are in order of (token, choice).  No workspace, no atomics.
+ *
+ * qlinear_grouped_int8: product row i of R, offsets[e] <= i < offsets[e+1], is
+ *   y[i] = bf16_rne(act((sum_k q_x q_w[e]) s_x weight_scale[e]))
+ *   with q_x, s_x the quantized row x[row_index[i]] (x[i] when row_index is NULL; then
+ *   R <= M).  Experts may have any number of rows, none included.
+ *   x             bf16 [M, K]
+ *   row_index     int32 [R] or NULL; an index outside [0, M) stands for a row of zeros
+ *   offsets       int32 [E + 1], nondecreasing, within [0, R] (else the rows' values are
+ *                 unspecified); rows of y in no expert's range are left untouched
+ *   weight        int8 [E, N, K], weight_scale float [E, N]
+ *   act           QPL_ACT_NONE or QPL_ACT_GELU_TANH
+ *   y             bf16 [R, N]
+ *   ws            at least qlinear_grouped_int8_workspace_bytes(R, K, N, E) bytes
+ *
+ * expert_combine: out[t] = bf16_rne(sum_j weights[t,j] y[slot[t,j]]), fp32, j ascending;
+ *   a slot outside [0, R) adds nothing (a token without experts gets zeros).
+ *   y bf16 [R, N], slot int32 [T, topk], weights float [T, topk], out bf16 [T, N].
+ *
+ * qlinear_moe_int8: a GELU MLP of experts, all of the above in one call:
+ *   plan of expert_ids; h = gelu(grouped(x, fc1)) with fc1 [E, H, K]; grouped(h, fc2) with
+ *   fc2 [E, N, H]; y [T, N] = combine with expert_weights float [T, topk].  h and
+ *   the experts' outputs are bf16.  ws of at least
+ *   qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E).
+ *
+ * expert_ids, row_index, slot, offsets and weights need 16-byte alignment as all other
+ * pointers do.  Errors as for the linears: QPL_ERR_SHAPE for E, topk or a size out
+ * of range, QPL_ERR_ARG for an unknown act.
+ */
+qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E,
+                       int32_t* row_index, int32_t* slot, int32_t* offsets, void* stream);
+size_t qlinear_grouped_int8_workspace_bytes(int64_t R, int64_t K, int64_t N, int64_t E);
+qpl_status qlinear_grouped_int8(const uint16_t* x, int64_t M, int64_t K, int64_t N, int64_t E,
+                                const int8_t* weight, const float* weight_scale,
+                                const int32_t* row_index, int64_t R, const int32_t* offsets, qpl_act act,
+                                uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+qpl_status expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot,
+                          const float* weights, int64_t T, int64_t topk, uint16_t* out, void* stream);
+size_t qlinear_moe_int8_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t H, int64_t N, int64_t E);
+qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, int64_t N, int64_t E, int64_t topk,
+                            const int32_t* expert_ids, const float* expert_weights,
+                            const int8_t* fc1_weight, const float* fc1_scale,
+                            const int8_t* fc2_weight, const float* fc2_scale,
+                            uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Dequantize a weight to bf16 (guide, "Kernels" section, last paragraph: on other
  * devices the weight is dequantized to compute_dtype on every forward and the
  * layer runs as a regular linear; that linear is the caller's).
@@ -317,7 +402,7 @@ qpl_status dequant_weight(qpl_scheme scheme, const uint8_t* weight, const void* 
                           float weight_scale_2, int64_t N, int64_t K,
                           uint16_t* w_bf16, void* stream);
 
-/* Bytes of scratch that qlinear_fp8r / qlinear_nvfp4 need for these sizes
+/* Bytes of scratch that the scheme's linear needs for these sizes
  * (0 if the sizes are invalid).  The scratch may be reused between calls that
  * are ordered on one stream. */
 size_t qlinear_workspace_bytes(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R);
@@ -364,7 +449,12 @@ typedef enum {
   QPL_KERNEL_QUANT_INT4_LOWRANK = 16, /* INT4 quantize fused with x L1 (qlinear_int4, R > 0) */
   QPL_KERNEL_GEMM_EPILOGUE = 17,    /* any GEMM with a GELU or QKV epilogue (the *_ex calls, fc1 of
                                        qlinear_mlp_nvfp4) */
-  QPL_KERNEL_COUNT = 18
+  QPL_KERNEL_QUANT_INT8 = 18,       /* quant_act_int8, and the quantize inside the 8-bit integer linears */
+  QPL_KERNEL_GEMM_INT8 = 19,
+  QPL_KERNEL_GEMM_INT8_GROUPED = 20,
+  QPL_KERNEL_EXPERT_PLAN = 21,
+  QPL_KERNEL_EXPERT_COMBINE = 22,
+  QPL_KERNEL_COUNT = 23
 } qpl_kernel;
 
 void qpl_timing_enable(int on);

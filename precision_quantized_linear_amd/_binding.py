@@ -15,17 +15,22 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqpl.so")
 QPL_FP8R = 0
 QPL_NVFP4 = 1
 QPL_INT4 = 2
+QPL_INT8 = 3
 
 EXPORTS = ("quant_act_fp8_row", "quant_act_nvfp4", "qlinear_fp8r", "qlinear_nvfp4", "dequant_weight",
            "quant_weight_awq", "qlinear_awq_w4a16", "quant_act_int4", "qlinear_int4", "qlinear_fp8r_ex",
            "qlinear_nvfp4_ex", "qlinear_int4_ex", "qlinear_mlp_nvfp4", "qlinear_mlp_nvfp4_workspace_bytes",
            "qlinear_workspace_bytes", "qpl_amax_bf16", "qpl_nvfp4_global_scale", "qpl_status_str",
-           "qpl_timing_enable", "qpl_timing_select", "qpl_timing_collect", "qlinear_fp8r_noalloc")
+           "qpl_timing_enable", "qpl_timing_select", "qpl_timing_collect", "qlinear_fp8r_noalloc",
+           "quant_act_int8", "qlinear_int8", "qlinear_int8_ex", "expert_plan", "qlinear_grouped_int8",
+           "qlinear_grouped_int8_workspace_bytes", "expert_combine", "qlinear_moe_int8",
+           "qlinear_moe_int8_workspace_bytes")
 
 # qpl_kernel order of include/qpl.h
 KERNELS = ("quant_fp8_row", "quant_nvfp4", "quant_nvfp4_linear", "gemm_fp8r", "gemm_nvfp4", "gemm_nvfp4_lowrank",
            "lowrank_prep", "dequant", "amax", "nvfp4_prep", "quant_nvfp4_lowrank", "quant_w4g", "gemv_w4a16",
-           "quant_int4", "int4_expand", "gemm_int4", "quant_int4_lowrank", "gemm_epilogue")
+           "quant_int4", "int4_expand", "gemm_int4", "quant_int4_lowrank", "gemm_epilogue", "quant_int8", "gemm_int8",
+           "gemm_int8_grouped", "expert_plan", "expert_combine")
 
 QPL_ACT_NONE = 0
 QPL_ACT_GELU_TANH = 1
@@ -79,6 +84,13 @@ def load():
         "qlinear_int4_ex": [P, I64, I64, I64, P, P, P, P, P, I64, P, P, P, SZ, P],
         "qlinear_mlp_nvfp4": [P, I64, I64, I64, I64, P, P, P, P, SZ, P],
         "qlinear_fp8r_noalloc": [P, I64, I64, I64, P, P, P, P],
+        "quant_act_int8": [P, I64, I64, P, P, P, P],
+        "qlinear_int8": [P, I64, I64, I64, P, P, P, P, P, SZ, P],
+        "qlinear_int8_ex": [P, I64, I64, I64, P, P, P, P, P, P, SZ, P],
+        "expert_plan": [P, I64, I64, I64, P, P, P, P],
+        "qlinear_grouped_int8": [P, I64, I64, I64, I64, P, P, P, I64, P, ctypes.c_int, P, P, SZ, P],
+        "expert_combine": [P, I64, I64, P, P, I64, I64, P, P],
+        "qlinear_moe_int8": [P, I64, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -88,6 +100,10 @@ def load():
     lib.qlinear_workspace_bytes.restype = SZ
     lib.qlinear_mlp_nvfp4_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64]
     lib.qlinear_mlp_nvfp4_workspace_bytes.restype = SZ
+    lib.qlinear_grouped_int8_workspace_bytes.argtypes = [I64, I64, I64, I64]
+    lib.qlinear_grouped_int8_workspace_bytes.restype = SZ
+    lib.qlinear_moe_int8_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64]
+    lib.qlinear_moe_int8_workspace_bytes.restype = SZ
     lib.qpl_nvfp4_global_scale.argtypes = [F]
     lib.qpl_nvfp4_global_scale.restype = F
     lib.qpl_status_str.argtypes = [ctypes.c_int]
@@ -330,6 +346,167 @@ def qlinear_mlp_nvfp4(x, fc1, fc2, y=None, workspace=None, stream=None):
     _check("qlinear_mlp_nvfp4", load().qlinear_mlp_nvfp4(_ptr(x), M, K, H, N, ctypes.byref(l1), ctypes.byref(l2),
                                                          _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
                                                          _stream(stream)))
+    return y
+
+
+def _on_current(t, name):
+    """The calls run on the current device: a tensor of another one would be read across devices."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current GPU, got {t.device}")
+
+
+def _out(t, shape, dtype, device, stream, name):
+    """t checked, or a new tensor that belongs to the stream the call runs on."""
+    if t is not None:
+        _expect(t, dtype, shape, name)
+        _on_current(t, name)
+        return t
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(ws, need, device, stream):
+    """(workspace, its bytes): the caller's, or a new one (need 0: sizes that the call refuses)."""
+    if ws is None:
+        ws = _out(None, (max(need, 1),), torch.uint8, device, stream, "workspace")
+    elif not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    _on_current(ws, "workspace")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _inputs(**tensors):
+    """name=(tensor or None, dtype, shape): each contiguous on the current GPU."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is not None:
+            _expect(t, dtype, shape, name)
+            _on_current(t, name)
+
+
+def quant_act_int8(x, smooth=None, x_q=None, x_scale=None, stream=None):
+    """bf16 [M,K] -> (int8 codes [M,K], fp32 row scales [M]); with smooth (float32 [K]) the
+    quantized activation is bf16(x / smooth).  The same call quantizes a weight [N,K]."""
+    M, K = _dims(x, 2, "x")
+    _inputs(x=(x, torch.bfloat16, (M, K)), smooth=(smooth, torch.float32, (K,)))
+    x_q = _out(x_q, (M, K), torch.int8, x.device, stream, "x_q")
+    x_scale = _out(x_scale, (M,), torch.float32, x.device, stream, "x_scale")
+    _check("quant_act_int8", load().quant_act_int8(_ptr(x), M, K, _ptr(smooth), _ptr(x_q), _ptr(x_scale),
+                                                    _stream(stream)))
+    return x_q, x_scale
+
+
+def qlinear_int8(x, weight, weight_scale, y=None, workspace=None, stream=None, smooth=None, act=None, qkv=None):
+    """y[M,N] bf16 = 8-bit integer linear of bf16 x [M,K] with int8 weight [N,K] and fp32
+    weight_scale [N]; smooth, act and qkv as in qlinear_int4."""
+    M, K = _dims(x, 2, "x")
+    N = _dims(weight, 2, "weight")[0]
+    _inputs(x=(x, torch.bfloat16, (M, K)), weight=(weight, torch.int8, (N, K)),
+            weight_scale=(weight_scale, torch.float32, (N,)), smooth=(smooth, torch.float32, (K,)))
+    if qkv is not None:
+        for t, name in zip(qkv[:3], ("q", "k", "v")):
+            _dims(t, 3, name)
+            _on_current(t, name)
+    elif act in _ACTS:
+        y = _out(y, (M, N), torch.bfloat16, x.device, stream, "y")
+    e, y, out = _epilogue(act, qkv, M, N, y, x.device)
+    ws, nbytes = _scratch(workspace, qlinear_workspace_bytes(QPL_INT8, M, K, N), x.device, stream)
+    args = (_ptr(x), M, K, N, _ptr(weight), _ptr(weight_scale), _ptr(smooth))
+    if e is None:
+        _check("qlinear_int8", load().qlinear_int8(*args, _ptr(y), _ptr(ws), nbytes, _stream(stream)))
+    else:
+        _check("qlinear_int8_ex", load().qlinear_int8_ex(*args, _ref(e), _ptr(y), _ptr(ws), nbytes, _stream(stream)))
+    return out
+
+
+def expert_plan(expert_ids, num_experts, row_index=None, slot=None, offsets=None, stream=None):
+    """Router choices int32 [T, topk] sorted by expert -> (row_index int32 [T topk]: the token of
+    each place; slot int32 [T, topk]: the place of each choice; offsets int32 [num_experts + 1]:
+    the experts' first places).  An id outside [0, num_experts) gets slot -1; row_index is -1
+    behind the last place."""
+    T, topk = _dims(expert_ids, 2, "expert_ids")
+    _inputs(expert_ids=(expert_ids, torch.int32, (T, topk)))
+    num_experts = int(num_experts)
+    if num_experts < 1:
+        raise ValueError(f"num_experts: expected at least 1, got {num_experts}")
+    row_index = _out(row_index, (T * topk,), torch.int32, expert_ids.device, stream, "row_index")
+    slot = _out(slot, (T, topk), torch.int32, expert_ids.device, stream, "slot")
+    offsets = _out(offsets, (num_experts + 1,), torch.int32, expert_ids.device, stream, "offsets")
+    _check("expert_plan", load().expert_plan(_ptr(expert_ids), T, topk, num_experts, _ptr(row_index), _ptr(slot),
+                                             _ptr(offsets), _stream(stream)))
+    return row_index, slot, offsets
+
+
+def qlinear_grouped_int8_workspace_bytes(R, K, N, E):
+    return int(load().qlinear_grouped_int8_workspace_bytes(R, K, N, E))
+
+
+def qlinear_grouped_int8(x, weight, weight_scale, offsets, row_index=None, y=None, workspace=None, stream=None,
+                         act=None):
+    """y[R,N] bf16: rows offsets[e] .. offsets[e+1] - 1 are the 8-bit integer linear of
+    x[row_index[i]] (bf16 [M,K]; x[i] without row_index, R = M) with expert e's int8 weight
+    [E,N,K] and fp32 weight_scale [E,N].  offsets int32 [E + 1] and row_index int32 [R] stay on
+    the GPU.  Rows of y in no expert's range are not written (a new y holds anything there)."""
+    M, K = _dims(x, 2, "x")
+    E, N = _dims(weight, 3, "weight")[:2]
+    R = M if row_index is None else _dims(row_index, 1, "row_index")[0]
+    _inputs(x=(x, torch.bfloat16, (M, K)), weight=(weight, torch.int8, (E, N, K)),
+            weight_scale=(weight_scale, torch.float32, (E, N)), offsets=(offsets, torch.int32, (E + 1,)),
+            row_index=(row_index, torch.int32, (R,)))
+    if act not in _ACTS:
+        raise ValueError(f"act: expected one of {sorted(k for k in _ACTS if k)}, got {act!r}")
+    y = _out(y, (R, N), torch.bfloat16, x.device, stream, "y")
+    ws, nbytes = _scratch(workspace, qlinear_grouped_int8_workspace_bytes(R, K, N, E), x.device, stream)
+    _check("qlinear_grouped_int8", load().qlinear_grouped_int8(
+        _ptr(x), M, K, N, E, _ptr(weight), _ptr(weight_scale), _ptr(row_index), R, _ptr(offsets), _ACTS[act], _ptr(y),
+        _ptr(ws), nbytes, _stream(stream)))
+    return y
+
+
+def expert_combine(y, slot, weights, out=None, stream=None):
+    """out[t] bf16 [T,N] = sum_j weights[t,j] y[slot[t,j]] of bf16 y [R,N], int32 slot [T,topk] and
+    fp32 weights [T,topk]; a slot outside [0, R) adds nothing."""
+    R, N = _dims(y, 2, "y")
+    T, topk = _dims(slot, 2, "slot")
+    _inputs(y=(y, torch.bfloat16, (R, N)), slot=(slot, torch.int32, (T, topk)),
+            weights=(weights, torch.float32, (T, topk)))
+    out = _out(out, (T, N), torch.bfloat16, y.device, stream, "out")
+    _check("expert_combine", load().expert_combine(_ptr(y), R, N, _ptr(slot), _ptr(weights), T, topk, _ptr(out),
+                                                   _stream(stream)))
+    return out
+
+
+def qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E):
+    return int(load().qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E))
+
+
+def qlinear_moe_int8(x, expert_ids, expert_weights, fc1, fc2, y=None, workspace=None, stream=None):
+    """y [T,N] bf16 = sum_j expert_weights[t,j] fc2_e(bf16(gelu(fc1_e(x[t])))) over e = expert_ids[t,j]
+    (int32 [T,topk]; an id outside the experts adds nothing); fc1 and fc2 are dicts with weight
+    int8 [E,H,K] / [E,N,H] and weight_scale float32 [E,H] / [E,N]."""
+    T, K = _dims(x, 2, "x")
+    topk = _dims(expert_ids, 2, "expert_ids")[1]
+    E, H = _dims(fc1["weight"], 3, "fc1.weight")[:2]
+    N = _dims(fc2["weight"], 3, "fc2.weight")[1]
+    _inputs(x=(x, torch.bfloat16, (T, K)), expert_ids=(expert_ids, torch.int32, (T, topk)),
+            expert_weights=(expert_weights, torch.float32, (T, topk)),
+            **{"fc1.weight": (fc1["weight"], torch.int8, (E, H, K)),
+               "fc1.weight_scale": (fc1["weight_scale"], torch.float32, (E, H)),
+               "fc2.weight": (fc2["weight"], torch.int8, (E, N, H)),
+               "fc2.weight_scale": (fc2["weight_scale"], torch.float32, (E, N))})
+    y = _out(y, (T, N), torch.bfloat16, x.device, stream, "y")
+    ws, nbytes = _scratch(workspace, qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E), x.device, stream)
+    _check("qlinear_moe_int8", load().qlinear_moe_int8(
+        _ptr(x), T, K, H, N, E, topk, _ptr(expert_ids), _ptr(expert_weights), _ptr(fc1["weight"]),
+        _ptr(fc1["weight_scale"]), _ptr(fc2["weight"]), _ptr(fc2["weight_scale"]), _ptr(y), _ptr(ws), nbytes,
+        _stream(stream)))
     return y
 
 

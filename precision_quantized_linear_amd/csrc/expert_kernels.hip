@@ -1,0 +1,176 @@
+// Routing of tokens to experts for gfx950: the sort of the router's choices by expert
+// and the weighted sum that brings the experts' rows back to their tokens.
+#include "qpl_device.h"
+#include "qpl_internal.h"
+
+namespace qpl {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Plan: a stable counting sort of n choices ids[i] in [0, E) without atomics or a
+// workspace.  Workgroup e serves expert e: it counts the choices below e (the
+// expert's first place) and its own, then hands out its places in order of i.
+// Each wavefront owns a contiguous run of choices, so a place is the expert's first +
+// the counts of earlier wavefronts + a ballot prefix.  Workgroup E serves the ids outside
+// [0, E): slot -1, and row_index -1 behind the last place.  Every workgroup reads
+// all choices (from L2), which costs less than a second launch.
+// ---------------------------------------------------------------------------
+template <int W>
+__global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ ids, int n, int topk, int E,
+                                                        int* __restrict__ row_index, int* __restrict__ slot,
+                                                        int* __restrict__ offsets) {
+  __shared__ int below_s[W], own_s[W];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int run = (n / (256 * W) + 1) * 256;  // choices per wavefront, a multiple of 256
+  const int64_t first = (int64_t)wv * run;
+  const int lo = first < n ? (int)first : n;
+  const int hi = first + run < n ? (int)(first + run) : n;
+  const uint64_t before = (1ull << lane) - 1ull;
+  // four consecutive choices of a lane; behind the end an id that is nobody's (INT_MIN
+  // counts as outside [0, E), but its place in the arrays is never written)
+  auto load = [&](int i, int (&v)[4]) {
+    if (i + 4 <= hi) {
+      const i32x4 t = *reinterpret_cast<const i32x4*>(ids + i);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = t[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = i + c < hi ? ids[i + c] : INT32_MIN;
+    }
+  };
+  for (int64_t e64 = blockIdx.x; e64 <= E; e64 += gridDim.x) {
+    const int e = (int)e64;
+    int below = 0, own = 0;
+    for (int i = lo + 4 * lane; i < hi; i += 256) {
+      int v[4];
+      load(i, v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        below += v[c] >= 0 && v[c] < e;
+        own += v[c] == e;
+      }
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      below += __shfl_xor(below, d, 64);
+      own += __shfl_xor(own, d, 64);
+    }
+    if (lane == 0) {
+      below_s[wv] = below;
+      own_s[wv] = own;
+    }
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < W; ++w) base += below_s[w];
+    if (threadIdx.x == 0) offsets[e] = base;
+    if (e < E) {
+      int place = base;
+      for (int w = 0; w < wv; ++w) place += own_s[w];
+      if (own_s[wv] != 0) {
+        for (int i0 = lo; i0 < hi; i0 += 256) {
+          const int i = i0 + 4 * lane;
+          int v[4];
+          load(i, v);
+          uint64_t b[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) b[c] = __ballot(v[c] == e);
+          int at = place;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            at += __popcll(b[c] & before);
+            place += __popcll(b[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (v[c] == e) {
+              slot[i + c] = at;
+              row_index[at] = (i + c) / topk;
+              ++at;
+            }
+        }
+      }
+    } else {
+      for (int i = lo + 4 * lane; i < hi; i += 256) {
+        int v[4];
+        load(i, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (i + c < hi && (v[c] < 0 || v[c] >= E)) slot[i + c] = -1;
+      }
+      for (int64_t i = (int64_t)base + threadIdx.x; i < n; i += 64 * W) row_index[i] = -1;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: out[t] = bf16(sum_j weight[t, j] y[slot[t, j]]), fp32, j ascending; a slot
+// outside [0, R) adds nothing.  VEC columns per thread (8: one 16-byte load per
+// row; 1 where rows are not 16-byte aligned).
+// ---------------------------------------------------------------------------
+template <int VEC>
+__global__ __launch_bounds__(256) void k_expert_combine(const uint16_t* __restrict__ y, int64_t R, int64_t N,
+                                                        const int* __restrict__ slot,
+                                                        const float* __restrict__ weight, int64_t T, int topk,
+                                                        uint16_t* __restrict__ out) {
+  const int64_t nv = N / VEC;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * nv; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / nv, c = (i - t * nv) * VEC;
+    const int* st = slot + t * topk;
+    const float* wt = weight + t * topk;
+    if constexpr (VEC == 8) {
+      float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int j = 0; j < topk; ++j) {
+        const int64_t s = st[j];
+        if (s >= 0 && s < R) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(y + s * N + c);
+          const float w = wt[j];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a[2 * k] = __builtin_fmaf(w, bf16_lo(v[k]), a[2 * k]);
+            a[2 * k + 1] = __builtin_fmaf(w, bf16_hi(v[k]), a[2 * k + 1]);
+          }
+        }
+      }
+      *reinterpret_cast<u32x4*>(out + t * N + c) =
+          u32x4{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7])};
+    } else {
+      float a = 0.0f;
+      for (int j = 0; j < topk; ++j) {
+        const int64_t s = st[j];
+        if (s >= 0 && s < R) a = __builtin_fmaf(wt[j], __uint_as_float((uint32_t)y[s * N + c] << 16), a);
+      }
+      out[t * N + c] = (uint16_t)pack_bf16(a, 0.0f);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
+                              int32_t* slot, int32_t* offsets, hipStream_t stream) {
+  const dim3 grid((unsigned)(E + 1));
+  if (n <= 4096)
+    hipLaunchKernelGGL((k_expert_plan<4>), grid, dim3(256), 0, stream, ids, (int)n, (int)topk, (int)E, row_index, slot,
+                       offsets);
+  else
+    hipLaunchKernelGGL((k_expert_plan<16>), grid, dim3(1024), 0, stream, ids, (int)n, (int)topk, (int)E, row_index,
+                       slot, offsets);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot, const float* weights,
+                                 int64_t T, int64_t topk, uint16_t* out, hipStream_t stream) {
+  const int64_t threads = N % 8 == 0 ? T * (N / 8) : T * N;
+  const int64_t blocks = (threads + 255) / 256;
+  const dim3 grid((unsigned)(blocks < (int64_t(1) << 22) ? blocks : int64_t(1) << 22)), block(256);
+  if (N % 8 == 0)
+    hipLaunchKernelGGL(k_expert_combine<8>, grid, block, 0, stream, y, R, N, slot, weights, T, (int)topk, out);
+  else
+    hipLaunchKernelGGL(k_expert_combine<1>, grid, block, 0, stream, y, R, N, slot, weights, T, (int)topk, out);
+  return hipGetLastError();
+}
+
+}  // namespace qpl

@@ -1,0 +1,430 @@
+// 8-bit integer linears for gfx950: y = act((q_x q_w^T) s_x s_w) with a scale for each
+// row of x (token) and each row of W (output channel), dense or grouped by expert.
+//
+// Quantizer.  a = max_k |x[m, k]|, s = fp32(a / 127), q = rint(127 x / a), ties to even.
+// The sums of products are int32 and exact for K <= 2^17 (127 * 128 * 2^17 < 2^31), so a
+// result does not depend on how K is split over wavefronts or workgroups.
+#include "qpl_gemm.h"
+
+namespace qpl {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Row quantizer: one wavefront per row, four rows per workgroup (VPT 16-byte vectors
+// per lane stay in registers between the two passes; VPT == 0 streams the row twice).
+//
+// The code is rint of the exact quotient 127 x / a.  x = i 2^p and a = j 2^q have 8-bit
+// integers i, j, so 127 x / a either is a tie (k + 1/2, at most 8 significant bits) or
+// differs from every tie by more than 1 / (254 * 255) = 1.5e-5 of itself: the numerator
+// of the difference is a nonzero integer over 2 * 127 i.  t = x * fp32(127 / a) is off
+// by less than 2^-22.9 of itself.  Rounding t to 16 fraction bits (off by at most 2^-17 =
+// 7.6e-6) puts a tie back on the tie and moves nothing across one; then adding 1.5 * 2^23
+// rounds to the nearest integer, ties to even, and leaves the code in the low byte.
+// ---------------------------------------------------------------------------
+struct RowCode {
+  float s, r, up;  // scale; 127 / (a up); up = 2^100 for rows whose 127 / a might overflow, else 1
+  bool zero, tiny;
+};
+
+__device__ __forceinline__ RowCode row_code(float amax) {
+  RowCode d;
+  d.s = amax / 127.0f;
+  d.zero = !(amax > 0.0f);
+  d.tiny = amax < 0x1p-100f;
+  d.up = d.tiny ? 0x1p100f : 1.0f;
+  d.r = d.zero ? 0.0f : 127.0f / (amax * d.up);
+  return d;
+}
+
+// Bits whose low byte is the code of x.
+__device__ __forceinline__ uint32_t code_bits(float x, float r) {
+  const uint32_t t = (__float_as_uint(x * r) + 0x40u) & 0xFFFFFF80u;
+  return __float_as_uint(__uint_as_float(t) + 0x1.8p23f);
+}
+
+// Codes of two bf16 pairs, in order.
+__device__ __forceinline__ uint32_t code_word(uint32_t a, uint32_t b, const RowCode& d) {
+  const float u = d.tiny ? d.up : 1.0f;
+  float x0 = bf16_lo(a), x1 = bf16_hi(a), x2 = bf16_lo(b), x3 = bf16_hi(b);
+  if (d.tiny) {
+    x0 *= u;
+    x1 *= u;
+    x2 *= u;
+    x3 *= u;
+  }
+  const uint32_t lo = __builtin_amdgcn_perm(code_bits(x1, d.r), code_bits(x0, d.r), 0x0C0C0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(code_bits(x3, d.r), code_bits(x2, d.r), 0x04000C0Cu);
+  return lo | hi;
+}
+
+__device__ __forceinline__ u32x2 code_vec(const u32x4& v, const RowCode& d) {
+  return u32x2{code_word(v.x, v.y, d), code_word(v.z, v.w, d)};
+}
+
+__device__ __forceinline__ uint32_t vec_absmax8(const u32x4& v, uint32_t m) {
+  return absmax_acc(absmax_acc(absmax_acc(absmax_acc(m, v.x), v.y), v.z), v.w);
+}
+
+__device__ __forceinline__ u32x4 smooth_vec(const u32x4& v, const float* __restrict__ lam) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(lam), b = *reinterpret_cast<const f32x4*>(lam + 4);
+  return u32x4{smooth_pair(v.x, a[0], a[1]), smooth_pair(v.y, a[2], a[3]), smooth_pair(v.z, b[0], b[1]),
+               smooth_pair(v.w, b[2], b[3])};
+}
+
+// GATHER: row i is x[row_index[i]] (a row of zeros for an index outside x).
+template <int VPT, bool SMOOTH, bool GATHER>
+__device__ __forceinline__ void quant_row(const uint16_t* __restrict__ x, int64_t rows_x, int64_t row, int64_t K,
+                                          const float* __restrict__ lam, const int* __restrict__ row_index,
+                                          int8_t* __restrict__ xq, float* __restrict__ xs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t nv = K >> 3;
+  u32x2* qr = reinterpret_cast<u32x2*>(xq + row * K);
+  int64_t src = row;
+  if constexpr (GATHER) {
+    src = row_index[row];
+    if (src < 0 || src >= rows_x) {
+      for (int64_t j = lane; j < nv; j += 64) qr[j] = u32x2{0u, 0u};
+      if (lane == 0) xs[row] = 0.0f;
+      return;
+    }
+  }
+  const u32x4* xr = reinterpret_cast<const u32x4*>(x + src * K);
+  uint32_t am = 0;
+  if constexpr (VPT > 0) {
+    u32x4 v[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t j = lane + 64 * i;
+      if (j < nv) {
+        v[i] = GATHER ? xr[j] : __builtin_nontemporal_load(xr + j);
+        if constexpr (SMOOTH) v[i] = smooth_vec(v[i], lam + 8 * j);
+        am = vec_absmax8(v[i], am);
+      }
+    }
+    const RowCode d = row_code(wave_max(absmax_value(am)));
+    if (lane == 0) xs[row] = d.s;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t j = lane + 64 * i;
+      if (j < nv) qr[j] = code_vec(v[i], d);
+    }
+  } else {
+    for (int64_t j = lane; j < nv; j += 64) {
+      u32x4 v = xr[j];
+      if constexpr (SMOOTH) v = smooth_vec(v, lam + 8 * j);
+      am = vec_absmax8(v, am);
+    }
+    const RowCode d = row_code(wave_max(absmax_value(am)));
+    if (lane == 0) xs[row] = d.s;
+    for (int64_t j = lane; j < nv; j += 64) {
+      u32x4 v = xr[j];
+      if constexpr (SMOOTH) v = smooth_vec(v, lam + 8 * j);
+      qr[j] = code_vec(v, d);
+    }
+  }
+}
+
+// One row tile of a grouped product: rows [m0, m1) of expert e.
+struct RowTile {
+  int m0, m1, e, pad;
+};
+
+// The experts' rows cut into tiles of `tm` rows that never cross an expert, in order;
+// count[0] = their number (at most cap).  offsets [E + 1] are clamped into [0, R], so
+// whatever they hold no tile leaves the R rows.  One workgroup.
+__device__ __forceinline__ void build_row_tiles(const int* __restrict__ offsets, int E, int R, int tm, int cap,
+                                                int* __restrict__ count, RowTile* __restrict__ tiles) {
+  __shared__ int wsum[4];
+  __shared__ int base;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  if (threadIdx.x == 0) base = 0;
+  __syncthreads();
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    const int e = e0 + (int)threadIdx.x;
+    int lo = 0, hi = 0;
+    if (e < E) {
+      lo = min(max(offsets[e], 0), R);
+      hi = min(max(offsets[e + 1], lo), R);
+    }
+    const int n = (int)(((int64_t)hi - lo + tm - 1) / tm);
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += o;
+    }
+    if (lane == 63) wsum[wv] = sum;
+    __syncthreads();
+    int first = base + sum - n;
+    for (int w = 0; w < wv; ++w) first += wsum[w];
+    for (int i = 0; i < n && first + i < cap; ++i)
+      tiles[first + i] = RowTile{lo + i * tm, (int)min((int64_t)hi, (int64_t)lo + (int64_t)(i + 1) * tm), e, 0};
+    __syncthreads();
+    if (threadIdx.x == 0) base += wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) count[0] = min(base, cap);
+}
+
+struct TilePlan {
+  const int* offsets;
+  int E, R, tm, cap;
+  int* count;
+  RowTile* tiles;
+};
+
+template <int VPT, bool SMOOTH, bool GROUPED, bool GATHER>
+__global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__ x, int64_t rows_x, int64_t rows,
+                                                    int64_t K, const float* __restrict__ lam,
+                                                    const int* __restrict__ row_index, int8_t* __restrict__ xq,
+                                                    float* __restrict__ xs, TilePlan plan) {
+  int64_t blk = blockIdx.x, nblk = gridDim.x;
+  if constexpr (GROUPED) {
+    // workgroup 0 cuts the experts' rows into tiles for the product that follows
+    if (blk == 0) {
+      build_row_tiles(plan.offsets, plan.E, plan.R, plan.tm, plan.cap, plan.count, plan.tiles);
+      return;
+    }
+    blk -= 1;
+    nblk -= 1;
+  }
+  for (int64_t row = blk * 4 + (threadIdx.x >> 6); row < rows; row += nblk * 4)
+    quant_row<VPT, SMOOTH, GATHER>(x, rows_x, row, K, lam, row_index, xq, xs);
+}
+
+constexpr int64_t kQuantBlocks = int64_t(1) << 22;  // workgroups stride over rows past this many
+
+template <bool SMOOTH, bool GROUPED, bool GATHER>
+hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, const float* lam,
+                             const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
+  const int64_t per_lane = (K / 8 + 63) / 64;
+  const int64_t blocks = (rows + 3) / 4;
+  const dim3 grid((unsigned)((blocks < kQuantBlocks ? blocks : kQuantBlocks) + (GROUPED ? 1 : 0))), block(256);
+#define QPL_CASE(V)                                                                                          \
+  if (per_lane <= V || V == 0) {                                                                             \
+    hipLaunchKernelGGL((k_quant_int8<V, SMOOTH, GROUPED, GATHER>), grid, block, 0, stream, x, rows_x, rows, K, lam, \
+                       row_index, xq, xs, plan);                                                             \
+    return hipGetLastError();                                                                                \
+  }
+  QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(16) QPL_CASE(24) QPL_CASE(0)
+#undef QPL_CASE
+  return hipErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// The product without LDS staging.  A workgroup of W wavefronts owns 16 NT columns
+// of y (rows of the weight) and 16 MT rows; its wavefronts take the 128-byte pieces of K in
+// turn, each lane loading its MFMA operands (V_MFMA_I32_16X16X64_I8, 16 bytes per lane)
+// straight from memory, and their int32 sums meet in LDS.
+//
+// The operands are swapped (the MFMA computes y^T), so a lane holds four consecutive
+// columns of one row.  Row r of an operand and bytes 64 s + 16 (l / 16) of the piece go
+// to lane l with l % 16 = r.  x lanes past K read zeros, which makes the weight bytes beside them (the next
+// row's, or zeros past the weight's end) irrelevant.
+// ---------------------------------------------------------------------------
+struct Int8Args {
+  const int8_t* x;  // [rows, K]
+  const int8_t* w;  // [N, K], or [E, N, K]
+  const float* xs;
+  const float* ws;  // [N], or [E, N]
+  int64_t M, N;
+  int K;
+  int64_t tiles_m, tiles_n;
+  const int* count;      // grouped: number of row tiles
+  const RowTile* tiles;  // grouped: the row tiles
+};
+
+typedef int i32x4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, (int)kRawBufferWord3);
+}
+
+template <int MT, int NT, int W, int EPI, bool GROUPED>
+__global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __restrict__ Y, EpiArgs e) {
+  constexpr int U = MT * NT >= 8 ? 1 : 2;  // pieces loaded together
+  __shared__ i32x4 red[W][MT * NT][64];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int r16 = lane & 15, q = lane >> 4;
+  const int64_t tiles_m = GROUPED ? p.count[0] : p.tiles_m;
+  const int pieces = (p.K + 127) >> 7;
+  for (int64_t t = blockIdx.x; t < tiles_m * p.tiles_n; t += gridDim.x) {
+    const int64_t tm = t / p.tiles_n, n0 = (t - tm * p.tiles_n) * 16 * NT;
+    int64_t m0, m1;
+    const int8_t* w = p.w;
+    const float* wsc = p.ws;
+    if constexpr (GROUPED) {
+      const RowTile rt = p.tiles[tm];
+      m0 = rt.m0;
+      m1 = rt.m1;
+      w += (int64_t)rt.e * p.N * p.K;
+      wsc += (int64_t)rt.e * p.N;
+    } else {
+      m0 = tm * 16 * MT;
+      m1 = p.M - m0 < 16 * MT ? p.M : m0 + 16 * MT;
+    }
+    const int64_t nr = p.N - n0 < 16 * NT ? p.N - n0 : 16 * NT;
+    const __amdgpu_buffer_rsrc_t dx = make_rsrc(p.x + m0 * p.K, (m1 - m0) * p.K);
+    const __amdgpu_buffer_rsrc_t dw = make_rsrc(w + n0 * p.K, nr * p.K);
+    i32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    for (int c = wv; c < pieces; c += W * U) {
+      i32x4 fx[U][2][MT], fw[U][2][NT];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int k = (c + u * W) * 128 + 64 * s + 16 * q;
+          const bool in = k < p.K;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            fw[u][s][j] = load16(dw, in ? (uint32_t)((16 * j + r16) * p.K + k) : kOutOfRange);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            fx[u][s][i] = load16(dx, in ? (uint32_t)((16 * i + r16) * p.K + k) : kOutOfRange);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx[u][s][i], acc[i][j], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) red[wv][i * NT + j][lane] = acc[i][j];
+    __syncthreads();
+    // vector v: tile v / 64 (row block i, column block j), lane v % 64's four columns
+    for (int v = threadIdx.x; v < MT * NT * 64; v += 64 * W) {
+      const int tile = v >> 6, l = v & 63;
+      i32x4 sum = red[0][tile][l];
+#pragma unroll
+      for (int k = 1; k < W; ++k) sum += red[k][tile][l];
+      const int64_t m = m0 + 16 * (tile / NT) + (l & 15);
+      const int64_t n = n0 + 16 * (tile % NT) + 4 * (l >> 4);
+      if (m < m1 && n < p.N) {
+        const float sx = p.xs[m];
+        float o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[k] = ((float)sum[k] * sx) * wsc[n + k < p.N ? n + k : n];
+          if constexpr ((EPI & EPI_GELU) != 0) o[k] = gelu_tanh(o[k]);
+        }
+        uint16_t* dst = out_ptr<EPI>(Y, m, n, p.N, e);
+        const uint32_t w0 = pack_bf16(o[0], o[1]), w1 = pack_bf16(o[2], o[3]);
+        if ((p.N & 3) == 0) {
+          *reinterpret_cast<u32x2*>(dst) = u32x2{w0, w1};
+        } else {
+          dst[0] = (uint16_t)w0;
+          if (n + 1 < p.N) dst[1] = (uint16_t)(w0 >> 16);
+          if (n + 2 < p.N) dst[2] = (uint16_t)w1;
+          if (n + 3 < p.N) dst[3] = (uint16_t)(w1 >> 16);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+constexpr int64_t kDirectBlocks = int64_t(1) << 22;  // workgroups stride over tiles past this many
+
+template <int MT, int NT, int W, bool GROUPED>
+hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
+  p.tiles_m = row_tiles;
+  p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
+  const int64_t n = p.tiles_m * p.tiles_n;
+  const dim3 grid((unsigned)(n < kDirectBlocks ? n : kDirectBlocks)), block(64 * W);
+  EpiArgs e;
+  switch (epi_kind(ep, e)) {
+    case 0: hipLaunchKernelGGL((k_int8_direct<MT, NT, W, 0, GROUPED>), grid, block, 0, stream, p, y, e); break;
+    case EPI_GELU:
+      hipLaunchKernelGGL((k_int8_direct<MT, NT, W, EPI_GELU, GROUPED>), grid, block, 0, stream, p, y, e);
+      break;
+    case EPI_QKV:
+      if constexpr (!GROUPED) {
+        hipLaunchKernelGGL((k_int8_direct<MT, NT, W, EPI_QKV, false>), grid, block, 0, stream, p, y, e);
+        break;
+      }
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const float* lam, int8_t* xq, float* xs,
+                             hipStream_t stream) {
+  const TilePlan none{};
+  return lam ? launch_quant_rows<true, false, false>(x, M, M, K, lam, nullptr, xq, xs, none, stream)
+             : launch_quant_rows<false, false, false>(x, M, M, K, nullptr, nullptr, xq, xs, none, stream);
+}
+
+hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,
+                            int64_t N, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
+  Int8Args p{};
+  p.x = xq;
+  p.w = w;
+  p.xs = xs;
+  p.ws = ws;
+  p.M = M;
+  p.N = N;
+  p.K = (int)K;
+  if (M <= 16) return launch_direct<1, 1, 8, false>(p, (M + 15) / 16, ep, y, stream);
+  return launch_direct<4, 4, 4, false>(p, (M + 63) / 64, ep, y, stream);
+}
+
+// Rows of a grouped product's tile.
+static int grouped_tile(int64_t R, int64_t E) { return R <= 16 * E ? 16 : 64; }
+
+int64_t grouped_row_tiles(int64_t R, int64_t E) {
+  const int tm = grouped_tile(R, E);
+  return R / tm + (E < R ? E : R);
+}
+
+hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, const int32_t* row_index,
+                                     const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
+                                     hipStream_t stream) {
+  TilePlan t;
+  t.offsets = offsets;
+  t.E = (int)E;
+  t.R = (int)R;
+  t.tm = grouped_tile(R, E);
+  t.cap = (int)grouped_row_tiles(R, E);
+  t.count = tiles;
+  t.tiles = reinterpret_cast<RowTile*>(tiles) + 1;
+  return row_index ? launch_quant_rows<false, true, true>(x, rows_x, R, K, nullptr, row_index, xq, xs, t, stream)
+                   : launch_quant_rows<false, true, false>(x, rows_x, R, K, nullptr, nullptr, xq, xs, t, stream);
+}
+
+hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t R,
+                                    int64_t K, int64_t N, int64_t E, const int32_t* tiles, const Epilogue& ep,
+                                    uint16_t* y, hipStream_t stream) {
+  Int8Args p{};
+  p.x = xq;
+  p.w = w;
+  p.xs = xs;
+  p.ws = ws;
+  p.M = R;
+  p.N = N;
+  p.K = (int)K;
+  p.count = tiles;
+  p.tiles = reinterpret_cast<const RowTile*>(tiles) + 1;
+  const int64_t cap = grouped_row_tiles(R, E);
+  if (grouped_tile(R, E) == 16) return launch_direct<1, 1, 8, true>(p, cap, ep, y, stream);
+  return launch_direct<4, 4, 4, true>(p, cap, ep, y, stream);
+}
+
+}  // namespace qpl

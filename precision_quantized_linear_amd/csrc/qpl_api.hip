@@ -43,7 +43,10 @@ int64_t nvfp4_slabs(int64_t K) { return (K + 127) / 128; }
 // (2K bytes each) the same way (K <= 2^21) and store their scales through a
 // descriptor below 2^31 bytes.
 constexpr int64_t kMaxKBytePitch = (int64_t(1) << 30) / 256;
+// INT8: 2^17 products of at most 127 * 128 stay below 2^31.
+constexpr int64_t kMaxKInt8 = int64_t(1) << 17;
 qpl_status check_gemm_k(qpl_scheme scheme, int64_t M, int64_t K, int64_t R) {
+  if (scheme == QPL_INT8) return K <= kMaxKInt8 ? QPL_OK : QPL_ERR_SHAPE;
   const int64_t pitch = scheme == QPL_NVFP4 ? K / 2 : K;
   if (pitch >= kMaxKBytePitch) return QPL_ERR_SHAPE;
   if (R > 0) {
@@ -80,7 +83,7 @@ size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int64_t rank_pad(int64_t R) { return (R + 31) / 32 * 32; }
 
-// Workspace layout.  fp8r: [xq: M*K bytes][xs: 4*M bytes].  nvfp4: [xq: M*K/2 packed
+// Workspace layout.  fp8r and INT8: [xq: M*K bytes][xs: 4*M bytes].  nvfp4: [xq: M*K/2 packed
 // E2M1 codes][xs: 8*M*S block scales slab-major [S, M, 8]], S = ceil(K/128), and, as
 // part 5, [wsl: 8*N*S] the weight's block scales in the same layout.  INT4:
 // [xq: M*K][w8: N*K] (code values as E4M3 bytes) and, as parts 5 and 6, the
@@ -95,7 +98,7 @@ struct Layout {
 Layout layout(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R) {
   Layout L;
   size_t parts[7] = {0, 0, 0, 0, 0, 0, 0};
-  if (scheme == QPL_FP8R) {
+  if (scheme == QPL_FP8R || scheme == QPL_INT8) {
     parts[0] = size_t(M) * size_t(K);
     parts[1] = size_t(4) * size_t(M);
   } else {
@@ -405,10 +408,10 @@ QPL_EXPORT const char* qpl_status_str(qpl_status status) {
 QPL_EXPORT float qpl_nvfp4_global_scale(float amax) { return amax / 2688.0f; }
 
 QPL_EXPORT size_t qlinear_workspace_bytes(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R) {
-  if (scheme != QPL_FP8R && scheme != QPL_NVFP4 && scheme != QPL_INT4) return 0;
+  if (scheme != QPL_FP8R && scheme != QPL_NVFP4 && scheme != QPL_INT4 && scheme != QPL_INT8) return 0;
   if (check_gemm_dims(M, K, N) != QPL_OK || R < 0 || R > kMaxRank) return 0;
   if (scheme == QPL_INT4 && K % 64 != 0) return 0;
-  if (scheme == QPL_FP8R && R != 0) return 0;
+  if ((scheme == QPL_FP8R || scheme == QPL_INT8) && R != 0) return 0;
   if (check_gemm_k(scheme, M, K, R) != QPL_OK) return 0;
   return layout(scheme, M, K, N, R).total;
 }
@@ -653,6 +656,228 @@ QPL_EXPORT qpl_status qlinear_int4_ex(const uint16_t* x, int64_t M, int64_t K, i
                                       const uint16_t* lora_up, int64_t R, const qpl_epilogue* epi, uint16_t* y,
                                       void* ws, size_t ws_bytes, void* stream) {
   return int4_linear(x, M, K, N, weight, weight_scale, smooth, lora_down, lora_up, R, epi, y, ws, ws_bytes, stream);
+}
+
+QPL_EXPORT qpl_status quant_act_int8(const uint16_t* x, int64_t M, int64_t K, const float* smooth, int8_t* x_q,
+                                     float* x_scale, void* stream) {
+  if (!x || !x_q || !x_scale) return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(x_q) || !aligned16(x_scale) || !aligned16(smooth)) return QPL_ERR_ALIGN;
+  qpl_status s = check_dims(M, K);
+  if (s != QPL_OK) return s;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_QUANT_INT8, st)(qpl::launch_quant_int8(x, M, K, smooth, x_q, x_scale, st)));
+}
+
+namespace {
+
+qpl_status int8_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* weight,
+                       const float* weight_scale, const float* smooth, const qpl_epilogue* epi, uint16_t* y, void* ws,
+                       size_t ws_bytes, void* stream) {
+  if (!x || !weight || !weight_scale || !ws) return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(weight_scale) || !aligned16(y) || !aligned16(ws) ||
+      !aligned16(smooth))
+    return QPL_ERR_ALIGN;
+  qpl_status s = check_gemm_dims(M, K, N);
+  if (s != QPL_OK) return s;
+  if ((s = check_gemm_k(QPL_INT8, M, K, 0)) != QPL_OK) return s;
+  qpl::Epilogue ep;
+  if ((s = epilogue_of(epi, M, N, y, ep)) != QPL_OK) return s;
+  const Layout L = layout(QPL_INT8, M, K, N, 0);
+  if (ws_bytes < L.total) return QPL_ERR_WORKSPACE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int8_t* xq = reinterpret_cast<int8_t*>(base + L.off[0]);
+  float* xs = reinterpret_cast<float*>(base + L.off[1]);
+  if ((s = launched(Timed(QPL_KERNEL_QUANT_INT8, st)(qpl::launch_quant_int8(x, M, K, smooth, xq, xs, st)))) != QPL_OK)
+    return s;
+  return launched(Timed(gemm_kind(ep, QPL_KERNEL_GEMM_INT8), st)(
+      qpl::launch_gemm_int8(xq, xs, weight, weight_scale, M, K, N, ep, y, st)));
+}
+
+// ---- experts ------------------------------------------------------------------
+constexpr int64_t kMaxExperts = 65536;
+constexpr int64_t kMaxTopk = 256;
+// rows and places are 32-bit, with room to round up to a tile
+constexpr int64_t kMaxPlaces = (int64_t(1) << 31) - (int64_t(1) << 16);
+
+qpl_status check_grouped(int64_t R, int64_t K, int64_t N, int64_t E) {
+  qpl_status s = check_gemm_dims(R, K, N);
+  if (s != QPL_OK) return s;
+  if (R >= kMaxPlaces || E < 1 || E > kMaxExperts) return QPL_ERR_SHAPE;
+  if (N > kMaxElems / K / E) return QPL_ERR_SHAPE;
+  return check_gemm_k(QPL_INT8, R, K, 0);
+}
+
+qpl_status check_choices(int64_t T, int64_t topk) {
+  if (T < 1 || topk < 1 || topk > kMaxTopk || T >= kMaxPlaces / topk) return QPL_ERR_SHAPE;
+  return QPL_OK;
+}
+
+// Workspace of a grouped product: [xq: R K][xs: 4 R][row tiles: 16 (1 + their bound)].
+struct GroupedLayout {
+  size_t xs = 0, tiles = 0, total = 0;
+};
+
+GroupedLayout grouped_layout(int64_t R, int64_t K, int64_t E) {
+  GroupedLayout L;
+  L.xs = round256(size_t(R) * size_t(K));
+  L.tiles = L.xs + round256(size_t(4) * size_t(R));
+  L.total = L.tiles + round256(size_t(16) * size_t(1 + qpl::grouped_row_tiles(R, E)));
+  return L;
+}
+
+// The two launches of a grouped product, arguments checked.
+qpl_status grouped_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, int64_t E, const int8_t* weight,
+                          const float* weight_scale, const int32_t* row_index, int64_t R, const int32_t* offsets,
+                          const qpl::Epilogue& ep, uint16_t* y, uint8_t* ws, hipStream_t st) {
+  const GroupedLayout L = grouped_layout(R, K, E);
+  int8_t* xq = reinterpret_cast<int8_t*>(ws);
+  float* xs = reinterpret_cast<float*>(ws + L.xs);
+  int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+  const qpl_status s = launched(Timed(QPL_KERNEL_QUANT_INT8, st)(
+      qpl::launch_quant_int8_grouped(x, M, R, K, row_index, offsets, E, xq, xs, tiles, st)));
+  if (s != QPL_OK) return s;
+  return launched(Timed(QPL_KERNEL_GEMM_INT8_GROUPED, st)(
+      qpl::launch_gemm_int8_grouped(xq, xs, weight, weight_scale, R, K, N, E, tiles, ep, y, st)));
+}
+
+// Workspace of the MLP of experts: the arrays of the plan, h, the experts' outputs, and the
+// workspace of either product (they run one after the other).
+struct MoeLayout {
+  size_t row_index = 0, slot = 0, offsets = 0, h = 0, out = 0, ws = 0, total = 0;
+};
+
+MoeLayout moe_layout(int64_t R, int64_t K, int64_t H, int64_t N, int64_t E) {
+  MoeLayout L;
+  const size_t ints = round256(size_t(4) * size_t(R));
+  L.slot = L.row_index + ints;
+  L.offsets = L.slot + ints;
+  L.h = L.offsets + round256(size_t(4) * size_t(E + 1));
+  L.out = L.h + round256(size_t(2) * size_t(R) * size_t(H));
+  L.ws = L.out + round256(size_t(2) * size_t(R) * size_t(N));
+  const size_t w1 = grouped_layout(R, K, E).total, w2 = grouped_layout(R, H, E).total;
+  L.total = L.ws + (w1 > w2 ? w1 : w2);
+  return L;
+}
+
+qpl_status check_moe(int64_t T, int64_t topk, int64_t K, int64_t H, int64_t N, int64_t E) {
+  qpl_status s = check_choices(T, topk);
+  if (s != QPL_OK) return s;
+  if ((s = check_dims(T, K)) != QPL_OK) return s;
+  if ((s = check_grouped(T * topk, K, H, E)) != QPL_OK) return s;
+  return check_grouped(T * topk, H, N, E);
+}
+
+}  // namespace
+
+QPL_EXPORT qpl_status qlinear_int8(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* weight,
+                                   const float* weight_scale, const float* smooth, uint16_t* y, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  return int8_linear(x, M, K, N, weight, weight_scale, smooth, nullptr, y, ws, ws_bytes, stream);
+}
+
+QPL_EXPORT qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* weight,
+                                      const float* weight_scale, const float* smooth, const qpl_epilogue* epi,
+                                      uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  return int8_linear(x, M, K, N, weight, weight_scale, smooth, epi, y, ws, ws_bytes, stream);
+}
+
+QPL_EXPORT qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E, int32_t* row_index,
+                                  int32_t* slot, int32_t* offsets, void* stream) {
+  if (!expert_ids || !row_index || !slot || !offsets) return QPL_ERR_NULL;
+  if (!aligned16(expert_ids) || !aligned16(row_index) || !aligned16(slot) || !aligned16(offsets)) return QPL_ERR_ALIGN;
+  qpl_status s = check_choices(T, topk);
+  if (s != QPL_OK) return s;
+  if (E < 1 || E > kMaxExperts) return QPL_ERR_SHAPE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(
+      qpl::launch_expert_plan(expert_ids, T * topk, topk, E, row_index, slot, offsets, st)));
+}
+
+QPL_EXPORT size_t qlinear_grouped_int8_workspace_bytes(int64_t R, int64_t K, int64_t N, int64_t E) {
+  if (check_grouped(R, K, N, E) != QPL_OK) return 0;
+  return grouped_layout(R, K, E).total;
+}
+
+QPL_EXPORT qpl_status qlinear_grouped_int8(const uint16_t* x, int64_t M, int64_t K, int64_t N, int64_t E,
+                                           const int8_t* weight, const float* weight_scale, const int32_t* row_index,
+                                           int64_t R, const int32_t* offsets, qpl_act act, uint16_t* y, void* ws,
+                                           size_t ws_bytes, void* stream) {
+  if (!x || !weight || !weight_scale || !offsets || !y || !ws) return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(weight_scale) || !aligned16(row_index) ||
+      !aligned16(offsets) || !aligned16(y) || !aligned16(ws))
+    return QPL_ERR_ALIGN;
+  qpl_status s = check_dims(M, K);
+  if (s != QPL_OK) return s;
+  if ((s = check_grouped(R, K, N, E)) != QPL_OK) return s;
+  if (M >= kMaxPlaces || (!row_index && R > M)) return QPL_ERR_SHAPE;
+  if (act != QPL_ACT_NONE && act != QPL_ACT_GELU_TANH) return QPL_ERR_ARG;
+  if (ws_bytes < grouped_layout(R, K, E).total) return QPL_ERR_WORKSPACE;
+  if ((s = check_device()) != QPL_OK) return s;
+  qpl::Epilogue ep;
+  ep.gelu = act == QPL_ACT_GELU_TANH;
+  return grouped_linear(x, M, K, N, E, weight, weight_scale, row_index, R, offsets, ep, y, static_cast<uint8_t*>(ws),
+                        static_cast<hipStream_t>(stream));
+}
+
+QPL_EXPORT qpl_status expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot,
+                                     const float* weights, int64_t T, int64_t topk, uint16_t* out, void* stream) {
+  if (!y || !slot || !weights || !out) return QPL_ERR_NULL;
+  if (!aligned16(y) || !aligned16(slot) || !aligned16(weights) || !aligned16(out)) return QPL_ERR_ALIGN;
+  qpl_status s = check_choices(T, topk);
+  if (s != QPL_OK) return s;
+  if (R < 1 || R >= kMaxPlaces || N < 1 || N >= kMaxDim || R > kMaxElems / N || T > kMaxElems / N)
+    return QPL_ERR_SHAPE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_EXPERT_COMBINE, st)(
+      qpl::launch_expert_combine(y, R, N, slot, weights, T, topk, out, st)));
+}
+
+QPL_EXPORT size_t qlinear_moe_int8_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t H, int64_t N,
+                                                   int64_t E) {
+  if (check_moe(T, topk, K, H, N, E) != QPL_OK) return 0;
+  return moe_layout(T * topk, K, H, N, E).total;
+}
+
+QPL_EXPORT qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, int64_t N, int64_t E,
+                                       int64_t topk, const int32_t* expert_ids, const float* expert_weights,
+                                       const int8_t* fc1_weight, const float* fc1_scale, const int8_t* fc2_weight,
+                                       const float* fc2_scale, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !expert_ids || !expert_weights || !fc1_weight || !fc1_scale || !fc2_weight || !fc2_scale || !y || !ws)
+    return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(expert_ids) || !aligned16(expert_weights) || !aligned16(fc1_weight) ||
+      !aligned16(fc1_scale) || !aligned16(fc2_weight) || !aligned16(fc2_scale) || !aligned16(y) || !aligned16(ws))
+    return QPL_ERR_ALIGN;
+  qpl_status s = check_moe(T, topk, K, H, N, E);
+  if (s != QPL_OK) return s;
+  const int64_t R = T * topk;
+  const MoeLayout L = moe_layout(R, K, H, N, E);
+  if (ws_bytes < L.total) return QPL_ERR_WORKSPACE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int32_t* row_index = reinterpret_cast<int32_t*>(base + L.row_index);
+  int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot);
+  int32_t* offsets = reinterpret_cast<int32_t*>(base + L.offsets);
+  uint16_t* h = reinterpret_cast<uint16_t*>(base + L.h);
+  uint16_t* out = reinterpret_cast<uint16_t*>(base + L.out);
+  if ((s = launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(
+           qpl::launch_expert_plan(expert_ids, R, topk, E, row_index, slot, offsets, st)))) != QPL_OK)
+    return s;
+  qpl::Epilogue gelu, plain;
+  gelu.gelu = true;
+  if ((s = grouped_linear(x, T, K, H, E, fc1_weight, fc1_scale, row_index, R, offsets, gelu, h, base + L.ws, st)) !=
+      QPL_OK)
+    return s;
+  if ((s = grouped_linear(h, R, H, N, E, fc2_weight, fc2_scale, nullptr, R, offsets, plain, out, base + L.ws, st)) !=
+      QPL_OK)
+    return s;
+  return launched(Timed(QPL_KERNEL_EXPERT_COMBINE, st)(
+      qpl::launch_expert_combine(out, R, N, slot, expert_weights, T, topk, y, st)));
 }
 
 QPL_EXPORT qpl_status dequant_weight(qpl_scheme scheme, const uint8_t* weight, const void* weight_scale,

@@ -116,4 +116,27 @@ hipError_t launch_gemm_int4(const uint8_t* x8, const float* xs, const uint8_t* w
 hipError_t launch_lowrank_prep(const uint16_t* l1, const uint16_t* l2, int64_t K, int64_t N, int64_t R, int64_t kl,
                                uint16_t* l1t, uint16_t* l2t, hipStream_t stream);
 
+
+// 8-bit integer linears.  Quantizer: codes [M, K] and scales [M] of x (divided by lam
+// [K] first when not nullptr).  GEMM: y = bf16(act((xq w^T) xs ws)).
+hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const float* lam, int8_t* xq, float* xs,
+                             hipStream_t stream);
+hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,
+                            int64_t N, const Epilogue& ep, uint16_t* y, hipStream_t stream);
+// Grouped by expert: the quantizer writes the R product rows (row i from
+// x[row_index[i]], or x[i] without row_index) and, from offsets [E + 1], the list of
+// row tiles that the product walks: 16 (1 + grouped_row_tiles(R, E)) bytes.
+int64_t grouped_row_tiles(int64_t R, int64_t E);
+hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, const int32_t* row_index,
+                                     const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
+                                     hipStream_t stream);
+hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t R,
+                                    int64_t K, int64_t N, int64_t E, const int32_t* tiles, const Epilogue& ep,
+                                    uint16_t* y, hipStream_t stream);
+// Routing: choices ids [n] sorted by expert, and the experts' rows summed per token.
+hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
+                              int32_t* slot, int32_t* offsets, hipStream_t stream);
+hipError_t launch_expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot, const float* weights,
+                                 int64_t T, int64_t topk, uint16_t* out, hipStream_t stream);
+
 }  // namespace qpl
