@@ -363,6 +363,257 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// The product through LDS, for enough rows to reuse the weight.  A workgroup of four
+// wavefronts (2 x 2) owns 64 NJM rows of x by 64 NI columns; a wavefront
+// owns 32 NJ x 32 NI (V_MFMA_I32_32X32X32_I8, int32 accumulators).  Workgroups are
+// persistent; K is walked in 128-byte pieces of both operands, two stages of them in
+// LDS, filled by buffer_load_dwordx4 ... lds: piece P + 1's loads are issued between
+// piece P's MFMAs, so they have the whole piece to arrive.  The pieces of all of a
+// workgroup's tiles form one stream.
+//
+// A tile with at most half (a quarter) of its rows present, an expert's last one for
+// instance, runs with NJ = NJM / 2 (/ 4), so that its MFMAs are mostly on rows that
+// exist.  Chunk c of a 128-byte stage row r sits at chunk c ^ (r % 8): the 16-byte
+// operand reads of a wavefront fall on distinct banks.
+//
+// Top of a piece: wait for its loads (issued during the piece before; only the output
+// stores issued after them may be in flight), then a barrier: the piece is in LDS for
+// every wavefront, and every wavefront is done with the piece before, whose stage the next
+// loads fill.
+// ---------------------------------------------------------------------------
+struct StagedArgs {
+  Int8Args g;
+  int tiles_m, tiles_n;  // tiles_m unused when grouped
+  int nwg;
+};
+
+// Tile (row tile, column tile) at position s of the walk: groups of four row tiles,
+// column by column, so that workgroups of one XCD share operand rows in its L2.
+__device__ __forceinline__ void walk(int64_t s, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int64_t per_group = (int64_t)GROUP_M * tiles_n;
+  const int g = (int)(s / per_group);
+  const int gm = min(tiles_m - g * GROUP_M, GROUP_M);
+  const int r = (int)(s - g * per_group);
+  tm = g * GROUP_M + r % gm;
+  tn = r / gm;
+}
+
+template <int NI, int NJM, int EPI, bool GROUPED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NI * NJM == 16 ? 1 : 2, NI * NJM == 16 ? 1 : 2)))
+void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
+  constexpr int XR = 64 * NJM, WR = 64 * NI;     // rows of x and of W per stage
+  constexpr int STAGE = (XR + WR) * PR_ROW;
+  constexpr int XL = 2 * NJM, LOADS = XL + 2 * NI;  // loads per wavefront per piece: x, all
+  constexpr int SBUF = (XR + WR) * 4;            // output scales of a tile
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * SBUF + 256];
+  const Int8Args& p = a.g;
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wv >> 1, wn = wv & 1;
+  const int h = lane >> 5, r32 = lane & 31;
+  const int b = blockIdx.x;
+  const uint32_t lbase = lds_address(lds), sbase = lds_address(lsc);
+  const int tiles_m = GROUPED ? __builtin_amdgcn_readfirstlane(p.count[0]) : a.tiles_m;
+  const int64_t ntiles = (int64_t)tiles_m * a.tiles_n;
+  const int np = (p.K + PR_ROW - 1) / PR_ROW;
+
+  struct Tile {
+    int64_t m0, n0;
+    int rows, e;
+  };
+  auto position = [&](int i) {
+    return (a.nwg & 7) == 0 ? (int64_t)i * a.nwg + (b & 7) * (a.nwg >> 3) + (b >> 3) : (int64_t)i * a.nwg + b;
+  };
+  auto tile = [&](int i) {
+    Tile t;
+    int tm, tn;
+    walk(position(i), tiles_m, a.tiles_n, tm, tn);
+    t.n0 = (int64_t)tn * WR;
+    if constexpr (GROUPED) {
+      const RowTile rt = p.tiles[tm];
+      t.m0 = rt.m0;
+      t.rows = rt.m1 - rt.m0;
+      t.e = rt.e;
+    } else {
+      t.m0 = (int64_t)tm * XR;
+      t.rows = (int)(p.M - t.m0 < XR ? p.M - t.m0 : XR);
+      t.e = 0;
+    }
+    return t;
+  };
+  int nt = 0;
+  while (position(nt) < ntiles) ++nt;
+
+  // load q of an operand: rows (rows / 4) wv + 8 q .. + 7; lane l fills row + l / 8, stage
+  // chunk l % 8, with the row's chunk (l % 8) ^ (l / 8)
+  const int lc = (lane & 7) ^ (lane >> 3);
+  const uint32_t vx = (uint32_t)((XR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
+  const uint32_t vw = (uint32_t)((WR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
+
+  struct Piece {
+    u32x4 dx, dw, ds;
+    int koff, stage, par;
+    bool first, valid;
+  };
+  int s_i = 0, s_k = 0, s_stage = 0;
+  Tile s_t{0, 0, 0, 0};
+  if (nt > 0) s_t = tile(0);
+  auto next_piece = [&]() {
+    Piece r;
+    r.valid = s_i < nt;
+    r.stage = s_stage;
+    r.first = s_k == 0;
+    r.par = s_i & 1;
+    r.koff = s_k * PR_ROW;
+    const int rn = (int)(p.N - s_t.n0 < WR ? p.N - s_t.n0 : WR);
+    r.dx = make_desc(p.x + s_t.m0 * p.K, (int64_t)s_t.rows * p.K);
+    r.dw = make_desc(p.w + ((int64_t)s_t.e * p.N + s_t.n0) * p.K, (int64_t)rn * p.K);
+    const bool row = wv < 2;
+    r.ds = make_desc(row ? p.xs + s_t.m0 : p.ws + (int64_t)s_t.e * p.N + s_t.n0, (row ? s_t.rows : rn) * 4);
+    s_stage ^= 1;
+    if (++s_k == np) {
+      s_k = 0;
+      ++s_i;
+      if (s_i < nt) s_t = tile(s_i);
+    }
+    return r;
+  };
+  auto issue = [&](const Piece& s, int d) {
+    const bool in = s.valid && s.koff + 16 * lc < p.K;
+    const int q = d < XL ? d : d - XL;
+    const uint32_t dst = lbase + s.stage * STAGE + (d < XL ? XR / 4 * wv + 8 * q : XR + WR / 4 * wv + 8 * q) * PR_ROW;
+    const uint32_t vo = in ? (d < XL ? vx : vw) + (uint32_t)(8 * q * p.K) : kOutOfRange;
+    dma16(dst, vo, d < XL ? s.dx : s.dw, s.koff);
+  };
+  // the tile's output scales, 64 per load: wavefronts 0 and 1 those of x, 2 and 3 those of W; every
+  // piece issues two loads per wavefront (out of range, into a spare area, unless it starts a tile)
+  auto issue_scales = [&](const Piece& s, int hh) {
+    const int c = 2 * (wv & 1) + hh;
+    const bool real = s.valid && s.first && c < (wv < 2 ? NJM : NI);
+    const uint32_t dst = sbase + (real ? s.par * SBUF + (wv < 2 ? 0 : XR * 4) + c * 256 : 2 * SBUF);
+    dma4(dst, real ? (uint32_t)((c * 64 + lane) * 4) : kOutOfRange, s.ds, 0);
+  };
+
+  struct Frag {
+    i32x4 lo, hi;
+  };
+  auto frag = [&](const uint8_t* st, int row, int u) {
+    return Frag{*reinterpret_cast<const i32x4*>(st + proff(row, 4 * u + 2 * h)),
+                *reinterpret_cast<const i32x4*>(st + proff(row, 4 * u + 2 * h + 1))};
+  };
+  auto mma = [&](const Frag& w, const Frag& x, i32x16 c) {
+    c = __builtin_amdgcn_mfma_i32_32x32x32_i8(w.lo, x.lo, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(w.hi, x.hi, c, 0, 0, 0);
+  };
+  Frag fw[NI], fx[NJM];
+
+  {
+    const Piece s = next_piece();
+#pragma unroll
+    for (int d = 0; d < LOADS; ++d) issue(s, d);
+    issue_scales(s, 0);
+    issue_scales(s, 1);
+  }
+  int stores = 0;  // output stores in flight behind the current piece's loads
+  int cur = 0;
+  auto piece = [&](auto& acc, auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    constexpr int T = NI * NJ;  // tiles of 32 x 32 per wavefront
+    if (stores == 2 * NI * NJM) {
+      QPL_WAIT_VMCNT(2 * NI * NJM);
+    } else {
+      QPL_WAIT_VMCNT(0);
+    }
+    __builtin_amdgcn_s_barrier();
+    stores = 0;
+    const Piece s = next_piece();
+    const uint8_t* cs = lds + cur * STAGE;
+    const uint8_t* cw = cs + XR * PR_ROW;
+    cur ^= 1;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) fw[i] = frag(cw, wn * 32 * NI + i * 32 + r32, 0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) fx[j] = frag(cs, wm * 32 * NJ + j * 32 + r32, 0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        acc[i][j] = mma(fw[i], fx[j], acc[i][j]);
+        const int k = NJ * i + j;
+        if (i == NI - 1) fx[j] = frag(cs, wm * 32 * NJ + j * 32 + r32, 1);
+        if (j == NJ - 1) fw[i] = frag(cw, wn * 32 * NI + i * 32 + r32, 1);
+#pragma unroll
+        for (int d = 0; d < LOADS; ++d)
+          if (k == (d * T) / LOADS) issue(s, d);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    // x tile rows outermost: the fragments that the first half freed first come first
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        acc[i][j] = mma(fw[i], fx[j], acc[i][j]);
+        if (i == 0 && j == 0) {
+          issue_scales(s, 0);
+          issue_scales(s, 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+  auto run_tile = [&](const Tile& t, int i, auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    i32x16 acc[NI][NJ];
+#pragma unroll
+    for (int x = 0; x < NI; ++x)
+#pragma unroll
+      for (int y = 0; y < NJ; ++y) acc[x][y] = i32x16{};
+    for (int k = 0; k < np; ++k) piece(acc, nj);
+    const float* ls = reinterpret_cast<const float*>(lsc + (i & 1) * SBUF);
+    // the stores of a tile of fewer rows are waited for, so that `stores` has one value
+    stores = __builtin_amdgcn_readfirstlane(store_tile<NJ, NI, EPI>(
+        acc, wm, wn, lane, t.m0, t.n0, t.m0 + t.rows, p.N, Y, [&](int r) { return ls[r]; },
+        [&](int c) { return *reinterpret_cast<const f32x4*>(&ls[XR + c]); }, e));
+  };
+  for (int i = 0; i < nt; ++i) {
+    const Tile t = tile(i);
+    if (t.rows > XR / 2) {
+      run_tile(t, i, std::integral_constant<int, NJM>{});
+    } else if (NJM < 4 || t.rows > XR / 4) {
+      if constexpr (NJM >= 2) run_tile(t, i, std::integral_constant<int, NJM / 2>{});
+    } else {
+      if constexpr (NJM >= 4) run_tile(t, i, std::integral_constant<int, NJM / 4>{});
+    }
+  }
+  QPL_WAIT_VMCNT(0);
+  QPL_WAIT_LGKM0();
+}
+
+template <int NI, int NJM, bool GROUPED>
+hipError_t launch_staged(const Int8Args& g, int64_t row_tiles, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
+  StagedArgs a;
+  a.g = g;
+  a.tiles_m = (int)row_tiles;
+  a.tiles_n = (int)((g.N + 64 * NI - 1) / (64 * NI));
+  // one workgroup of 256 x 256 per CU, two of the smaller tiles
+  const int64_t n = row_tiles * a.tiles_n, most = NI * NJM == 16 ? 256 : 512;
+  a.nwg = (int)(n < most ? n : most);
+  const dim3 grid((unsigned)a.nwg), block(256);
+  EpiArgs e;
+  switch (epi_kind(ep, e)) {
+    case 0: hipLaunchKernelGGL((k_int8_staged<NI, NJM, 0, GROUPED>), grid, block, 0, stream, a, y, e); break;
+    case EPI_GELU: hipLaunchKernelGGL((k_int8_staged<NI, NJM, EPI_GELU, GROUPED>), grid, block, 0, stream, a, y, e); break;
+    case EPI_QKV:
+      if constexpr (!GROUPED) {
+        hipLaunchKernelGGL((k_int8_staged<NI, NJM, EPI_QKV, false>), grid, block, 0, stream, a, y, e);
+        break;
+      }
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const float* lam, int8_t* xq, float* xs,
@@ -383,11 +634,13 @@ hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, 
   p.N = N;
   p.K = (int)K;
   if (M <= 16) return launch_direct<1, 1, 8, false>(p, (M + 15) / 16, ep, y, stream);
-  return launch_direct<4, 4, 4, false>(p, (M + 63) / 64, ep, y, stream);
+  if (M <= 256) return launch_direct<4, 4, 4, false>(p, (M + 63) / 64, ep, y, stream);
+  if (((M + 255) / 256) * ((N + 255) / 256) >= 192) return launch_staged<4, 4, false>(p, (M + 255) / 256, ep, y, stream);
+  return launch_staged<2, 2, false>(p, (M + 127) / 128, ep, y, stream);
 }
 
 // Rows of a grouped product's tile.
-static int grouped_tile(int64_t R, int64_t E) { return R <= 16 * E ? 16 : 64; }
+static int grouped_tile(int64_t R, int64_t E) { return R <= 16 * E ? 16 : R <= 32 * E ? 64 : R <= 128 * E ? 128 : 256; }
 
 int64_t grouped_row_tiles(int64_t R, int64_t E) {
   const int tm = grouped_tile(R, E);
@@ -424,7 +677,9 @@ hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int
   p.tiles = reinterpret_cast<const RowTile*>(tiles) + 1;
   const int64_t cap = grouped_row_tiles(R, E);
   if (grouped_tile(R, E) == 16) return launch_direct<1, 1, 8, true>(p, cap, ep, y, stream);
-  return launch_direct<4, 4, 4, true>(p, cap, ep, y, stream);
+  if (grouped_tile(R, E) == 64) return launch_direct<4, 4, 4, true>(p, cap, ep, y, stream);
+  if (grouped_tile(R, E) == 128) return launch_staged<2, 2, true>(p, cap, ep, y, stream);
+  return launch_staged<4, 4, true>(p, cap, ep, y, stream);
 }
 
 }  // namespace qpl
