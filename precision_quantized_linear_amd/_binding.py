@@ -349,32 +349,24 @@ def qlinear_mlp_nvfp4(x, fc1, fc2, y=None, workspace=None, stream=None):
     return y
 
 
-def _on_current(t, name):
-    """The calls run on the current device: a tensor of another one would be read across devices."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _addr(t, dtype, shape, dev, name):
+    """Address of t, checked: contiguous, of this type and shape, on GPU dev (None: 0)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on the current GPU ({dev}), got "
+                         f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} device={t.device}")
+    return t.data_ptr()
+
+
+def _current(t, dims, name):
+    """The current GPU, which has to be t's: a call runs on it and reads all its tensors there."""
+    if t.dim() != dims:
+        raise ValueError(f"{name}: expected {dims} dimensions, got {tuple(t.shape)}")
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"{name}: expected a tensor on the current GPU, got {t.device}")
-
-
-def _out(t, shape, dtype, device, stream, name):
-    """t checked, or a new tensor that belongs to the stream the call runs on."""
-    if t is not None:
-        _expect(t, dtype, shape, name)
-        _on_current(t, name)
-        return t
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _scratch(ws, need, device, stream):
-    """(workspace, its bytes): the caller's, or a new one (need 0: sizes that the call refuses)."""
-    if ws is None:
-        ws = _out(None, (max(need, 1),), torch.uint8, device, stream, "workspace")
-    elif not ws.is_contiguous():
-        raise ValueError("workspace: expected a contiguous tensor")
-    _on_current(ws, "workspace")
-    return ws, ws.numel() * ws.element_size()
+    return dev
 
 
 def _dims(t, n, name):
@@ -383,46 +375,75 @@ def _dims(t, n, name):
     return t.shape
 
 
-def _inputs(**tensors):
-    """name=(tensor or None, dtype, shape): each contiguous on the current GPU."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is not None:
-            _expect(t, dtype, shape, name)
-            _on_current(t, name)
+def _queue(stream, dev):
+    """The hipStream_t of a call on GPU dev."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected a stream of the current GPU ({dev}), got one of {stream.device_index}")
+    return stream.cuda_stream
+
+
+def _new(shape, dtype, like, stream):
+    """A tensor on like's GPU that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scratch(ws, need, like, dev, stream):
+    """(workspace, its bytes): the caller's, or a new one (need 0: sizes that the call refuses)."""
+    if ws is None:
+        return _new((max(need, 1),), torch.uint8, like, stream), max(need, 1)
+    if not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError(f"workspace: expected a contiguous tensor on the current GPU ({dev}), got {ws.device}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _act_code(act):
+    if act not in _ACTS:
+        raise ValueError(f"act: expected one of {sorted(k for k in _ACTS if k)}, got {act!r}")
+    return _ACTS[act]
 
 
 def quant_act_int8(x, smooth=None, x_q=None, x_scale=None, stream=None):
     """bf16 [M,K] -> (int8 codes [M,K], fp32 row scales [M]); with smooth (float32 [K]) the
     quantized activation is bf16(x / smooth).  The same call quantizes a weight [N,K]."""
-    M, K = _dims(x, 2, "x")
-    _inputs(x=(x, torch.bfloat16, (M, K)), smooth=(smooth, torch.float32, (K,)))
-    x_q = _out(x_q, (M, K), torch.int8, x.device, stream, "x_q")
-    x_scale = _out(x_scale, (M,), torch.float32, x.device, stream, "x_scale")
-    _check("quant_act_int8", load().quant_act_int8(_ptr(x), M, K, _ptr(smooth), _ptr(x_q), _ptr(x_scale),
-                                                    _stream(stream)))
+    dev = _current(x, 2, "x")
+    M, K = x.shape
+    x_q = _new((M, K), torch.int8, x, stream) if x_q is None else x_q
+    x_scale = _new((M,), torch.float32, x, stream) if x_scale is None else x_scale
+    _check("quant_act_int8", load().quant_act_int8(
+        _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, _addr(smooth, torch.float32, (K,), dev, "smooth"),
+        _addr(x_q, torch.int8, (M, K), dev, "x_q"), _addr(x_scale, torch.float32, (M,), dev, "x_scale"),
+        _queue(stream, dev)))
     return x_q, x_scale
 
 
 def qlinear_int8(x, weight, weight_scale, y=None, workspace=None, stream=None, smooth=None, act=None, qkv=None):
     """y[M,N] bf16 = 8-bit integer linear of bf16 x [M,K] with int8 weight [N,K] and fp32
     weight_scale [N]; smooth, act and qkv as in qlinear_int4."""
-    M, K = _dims(x, 2, "x")
     N = _dims(weight, 2, "weight")[0]
-    _inputs(x=(x, torch.bfloat16, (M, K)), weight=(weight, torch.int8, (N, K)),
-            weight_scale=(weight_scale, torch.float32, (N,)), smooth=(smooth, torch.float32, (K,)))
-    if qkv is not None:
-        for t, name in zip(qkv[:3], ("q", "k", "v")):
-            _dims(t, 3, name)
-            _on_current(t, name)
-    elif act in _ACTS:
-        y = _out(y, (M, N), torch.bfloat16, x.device, stream, "y")
-    e, y, out = _epilogue(act, qkv, M, N, y, x.device)
-    ws, nbytes = _scratch(workspace, qlinear_workspace_bytes(QPL_INT8, M, K, N), x.device, stream)
-    args = (_ptr(x), M, K, N, _ptr(weight), _ptr(weight_scale), _ptr(smooth))
-    if e is None:
-        _check("qlinear_int8", load().qlinear_int8(*args, _ptr(y), _ptr(ws), nbytes, _stream(stream)))
+    dev = _current(x, 2, "x")
+    M, K = x.shape
+    args = (_addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, N, _addr(weight, torch.int8, (N, K), dev, "weight"),
+            _addr(weight_scale, torch.float32, (N,), dev, "weight_scale"),
+            _addr(smooth, torch.float32, (K,), dev, "smooth"))
+    act_code = _act_code(act)
+    ya = 0
+    if qkv is None:
+        y = _new((M, N), torch.bfloat16, x, stream) if y is None else y
+        ya = _addr(y, torch.bfloat16, (M, N), dev, "y")
     else:
-        _check("qlinear_int8_ex", load().qlinear_int8_ex(*args, _ref(e), _ptr(y), _ptr(ws), nbytes, _stream(stream)))
+        for t, name in zip(qkv[:3], ("q", "k", "v")):
+            _addr(t, torch.bfloat16, _dims(qkv[0], 3, "q"), dev, name)
+    ws, nbytes = _scratch(workspace, qlinear_workspace_bytes(QPL_INT8, M, K, N), x, dev, stream)
+    if act_code == QPL_ACT_NONE and qkv is None:
+        _check("qlinear_int8", load().qlinear_int8(*args, ya, ws.data_ptr(), nbytes, _queue(stream, dev)))
+        return y
+    e, _, out = _epilogue(act, qkv, M, N, y, x.device)
+    _check("qlinear_int8_ex", load().qlinear_int8_ex(*args, _ref(e), ya, ws.data_ptr(), nbytes, _queue(stream, dev)))
     return out
 
 
@@ -431,16 +452,18 @@ def expert_plan(expert_ids, num_experts, row_index=None, slot=None, offsets=None
     each place; slot int32 [T, topk]: the place of each choice; offsets int32 [num_experts + 1]:
     the experts' first places).  An id outside [0, num_experts) gets slot -1; row_index is -1
     behind the last place."""
-    T, topk = _dims(expert_ids, 2, "expert_ids")
-    _inputs(expert_ids=(expert_ids, torch.int32, (T, topk)))
-    num_experts = int(num_experts)
-    if num_experts < 1:
-        raise ValueError(f"num_experts: expected at least 1, got {num_experts}")
-    row_index = _out(row_index, (T * topk,), torch.int32, expert_ids.device, stream, "row_index")
-    slot = _out(slot, (T, topk), torch.int32, expert_ids.device, stream, "slot")
-    offsets = _out(offsets, (num_experts + 1,), torch.int32, expert_ids.device, stream, "offsets")
-    _check("expert_plan", load().expert_plan(_ptr(expert_ids), T, topk, num_experts, _ptr(row_index), _ptr(slot),
-                                             _ptr(offsets), _stream(stream)))
+    dev = _current(expert_ids, 2, "expert_ids")
+    T, topk = expert_ids.shape
+    E = int(num_experts)
+    if E < 1:
+        raise ValueError(f"num_experts: expected at least 1, got {E}")
+    row_index = _new((T * topk,), torch.int32, expert_ids, stream) if row_index is None else row_index
+    slot = _new((T, topk), torch.int32, expert_ids, stream) if slot is None else slot
+    offsets = _new((E + 1,), torch.int32, expert_ids, stream) if offsets is None else offsets
+    _check("expert_plan", load().expert_plan(
+        _addr(expert_ids, torch.int32, (T, topk), dev, "expert_ids"), T, topk, E,
+        _addr(row_index, torch.int32, (T * topk,), dev, "row_index"), _addr(slot, torch.int32, (T, topk), dev, "slot"),
+        _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), _queue(stream, dev)))
     return row_index, slot, offsets
 
 
@@ -454,32 +477,33 @@ def qlinear_grouped_int8(x, weight, weight_scale, offsets, row_index=None, y=Non
     x[row_index[i]] (bf16 [M,K]; x[i] without row_index, R = M) with expert e's int8 weight
     [E,N,K] and fp32 weight_scale [E,N].  offsets int32 [E + 1] and row_index int32 [R] stay on
     the GPU.  Rows of y in no expert's range are not written (a new y holds anything there)."""
-    M, K = _dims(x, 2, "x")
-    E, N = _dims(weight, 3, "weight")[:2]
+    E, N, _ = _dims(weight, 3, "weight")
+    dev = _current(x, 2, "x")
+    M, K = x.shape
     R = M if row_index is None else _dims(row_index, 1, "row_index")[0]
-    _inputs(x=(x, torch.bfloat16, (M, K)), weight=(weight, torch.int8, (E, N, K)),
-            weight_scale=(weight_scale, torch.float32, (E, N)), offsets=(offsets, torch.int32, (E + 1,)),
-            row_index=(row_index, torch.int32, (R,)))
-    if act not in _ACTS:
-        raise ValueError(f"act: expected one of {sorted(k for k in _ACTS if k)}, got {act!r}")
-    y = _out(y, (R, N), torch.bfloat16, x.device, stream, "y")
-    ws, nbytes = _scratch(workspace, qlinear_grouped_int8_workspace_bytes(R, K, N, E), x.device, stream)
+    act_code = _act_code(act)
+    y = _new((R, N), torch.bfloat16, x, stream) if y is None else y
+    ws, nbytes = _scratch(workspace, qlinear_grouped_int8_workspace_bytes(R, K, N, E), x, dev, stream)
     _check("qlinear_grouped_int8", load().qlinear_grouped_int8(
-        _ptr(x), M, K, N, E, _ptr(weight), _ptr(weight_scale), _ptr(row_index), R, _ptr(offsets), _ACTS[act], _ptr(y),
-        _ptr(ws), nbytes, _stream(stream)))
+        _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, N, E, _addr(weight, torch.int8, (E, N, K), dev, "weight"),
+        _addr(weight_scale, torch.float32, (E, N), dev, "weight_scale"),
+        _addr(row_index, torch.int32, (R,), dev, "row_index"), R,
+        _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), act_code, _addr(y, torch.bfloat16, (R, N), dev, "y"),
+        ws.data_ptr(), nbytes, _queue(stream, dev)))
     return y
 
 
 def expert_combine(y, slot, weights, out=None, stream=None):
     """out[t] bf16 [T,N] = sum_j weights[t,j] y[slot[t,j]] of bf16 y [R,N], int32 slot [T,topk] and
     fp32 weights [T,topk]; a slot outside [0, R) adds nothing."""
-    R, N = _dims(y, 2, "y")
     T, topk = _dims(slot, 2, "slot")
-    _inputs(y=(y, torch.bfloat16, (R, N)), slot=(slot, torch.int32, (T, topk)),
-            weights=(weights, torch.float32, (T, topk)))
-    out = _out(out, (T, N), torch.bfloat16, y.device, stream, "out")
-    _check("expert_combine", load().expert_combine(_ptr(y), R, N, _ptr(slot), _ptr(weights), T, topk, _ptr(out),
-                                                   _stream(stream)))
+    dev = _current(y, 2, "y")
+    R, N = y.shape
+    out = _new((T, N), torch.bfloat16, y, stream) if out is None else out
+    _check("expert_combine", load().expert_combine(
+        _addr(y, torch.bfloat16, (R, N), dev, "y"), R, N, _addr(slot, torch.int32, (T, topk), dev, "slot"),
+        _addr(weights, torch.float32, (T, topk), dev, "weights"), T, topk,
+        _addr(out, torch.bfloat16, (T, N), dev, "out"), _queue(stream, dev)))
     return out
 
 
@@ -491,22 +515,22 @@ def qlinear_moe_int8(x, expert_ids, expert_weights, fc1, fc2, y=None, workspace=
     """y [T,N] bf16 = sum_j expert_weights[t,j] fc2_e(bf16(gelu(fc1_e(x[t])))) over e = expert_ids[t,j]
     (int32 [T,topk]; an id outside the experts adds nothing); fc1 and fc2 are dicts with weight
     int8 [E,H,K] / [E,N,H] and weight_scale float32 [E,H] / [E,N]."""
-    T, K = _dims(x, 2, "x")
     topk = _dims(expert_ids, 2, "expert_ids")[1]
-    E, H = _dims(fc1["weight"], 3, "fc1.weight")[:2]
+    E, H, _ = _dims(fc1["weight"], 3, "fc1.weight")
     N = _dims(fc2["weight"], 3, "fc2.weight")[1]
-    _inputs(x=(x, torch.bfloat16, (T, K)), expert_ids=(expert_ids, torch.int32, (T, topk)),
-            expert_weights=(expert_weights, torch.float32, (T, topk)),
-            **{"fc1.weight": (fc1["weight"], torch.int8, (E, H, K)),
-               "fc1.weight_scale": (fc1["weight_scale"], torch.float32, (E, H)),
-               "fc2.weight": (fc2["weight"], torch.int8, (E, N, H)),
-               "fc2.weight_scale": (fc2["weight_scale"], torch.float32, (E, N))})
-    y = _out(y, (T, N), torch.bfloat16, x.device, stream, "y")
-    ws, nbytes = _scratch(workspace, qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E), x.device, stream)
+    dev = _current(x, 2, "x")
+    T, K = x.shape
+    y = _new((T, N), torch.bfloat16, x, stream) if y is None else y
+    ws, nbytes = _scratch(workspace, qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E), x, dev, stream)
     _check("qlinear_moe_int8", load().qlinear_moe_int8(
-        _ptr(x), T, K, H, N, E, topk, _ptr(expert_ids), _ptr(expert_weights), _ptr(fc1["weight"]),
-        _ptr(fc1["weight_scale"]), _ptr(fc2["weight"]), _ptr(fc2["weight_scale"]), _ptr(y), _ptr(ws), nbytes,
-        _stream(stream)))
+        _addr(x, torch.bfloat16, (T, K), dev, "x"), T, K, H, N, E, topk,
+        _addr(expert_ids, torch.int32, (T, topk), dev, "expert_ids"),
+        _addr(expert_weights, torch.float32, (T, topk), dev, "expert_weights"),
+        _addr(fc1["weight"], torch.int8, (E, H, K), dev, "fc1.weight"),
+        _addr(fc1["weight_scale"], torch.float32, (E, H), dev, "fc1.weight_scale"),
+        _addr(fc2["weight"], torch.int8, (E, N, H), dev, "fc2.weight"),
+        _addr(fc2["weight_scale"], torch.float32, (E, N), dev, "fc2.weight_scale"),
+        _addr(y, torch.bfloat16, (T, N), dev, "y"), ws.data_ptr(), nbytes, _queue(stream, dev)))
     return y
 
 

@@ -16,7 +16,7 @@ namespace {
 // [0, E): slot -1, and row_index -1 behind the last place.  Every workgroup reads
 // all choices (from L2), which costs less than a second launch.
 // ---------------------------------------------------------------------------
-template <int W>
+template <int W, int B>
 __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ ids, int n, int topk, int E,
                                                         int* __restrict__ row_index, int* __restrict__ slot,
                                                         int* __restrict__ offsets) {
@@ -27,29 +27,35 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
   const int lo = first < n ? (int)first : n;
   const int hi = first + run < n ? (int)(first + run) : n;
   const uint64_t before = (1ull << lane) - 1ull;
-  // four consecutive choices of a lane; behind the end an id that is nobody's (INT_MIN
-  // counts as outside [0, E), but its place in the arrays is never written)
-  auto load = [&](int i, int (&v)[4]) {
-    if (i + 4 <= hi) {
-      const i32x4 t = *reinterpret_cast<const i32x4*>(ids + i);
+  // B times four consecutive choices of a lane, 256 apart, in flight together; behind the end
+  // an id that is nobody's (INT_MIN is outside [0, E), but its place is never written)
+  auto load = [&](int i0, int (&v)[B][4]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = t[c];
-    } else {
+    for (int u = 0; u < B; ++u) {
+      const int i = i0 + 256 * u + 4 * lane;
+      if (i + 4 <= hi) {
+        const i32x4 t = *reinterpret_cast<const i32x4*>(ids + i);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = i + c < hi ? ids[i + c] : INT32_MIN;
+        for (int c = 0; c < 4; ++c) v[u][c] = t[c];
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[u][c] = i + c < hi ? ids[i + c] : INT32_MIN;
+      }
     }
   };
   for (int64_t e64 = blockIdx.x; e64 <= E; e64 += gridDim.x) {
     const int e = (int)e64;
     int below = 0, own = 0;
-    for (int i = lo + 4 * lane; i < hi; i += 256) {
-      int v[4];
-      load(i, v);
+    for (int i0 = lo; i0 < hi; i0 += 256 * B) {
+      int v[B][4];
+      load(i0, v);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        below += v[c] >= 0 && v[c] < e;
-        own += v[c] == e;
-      }
+      for (int u = 0; u < B; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          below += v[u][c] >= 0 && v[u][c] < e;
+          own += v[u][c] == e;
+        }
     }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) {
@@ -68,35 +74,43 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
       int place = base;
       for (int w = 0; w < wv; ++w) place += own_s[w];
       if (own_s[wv] != 0) {
-        for (int i0 = lo; i0 < hi; i0 += 256) {
-          const int i = i0 + 4 * lane;
-          int v[4];
-          load(i, v);
-          uint64_t b[4];
+        for (int i0 = lo; i0 < hi; i0 += 256 * B) {
+          int v[B][4];
+          load(i0, v);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) b[c] = __ballot(v[c] == e);
-          int at = place;
+          for (int u = 0; u < B; ++u) {
+            uint64_t b[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            at += __popcll(b[c] & before);
-            place += __popcll(b[c]);
-          }
+            for (int c = 0; c < 4; ++c) b[c] = __ballot(v[u][c] == e);
+            if ((b[0] | b[1] | b[2] | b[3]) == 0) continue;
+            int at = place;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (v[c] == e) {
-              slot[i + c] = at;
-              row_index[at] = (i + c) / topk;
-              ++at;
+            for (int c = 0; c < 4; ++c) {
+              at += __popcll(b[c] & before);
+              place += __popcll(b[c]);
             }
+            const int i = i0 + 256 * u + 4 * lane;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (v[u][c] == e) {
+                slot[i + c] = at;
+                row_index[at] = (i + c) / topk;
+                ++at;
+              }
+          }
         }
       }
     } else {
-      for (int i = lo + 4 * lane; i < hi; i += 256) {
-        int v[4];
-        load(i, v);
+      for (int i0 = lo; i0 < hi; i0 += 256 * B) {
+        int v[B][4];
+        load(i0, v);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (i + c < hi && (v[c] < 0 || v[c] >= E)) slot[i + c] = -1;
+        for (int u = 0; u < B; ++u)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = i0 + 256 * u + 4 * lane + c;
+            if (i < hi && (v[u][c] < 0 || v[u][c] >= E)) slot[i] = -1;
+          }
       }
       for (int64_t i = (int64_t)base + threadIdx.x; i < n; i += 64 * W) row_index[i] = -1;
     }
@@ -153,10 +167,10 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64
                               int32_t* slot, int32_t* offsets, hipStream_t stream) {
   const dim3 grid((unsigned)(E + 1));
   if (n <= 4096)
-    hipLaunchKernelGGL((k_expert_plan<4>), grid, dim3(256), 0, stream, ids, (int)n, (int)topk, (int)E, row_index, slot,
+    hipLaunchKernelGGL((k_expert_plan<4, 4>), grid, dim3(256), 0, stream, ids, (int)n, (int)topk, (int)E, row_index, slot,
                        offsets);
   else
-    hipLaunchKernelGGL((k_expert_plan<16>), grid, dim3(1024), 0, stream, ids, (int)n, (int)topk, (int)E, row_index,
+    hipLaunchKernelGGL((k_expert_plan<16, 8>), grid, dim3(1024), 0, stream, ids, (int)n, (int)topk, (int)E, row_index,
                        slot, offsets);
   return hipGetLastError();
 }

@@ -235,7 +235,10 @@ struct Int8Args {
   const RowTile* tiles;  // grouped: the row tiles
 };
 
-typedef int i32x4v __attribute__((ext_vector_type(4)));
+// Four outputs stored at 2-byte alignment: rows of y may start at any element.
+struct __attribute__((packed, aligned(2))) Segment4 {
+  u32x2 v;
+};
 
 __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
@@ -245,9 +248,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, (int)kRawBufferWord3);
 }
 
-template <int MT, int NT, int W, int EPI, bool GROUPED>
+// U: pieces of a wavefront in flight together.
+template <int MT, int NT, int W, int U, int EPI, bool GROUPED>
 __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __restrict__ Y, EpiArgs e) {
-  constexpr int U = MT * NT >= 8 ? 1 : 2;  // pieces loaded together
   __shared__ i32x4 red[W][MT * NT][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -325,8 +328,8 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
         }
         uint16_t* dst = out_ptr<EPI>(Y, m, n, p.N, e);
         const uint32_t w0 = pack_bf16(o[0], o[1]), w1 = pack_bf16(o[2], o[3]);
-        if ((p.N & 3) == 0) {
-          *reinterpret_cast<u32x2*>(dst) = u32x2{w0, w1};
+        if (n + 4 <= p.N) {
+          reinterpret_cast<Segment4*>(dst)->v = u32x2{w0, w1};
         } else {
           dst[0] = (uint16_t)w0;
           if (n + 1 < p.N) dst[1] = (uint16_t)(w0 >> 16);
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
 
 constexpr int64_t kDirectBlocks = int64_t(1) << 22;  // workgroups stride over tiles past this many
 
-template <int MT, int NT, int W, bool GROUPED>
+template <int MT, int NT, int W, int U, bool GROUPED>
 hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
   p.tiles_m = row_tiles;
   p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
@@ -349,13 +352,13 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
   const dim3 grid((unsigned)(n < kDirectBlocks ? n : kDirectBlocks)), block(64 * W);
   EpiArgs e;
   switch (epi_kind(ep, e)) {
-    case 0: hipLaunchKernelGGL((k_int8_direct<MT, NT, W, 0, GROUPED>), grid, block, 0, stream, p, y, e); break;
+    case 0: hipLaunchKernelGGL((k_int8_direct<MT, NT, W, U, 0, GROUPED>), grid, block, 0, stream, p, y, e); break;
     case EPI_GELU:
-      hipLaunchKernelGGL((k_int8_direct<MT, NT, W, EPI_GELU, GROUPED>), grid, block, 0, stream, p, y, e);
+      hipLaunchKernelGGL((k_int8_direct<MT, NT, W, U, EPI_GELU, GROUPED>), grid, block, 0, stream, p, y, e);
       break;
     case EPI_QKV:
       if constexpr (!GROUPED) {
-        hipLaunchKernelGGL((k_int8_direct<MT, NT, W, EPI_QKV, false>), grid, block, 0, stream, p, y, e);
+        hipLaunchKernelGGL((k_int8_direct<MT, NT, W, U, EPI_QKV, false>), grid, block, 0, stream, p, y, e);
         break;
       }
     default: return hipErrorInvalidValue;
@@ -367,9 +370,9 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
 // The product through LDS, for enough rows to reuse the weight.  A workgroup of four
 // wavefronts (2 x 2) owns 64 NJM rows of x by 64 NI columns; a wavefront
 // owns 32 NJ x 32 NI (V_MFMA_I32_32X32X32_I8, int32 accumulators).  Workgroups are
-// persistent; K is walked in 128-byte pieces of both operands, two stages of them in
-// LDS, filled by buffer_load_dwordx4 ... lds: piece P + 1's loads are issued between
-// piece P's MFMAs, so they have the whole piece to arrive.  The pieces of all of a
+// persistent; K is walked in 128-byte pieces of both operands, S stages of them in
+// LDS, filled by buffer_load_dwordx4 ... lds: piece P + S - 1's loads are issued between
+// piece P's MFMAs, so they have S - 1 pieces' time to arrive.  The pieces of all of a
 // workgroup's tiles form one stream.
 //
 // A tile with at most half (a quarter) of its rows present, an expert's last one for
@@ -377,10 +380,11 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
 // exist.  Chunk c of a 128-byte stage row r sits at chunk c ^ (r % 8): the 16-byte
 // operand reads of a wavefront fall on distinct banks.
 //
-// Top of a piece: wait for its loads (issued during the piece before; only the output
-// stores issued after them may be in flight), then a barrier: the piece is in LDS for
-// every wavefront, and every wavefront is done with the piece before, whose stage the next
-// loads fill.
+// Top of a piece: wait for its loads, then a barrier: the piece is in LDS for every
+// wavefront, and every wavefront is done with the piece before, whose stage the next loads fill.
+// A wavefront's vector memory operations retire in issue order, so the wait names how many
+// later ones may be in flight: the loads of S - 2 pieces (LOADS + 2 each) and the output
+// stores of an epilogue among the last S - 1 pieces.  A smaller number than that only waits longer.
 // ---------------------------------------------------------------------------
 struct StagedArgs {
   Int8Args g;
@@ -399,15 +403,20 @@ __device__ __forceinline__ void walk(int64_t s, int tiles_m, int tiles_n, int& t
   tn = r / gm;
 }
 
-template <int NI, int NJM, int EPI, bool GROUPED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NI * NJM == 16 ? 1 : 2, NI * NJM == 16 ? 1 : 2)))
+// Workgroups that share a CU: as many as its 160 KB of LDS hold.
+template <int NI, int NJM, int S>
+constexpr int staged_per_cu() { return (160 << 10) / (64 * (NI + NJM) * (PR_ROW + 4) * S + 256); }
+
+template <int NI, int NJM, int S, int EPI, bool GROUPED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu((staged_per_cu<NI, NJM, S>()), (staged_per_cu<NI, NJM, S>()))))
 void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   constexpr int XR = 64 * NJM, WR = 64 * NI;     // rows of x and of W per stage
   constexpr int STAGE = (XR + WR) * PR_ROW;
   constexpr int XL = 2 * NJM, LOADS = XL + 2 * NI;  // loads per wavefront per piece: x, all
   constexpr int SBUF = (XR + WR) * 4;            // output scales of a tile
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t lsc[2 * SBUF + 256];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * STAGE];
+  // output scales: a tile's are loaded up to S - 1 tiles ahead
+  __shared__ __attribute__((aligned(16))) uint8_t lsc[S * SBUF + 256];
   const Int8Args& p = a.g;
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -454,10 +463,10 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
 
   struct Piece {
     u32x4 dx, dw, ds;
-    int koff, stage, par;
+    int koff, stage, buf;
     bool first, valid;
   };
-  int s_i = 0, s_k = 0, s_stage = 0;
+  int s_i = 0, s_k = 0, s_stage = 0, s_buf = 0;
   Tile s_t{0, 0, 0, 0};
   if (nt > 0) s_t = tile(0);
   auto next_piece = [&]() {
@@ -465,17 +474,18 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     r.valid = s_i < nt;
     r.stage = s_stage;
     r.first = s_k == 0;
-    r.par = s_i & 1;
+    r.buf = s_buf;
     r.koff = s_k * PR_ROW;
     const int rn = (int)(p.N - s_t.n0 < WR ? p.N - s_t.n0 : WR);
     r.dx = make_desc(p.x + s_t.m0 * p.K, (int64_t)s_t.rows * p.K);
     r.dw = make_desc(p.w + ((int64_t)s_t.e * p.N + s_t.n0) * p.K, (int64_t)rn * p.K);
     const bool row = wv < 2;
     r.ds = make_desc(row ? p.xs + s_t.m0 : p.ws + (int64_t)s_t.e * p.N + s_t.n0, (row ? s_t.rows : rn) * 4);
-    s_stage ^= 1;
+    s_stage = s_stage == S - 1 ? 0 : s_stage + 1;
     if (++s_k == np) {
       s_k = 0;
       ++s_i;
+      s_buf = s_buf == S - 1 ? 0 : s_buf + 1;
       if (s_i < nt) s_t = tile(s_i);
     }
     return r;
@@ -492,7 +502,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   auto issue_scales = [&](const Piece& s, int hh) {
     const int c = 2 * (wv & 1) + hh;
     const bool real = s.valid && s.first && c < (wv < 2 ? NJM : NI);
-    const uint32_t dst = sbase + (real ? s.par * SBUF + (wv < 2 ? 0 : XR * 4) + c * 256 : 2 * SBUF);
+    const uint32_t dst = sbase + (real ? s.buf * SBUF + (wv < 2 ? 0 : XR * 4) + c * 256 : S * SBUF);
     dma4(dst, real ? (uint32_t)((c * 64 + lane) * 4) : kOutOfRange, s.ds, 0);
   };
 
@@ -509,29 +519,39 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   };
   Frag fw[NI], fx[NJM];
 
-  {
+#pragma unroll
+  for (int ahead = 0; ahead < S - 1; ++ahead) {
     const Piece s = next_piece();
 #pragma unroll
     for (int d = 0; d < LOADS; ++d) issue(s, d);
     issue_scales(s, 0);
     issue_scales(s, 1);
   }
-  int stores = 0;  // output stores in flight behind the current piece's loads
+  constexpr int LATER = (S - 2) * (LOADS + 2);  // loads of the pieces behind the current one
+  constexpr int STORES = 2 * NI * NJM;          // output stores of a whole tile
+  static_assert(LATER + STORES < 64, "vmcnt holds 63");
+  int st[S - 1] = {};  // stores issued by the epilogue after each of the last S - 1 pieces
   int cur = 0;
   auto piece = [&](auto& acc, auto nj) {
     constexpr int NJ = decltype(nj)::value;
     constexpr int T = NI * NJ;  // tiles of 32 x 32 per wavefront
-    if (stores == 2 * NI * NJM) {
-      QPL_WAIT_VMCNT(2 * NI * NJM);
+    int stores = 0;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) stores += st[i];
+    if (stores == STORES) {
+      QPL_WAIT_VMCNT(LATER + STORES);
     } else {
-      QPL_WAIT_VMCNT(0);
+      QPL_WAIT_VMCNT(LATER);
     }
     __builtin_amdgcn_s_barrier();
-    stores = 0;
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = S - 2; i > 0; --i) st[i] = st[i - 1];
+    st[0] = 0;
     const Piece s = next_piece();
     const uint8_t* cs = lds + cur * STAGE;
     const uint8_t* cw = cs + XR * PR_ROW;
-    cur ^= 1;
+    cur = cur == S - 1 ? 0 : cur + 1;
 #pragma unroll
     for (int i = 0; i < NI; ++i) fw[i] = frag(cw, wn * 32 * NI + i * 32 + r32, 0);
 #pragma unroll
@@ -562,7 +582,8 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
         __builtin_amdgcn_sched_barrier(0);
       }
   };
-  auto run_tile = [&](const Tile& t, int i, auto nj) {
+  int buf = 0;
+  auto run_tile = [&](const Tile& t, auto nj) {
     constexpr int NJ = decltype(nj)::value;
     i32x16 acc[NI][NJ];
 #pragma unroll
@@ -570,43 +591,42 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
 #pragma unroll
       for (int y = 0; y < NJ; ++y) acc[x][y] = i32x16{};
     for (int k = 0; k < np; ++k) piece(acc, nj);
-    const float* ls = reinterpret_cast<const float*>(lsc + (i & 1) * SBUF);
-    // the stores of a tile of fewer rows are waited for, so that `stores` has one value
-    stores = __builtin_amdgcn_readfirstlane(store_tile<NJ, NI, EPI>(
+    const float* ls = reinterpret_cast<const float*>(lsc + buf * SBUF);
+    buf = buf == S - 1 ? 0 : buf + 1;
+    st[0] = __builtin_amdgcn_readfirstlane(store_tile<NJ, NI, EPI, true>(
         acc, wm, wn, lane, t.m0, t.n0, t.m0 + t.rows, p.N, Y, [&](int r) { return ls[r]; },
         [&](int c) { return *reinterpret_cast<const f32x4*>(&ls[XR + c]); }, e));
   };
   for (int i = 0; i < nt; ++i) {
     const Tile t = tile(i);
-    if (t.rows > XR / 2) {
-      run_tile(t, i, std::integral_constant<int, NJM>{});
-    } else if (NJM < 4 || t.rows > XR / 4) {
-      if constexpr (NJM >= 2) run_tile(t, i, std::integral_constant<int, NJM / 2>{});
+    if (NJM == 1 || t.rows > XR / 2) {
+      run_tile(t, std::integral_constant<int, NJM>{});
+    } else if (NJM == 2 || t.rows > XR / 4) {
+      if constexpr (NJM >= 2) run_tile(t, std::integral_constant<int, NJM / 2>{});
     } else {
-      if constexpr (NJM >= 4) run_tile(t, i, std::integral_constant<int, NJM / 4>{});
+      if constexpr (NJM >= 4) run_tile(t, std::integral_constant<int, NJM / 4>{});
     }
   }
   QPL_WAIT_VMCNT(0);
   QPL_WAIT_LGKM0();
 }
 
-template <int NI, int NJM, bool GROUPED>
+template <int NI, int NJM, int S, bool GROUPED>
 hipError_t launch_staged(const Int8Args& g, int64_t row_tiles, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
   StagedArgs a;
   a.g = g;
   a.tiles_m = (int)row_tiles;
   a.tiles_n = (int)((g.N + 64 * NI - 1) / (64 * NI));
-  // one workgroup of 256 x 256 per CU, two of the smaller tiles
-  const int64_t n = row_tiles * a.tiles_n, most = NI * NJM == 16 ? 256 : 512;
+  const int64_t n = row_tiles * a.tiles_n, most = 256 * staged_per_cu<NI, NJM, S>();
   a.nwg = (int)(n < most ? n : most);
   const dim3 grid((unsigned)a.nwg), block(256);
   EpiArgs e;
   switch (epi_kind(ep, e)) {
-    case 0: hipLaunchKernelGGL((k_int8_staged<NI, NJM, 0, GROUPED>), grid, block, 0, stream, a, y, e); break;
-    case EPI_GELU: hipLaunchKernelGGL((k_int8_staged<NI, NJM, EPI_GELU, GROUPED>), grid, block, 0, stream, a, y, e); break;
+    case 0: hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, 0, GROUPED>), grid, block, 0, stream, a, y, e); break;
+    case EPI_GELU: hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, EPI_GELU, GROUPED>), grid, block, 0, stream, a, y, e); break;
     case EPI_QKV:
       if constexpr (!GROUPED) {
-        hipLaunchKernelGGL((k_int8_staged<NI, NJM, EPI_QKV, false>), grid, block, 0, stream, a, y, e);
+        hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, EPI_QKV, false>), grid, block, 0, stream, a, y, e);
         break;
       }
     default: return hipErrorInvalidValue;
@@ -633,10 +653,10 @@ hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, 
   p.M = M;
   p.N = N;
   p.K = (int)K;
-  if (M <= 16) return launch_direct<1, 1, 8, false>(p, (M + 15) / 16, ep, y, stream);
-  if (M <= 256) return launch_direct<4, 4, 4, false>(p, (M + 63) / 64, ep, y, stream);
-  if (((M + 255) / 256) * ((N + 255) / 256) >= 192) return launch_staged<4, 4, false>(p, (M + 255) / 256, ep, y, stream);
-  return launch_staged<2, 2, false>(p, (M + 127) / 128, ep, y, stream);
+  if (M <= 16) return launch_direct<1, 1, 8, 2, false>(p, (M + 15) / 16, ep, y, stream);
+  if (M <= 256) return launch_direct<4, 4, 4, 1, false>(p, (M + 63) / 64, ep, y, stream);
+  if (((M + 255) / 256) * ((N + 255) / 256) >= 192) return launch_staged<4, 4, 2, false>(p, (M + 255) / 256, ep, y, stream);
+  return launch_staged<2, 2, 4, false>(p, (M + 127) / 128, ep, y, stream);
 }
 
 // Rows of a grouped product's tile.
@@ -676,10 +696,10 @@ hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int
   p.count = tiles;
   p.tiles = reinterpret_cast<const RowTile*>(tiles) + 1;
   const int64_t cap = grouped_row_tiles(R, E);
-  if (grouped_tile(R, E) == 16) return launch_direct<1, 1, 8, true>(p, cap, ep, y, stream);
-  if (grouped_tile(R, E) == 64) return launch_direct<4, 4, 4, true>(p, cap, ep, y, stream);
-  if (grouped_tile(R, E) == 128) return launch_staged<2, 2, true>(p, cap, ep, y, stream);
-  return launch_staged<4, 4, true>(p, cap, ep, y, stream);
+  if (grouped_tile(R, E) == 16) return launch_direct<1, 1, 8, 2, true>(p, cap, ep, y, stream);
+  if (grouped_tile(R, E) == 64) return launch_direct<4, 4, 4, 1, true>(p, cap, ep, y, stream);
+  if (grouped_tile(R, E) == 128) return launch_staged<2, 2, 4, true>(p, cap, ep, y, stream);
+  return launch_staged<4, 4, 2, true>(p, cap, ep, y, stream);
 }
 
 }  // namespace qpl

@@ -111,8 +111,12 @@ __device__ __forceinline__ float to_f32(int v) { return (float)v; }
 // m0 + 64 wm + 32 j + l % 32); NI: 32-column blocks per wavefront (4: columns
 // n0 + 128 wn + ..., wn in 0..1; 2: n0 + 64 wn + ..., wn in 0..3).  Returns the
 // number of store instructions left in flight: 2 NJ NI on the interior path, 0 on
-// the edge path (which checks every element and drains its stores).
-template <int NJ, int NI, int EPI, bool FAST, class Acc, class RowScale, class ColScale>
+// the edge path (which checks every element and drains its stores).  ANY: rows of y may
+// start at any element, and 16-byte segments are stored at 2-byte alignment.
+struct __attribute__((packed, aligned(2))) Segment {
+  u32x4 v;
+};
+template <int NJ, int NI, int EPI, bool FAST, bool ANY, class Acc, class RowScale, class ColScale>
 __device__ __forceinline__ void store_tile_path(const Acc& acc, int wm, int wn, int lane, int64_t m0, int64_t n0,
                                                 int64_t M, int64_t N, uint16_t* __restrict__ y, const RowScale& rs,
                                                 const ColScale& cs, const EpiArgs& e) {
@@ -148,12 +152,16 @@ __device__ __forceinline__ void store_tile_path(const Acc& acc, int wm, int wn, 
         const int64_t n = n0 + wn * 32 * NI + i * 32 + (2 * gp + (lane >> 5)) * 8;
         // the segment's eight columns stay inside one head (head_dim >= 8, n % 8 == 0)
         uint16_t* dst = out_ptr<EPI>(y, m, n, N, e);
-        if constexpr (FAST) {
+        if constexpr (FAST && !ANY) {
           *reinterpret_cast<u32x4*>(dst) = v;
+        } else if constexpr (FAST) {
+          reinterpret_cast<Segment*>(dst)->v = v;
         } else if (m < M) {
           const uint32_t el[4] = {v.x, v.y, v.z, v.w};
-          if ((N & 7) == 0 && n + 8 <= N) {
+          if (!ANY && (N & 7) == 0 && n + 8 <= N) {
             *reinterpret_cast<u32x4*>(dst) = v;
+          } else if (ANY && n + 8 <= N) {
+            reinterpret_cast<Segment*>(dst)->v = v;
           } else {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -164,18 +172,18 @@ __device__ __forceinline__ void store_tile_path(const Acc& acc, int wm, int wn, 
   });
 }
 
-template <int NJ, int NI = 4, int EPI = 0, class Acc, class RowScale, class ColScale>
+template <int NJ, int NI = 4, int EPI = 0, bool ANY = false, class Acc, class RowScale, class ColScale>
 __device__ __forceinline__ int store_tile(const Acc& acc, int wm, int wn, int lane, int64_t m0, int64_t n0,
                                           int64_t M, int64_t N, uint16_t* __restrict__ y, const RowScale& rs,
                                           const ColScale& cs, const EpiArgs& e = EpiArgs{}) {
   // interior: the wavefront's rows and columns all inside the matrix; the two paths
   // are separate code, so the interior one has no per-segment branches
-  const bool fast = m0 + (wm + 1) * 32 * NJ <= M && n0 + (wn + 1) * 32 * NI <= N && (N & 7) == 0;
+  const bool fast = m0 + (wm + 1) * 32 * NJ <= M && n0 + (wn + 1) * 32 * NI <= N && (ANY || (N & 7) == 0);
   if (fast) {
-    store_tile_path<NJ, NI, EPI, true>(acc, wm, wn, lane, m0, n0, M, N, y, rs, cs, e);
+    store_tile_path<NJ, NI, EPI, true, ANY>(acc, wm, wn, lane, m0, n0, M, N, y, rs, cs, e);
     return 2 * NJ * NI;
   }
-  store_tile_path<NJ, NI, EPI, false>(acc, wm, wn, lane, m0, n0, M, N, y, rs, cs, e);
+  store_tile_path<NJ, NI, EPI, false, ANY>(acc, wm, wn, lane, m0, n0, M, N, y, rs, cs, e);
   QPL_WAIT_VMCNT(0);
   return 0;
 }
