@@ -257,8 +257,9 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
   const int r16 = lane & 15, q = lane >> 4;
   const int64_t tiles_m = GROUPED ? p.count[0] : p.tiles_m;
   const int pieces = (p.K + 127) >> 7;
-  for (int64_t t = blockIdx.x; t < tiles_m * p.tiles_n; t += gridDim.x) {
-    const int64_t tm = t / p.tiles_n, n0 = (t - tm * p.tiles_n) * 16 * NT;
+  for (int64_t tm = blockIdx.y; tm < tiles_m; tm += gridDim.y)
+  for (int64_t tn = blockIdx.x; tn < p.tiles_n; tn += gridDim.x) {
+    const int64_t n0 = tn * 16 * NT;
     int64_t m0, m1;
     const int8_t* w = p.w;
     const float* wsc = p.ws;
@@ -305,6 +306,14 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
             for (int j = 0; j < NT; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx[u][s][i], acc[i][j], 0, 0, 0);
     }
+    // The last MFMA's result is stored to LDS right behind the loop.  The wait states in
+    // between are spelled out: a build of this kernel had none on the path out of the loop,
+    // and stored sums without the last MFMA's share.
+    asm volatile("s_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -342,14 +351,16 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
   }
 }
 
-constexpr int64_t kDirectBlocks = int64_t(1) << 22;  // workgroups stride over tiles past this many
+// Workgroups stride over column and row tiles past these numbers.
+constexpr int64_t kDirectColumns = int64_t(1) << 21, kDirectRows = 65535;
 
 template <int MT, int NT, int W, int U, bool GROUPED>
 hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
   p.tiles_m = row_tiles;
   p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
-  const int64_t n = p.tiles_m * p.tiles_n;
-  const dim3 grid((unsigned)(n < kDirectBlocks ? n : kDirectBlocks)), block(64 * W);
+  const dim3 grid((unsigned)(p.tiles_n < kDirectColumns ? p.tiles_n : kDirectColumns),
+                  (unsigned)(row_tiles < kDirectRows ? row_tiles : kDirectRows));
+  const dim3 block(64 * W);
   EpiArgs e;
   switch (epi_kind(ep, e)) {
     case 0: hipLaunchKernelGGL((k_int8_direct<MT, NT, W, U, 0, GROUPED>), grid, block, 0, stream, p, y, e); break;
@@ -383,8 +394,8 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
 // Top of a piece: wait for its loads, then a barrier: the piece is in LDS for every
 // wavefront, and every wavefront is done with the piece before, whose stage the next loads fill.
 // A wavefront's vector memory operations retire in issue order, so the wait names how many
-// later ones may be in flight: the loads of S - 2 pieces (LOADS + 2 each) and the output
-// stores of an epilogue among the last S - 1 pieces.  A smaller number than that only waits longer.
+// later ones may be in flight: the loads of the pieces behind it (LOADS + 2 each) and the output
+// stores of epilogues issued after its loads.  A smaller number than that only waits longer.
 // ---------------------------------------------------------------------------
 struct StagedArgs {
   Int8Args g;
@@ -394,11 +405,13 @@ struct StagedArgs {
 
 // Tile (row tile, column tile) at position s of the walk: groups of four row tiles,
 // column by column, so that workgroups of one XCD share operand rows in its L2.
-__device__ __forceinline__ void walk(int64_t s, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int64_t per_group = (int64_t)GROUP_M * tiles_n;
-  const int g = (int)(s / per_group);
+// Tiles number below 2^31: y has at most 2^40 elements and a tile 2^12 of them, and the
+// grouped weights' columns, E N <= 2^36, bound the tiles of experts with few rows.
+__device__ __forceinline__ void walk(int s, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per_group = GROUP_M * tiles_n;
+  const int g = s / per_group;
   const int gm = min(tiles_m - g * GROUP_M, GROUP_M);
-  const int r = (int)(s - g * per_group);
+  const int r = s - g * per_group;
   tm = g * GROUP_M + r % gm;
   tn = r / gm;
 }
@@ -425,7 +438,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   const int b = blockIdx.x;
   const uint32_t lbase = lds_address(lds), sbase = lds_address(lsc);
   const int tiles_m = GROUPED ? __builtin_amdgcn_readfirstlane(p.count[0]) : a.tiles_m;
-  const int64_t ntiles = (int64_t)tiles_m * a.tiles_n;
+  const int ntiles = tiles_m * a.tiles_n;
   const int np = (p.K + PR_ROW - 1) / PR_ROW;
 
   struct Tile {
@@ -433,7 +446,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     int rows, e;
   };
   auto position = [&](int i) {
-    return (a.nwg & 7) == 0 ? (int64_t)i * a.nwg + (b & 7) * (a.nwg >> 3) + (b >> 3) : (int64_t)i * a.nwg + b;
+    return (a.nwg & 7) == 0 ? i * a.nwg + (b & 7) * (a.nwg >> 3) + (b >> 3) : i * a.nwg + b;
   };
   auto tile = [&](int i) {
     Tile t;
@@ -461,32 +474,36 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   const uint32_t vx = (uint32_t)((XR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
   const uint32_t vw = (uint32_t)((WR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
 
+  // The stream of pieces: the descriptors change where it enters a tile, from piece to
+  // piece only the byte offset along K does.
   struct Piece {
-    u32x4 dx, dw, ds;
     int koff, stage, buf;
     bool first, valid;
   };
   int s_i = 0, s_k = 0, s_stage = 0, s_buf = 0;
-  Tile s_t{0, 0, 0, 0};
-  if (nt > 0) s_t = tile(0);
+  u32x4 dx{}, dw{}, ds{};
+  auto enter = [&](int i) {
+    const Tile t = tile(i);
+    const int rn = (int)(p.N - t.n0 < WR ? p.N - t.n0 : WR);
+    dx = make_desc(p.x + t.m0 * p.K, (int64_t)t.rows * p.K);
+    dw = make_desc(p.w + ((int64_t)t.e * p.N + t.n0) * p.K, (int64_t)rn * p.K);
+    const bool row = wv < 2;
+    ds = make_desc(row ? p.xs + t.m0 : p.ws + (int64_t)t.e * p.N + t.n0, (row ? t.rows : rn) * 4);
+  };
+  // the piece to load next; its loads have to be issued before the following call
   auto next_piece = [&]() {
     Piece r;
     r.valid = s_i < nt;
-    r.stage = s_stage;
     r.first = s_k == 0;
+    if (r.first && r.valid) enter(s_i);
+    r.stage = s_stage;
     r.buf = s_buf;
     r.koff = s_k * PR_ROW;
-    const int rn = (int)(p.N - s_t.n0 < WR ? p.N - s_t.n0 : WR);
-    r.dx = make_desc(p.x + s_t.m0 * p.K, (int64_t)s_t.rows * p.K);
-    r.dw = make_desc(p.w + ((int64_t)s_t.e * p.N + s_t.n0) * p.K, (int64_t)rn * p.K);
-    const bool row = wv < 2;
-    r.ds = make_desc(row ? p.xs + s_t.m0 : p.ws + (int64_t)s_t.e * p.N + s_t.n0, (row ? s_t.rows : rn) * 4);
     s_stage = s_stage == S - 1 ? 0 : s_stage + 1;
     if (++s_k == np) {
       s_k = 0;
       ++s_i;
       s_buf = s_buf == S - 1 ? 0 : s_buf + 1;
-      if (s_i < nt) s_t = tile(s_i);
     }
     return r;
   };
@@ -495,7 +512,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     const int q = d < XL ? d : d - XL;
     const uint32_t dst = lbase + s.stage * STAGE + (d < XL ? XR / 4 * wv + 8 * q : XR + WR / 4 * wv + 8 * q) * PR_ROW;
     const uint32_t vo = in ? (d < XL ? vx : vw) + (uint32_t)(8 * q * p.K) : kOutOfRange;
-    dma16(dst, vo, d < XL ? s.dx : s.dw, s.koff);
+    dma16(dst, vo, d < XL ? dx : dw, s.koff);
   };
   // the tile's output scales, 64 per load: wavefronts 0 and 1 those of x, 2 and 3 those of W; every
   // piece issues two loads per wavefront (out of range, into a spare area, unless it starts a tile)
@@ -503,7 +520,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     const int c = 2 * (wv & 1) + hh;
     const bool real = s.valid && s.first && c < (wv < 2 ? NJM : NI);
     const uint32_t dst = sbase + (real ? s.buf * SBUF + (wv < 2 ? 0 : XR * 4) + c * 256 : S * SBUF);
-    dma4(dst, real ? (uint32_t)((c * 64 + lane) * 4) : kOutOfRange, s.ds, 0);
+    dma4(dst, real ? (uint32_t)((c * 64 + lane) * 4) : kOutOfRange, ds, 0);
   };
 
   struct Frag {
@@ -531,7 +548,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   constexpr int STORES = 2 * NI * NJM;          // output stores of a whole tile
   static_assert(LATER + STORES < 64, "vmcnt holds 63");
   int st[S - 1] = {};  // stores issued by the epilogue after each of the last S - 1 pieces
-  int cur = 0;
+  int cur = 0;         // stage of the piece being multiplied
   auto piece = [&](auto& acc, auto nj) {
     constexpr int NJ = decltype(nj)::value;
     constexpr int T = NI * NJ;  // tiles of 32 x 32 per wavefront
@@ -591,6 +608,8 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
 #pragma unroll
       for (int y = 0; y < NJ; ++y) acc[x][y] = i32x16{};
     for (int k = 0; k < np; ++k) piece(acc, nj);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");  // as behind the direct kernel's loop
+    __builtin_amdgcn_sched_barrier(0);
     const float* ls = reinterpret_cast<const float*>(lsc + buf * SBUF);
     buf = buf == S - 1 ? 0 : buf + 1;
     st[0] = __builtin_amdgcn_readfirstlane(store_tile<NJ, NI, EPI, true>(
