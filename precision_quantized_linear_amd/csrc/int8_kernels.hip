@@ -4,6 +4,8 @@
 // Quantizer.  a = max_k |x[m, k]|, s = fp32(a / 127), q = rint(127 x / a), ties to even.
 // The sums of products are int32 and exact for K <= 2^17 (127 * 128 * 2^17 < 2^31), so a
 // result does not depend on how K is split over wavefronts or workgroups.
+#include <cmath>
+
 #include "qpl_gemm.h"
 
 namespace qpl {
@@ -662,6 +664,76 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const floa
              : launch_quant_rows<false, false, false>(x, M, M, K, nullptr, nullptr, xq, xs, none, stream);
 }
 
+namespace {
+
+// ---------------------------------------------------------------------------
+// Which kernel multiplies.  A workgroup's time is about
+//   (pieces of 128 bytes of K) * piece + tile   microseconds
+// with the constants below, and the 256 CUs take the tiles in rounds; the shape with the least
+// time is taken.  The direct kernel's piece is its bytes at 42 KB/us (operand rows that do not
+// exist cost nothing), the staged kernel's was measured for each tile: about 60 KB/us of
+// operands up to 128 x 128, MFMAs and LDS reads above.  Measured, the best shape against the next ones (us):
+//   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 256x128 256x256
+//   1    4096 4096   5.3   7.0
+//   1    2048 6144   5.7   5.0   5.1   7.5
+//   16   4096 12288  16.9  15.7        14.3
+//   64   4096 4096   13    12.1  10.2  12.4
+//   64   8192 1024   9.6   12.7  16.4  21.1
+//   128  2048 6144                     7.9   9.1    13
+//   512  4096 4096                     18.6  17.6   22.9
+//   1024 4096 4096                           27.2   24.4    30.8
+//   512  4096 12288                                 40.4    33.9    51
+//   4096 4096 12288                                 220     210     183
+// ---------------------------------------------------------------------------
+struct Shape {
+  int rows, cols;
+  double piece, tile;
+};
+constexpr Shape kShapes[] = {{16, 16, 0, 0.3},      {16, 32, 0, 0.3},       {32, 32, 0, 0.3},       {64, 64, 0.28, 0.5},
+                             {64, 128, 0.46, 0.8},  {128, 128, 0.62, 1.2},  {256, 128, 0.87, 3.7},  {256, 256, 1.6, 8}};
+constexpr int kNumShapes = 8;
+
+// tiles_m(rows): row tiles of that height; rows_each: rows that a row tile has at most; part:
+// workgroups end at different times (grouped tiles differ in rows), so rounds are not whole.
+template <class F>
+int pick_shape(const F& tiles_m, double rows_each, int64_t K, int64_t N, bool part) {
+  int best = 0;
+  double least = 0;
+  for (int v = 0; v < kNumShapes; ++v) {
+    const Shape& s = kShapes[v];
+    const double tiles = tiles_m(s.rows) * (double)((N + s.cols - 1) / s.cols) / 256;
+    const double rounds = part ? (tiles + 0.5 > 1 ? tiles + 0.5 : 1) : __builtin_ceil(tiles);
+    const double piece = s.piece > 0 ? s.piece : ((rows_each < s.rows ? rows_each : s.rows) + s.cols) * 128 / 42e3;
+    const double t = rounds * ((double)((K + 127) / 128) * piece + s.tile);
+    if (v == 0 || t < least) {
+      best = v;
+      least = t;
+    }
+  }
+  return best;
+}
+
+template <bool GROUPED>
+hipError_t launch_shape(int v, const Int8Args& p, int64_t row_tiles, const Epilogue& ep, uint16_t* y,
+                        hipStream_t stream) {
+  switch (v) {
+    case 0: return launch_direct<1, 1, 16, 2, GROUPED>(p, row_tiles, ep, y, stream);
+    case 1: return launch_direct<1, 2, 8, 2, GROUPED>(p, row_tiles, ep, y, stream);
+    case 2: return launch_direct<2, 2, 8, 2, GROUPED>(p, row_tiles, ep, y, stream);
+    case 3: return launch_staged<1, 1, 4, GROUPED>(p, row_tiles, ep, y, stream);
+    case 4: return launch_staged<2, 1, 3, GROUPED>(p, row_tiles, ep, y, stream);
+    case 5:
+      // one workgroup per CU with four stages, or past 256 tiles two with two stages: 192 tiles of
+      // K = 2048 take 13.5 against 15.6 us, 384 of them 24.6 against 19.1 us
+      if (row_tiles * ((p.N + 127) / 128) <= 256) return launch_staged<2, 2, 4, GROUPED>(p, row_tiles, ep, y, stream);
+      return launch_staged<2, 2, 2, GROUPED>(p, row_tiles, ep, y, stream);
+    case 6: return launch_staged<2, 4, 3, GROUPED>(p, row_tiles, ep, y, stream);
+    default: return launch_staged<4, 4, 2, GROUPED>(p, row_tiles, ep, y, stream);
+  }
+}
+
+}  // namespace
+
 hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,
                             int64_t N, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
   Int8Args p{};
@@ -672,29 +744,38 @@ hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, 
   p.M = M;
   p.N = N;
   p.K = (int)K;
-  if (M <= 16) return launch_direct<1, 1, 8, 2, false>(p, (M + 15) / 16, ep, y, stream);
-  if (M <= 256) return launch_direct<4, 4, 4, 1, false>(p, (M + 63) / 64, ep, y, stream);
-  if (((M + 255) / 256) * ((N + 255) / 256) >= 192) return launch_staged<4, 4, 2, false>(p, (M + 255) / 256, ep, y, stream);
-  return launch_staged<2, 2, 4, false>(p, (M + 127) / 128, ep, y, stream);
+  const int v = pick_shape([&](int rows) { return (double)((M + rows - 1) / rows); }, (double)M, K, N, false);
+  return launch_shape<false>(v, p, (M + kShapes[v].rows - 1) / kShapes[v].rows, ep, y, stream);
 }
 
-// Rows of a grouped product's tile.
-static int grouped_tile(int64_t R, int64_t E) { return R <= 16 * E ? 16 : R <= 32 * E ? 64 : R <= 128 * E ? 128 : 256; }
-
-int64_t grouped_row_tiles(int64_t R, int64_t E) {
-  const int tm = grouped_tile(R, E);
-  return R / tm + (E < R ? E : R);
+// The shape of a grouped product.  The host knows the number of rows, not how the experts share
+// them: of E experts that R rows are dealt to, E (1 - (1 - 1/E)^R) have any, and half a tile more
+// than R / rows for each of them is a fair guess.
+static int grouped_shape(int64_t R, int64_t K, int64_t N, int64_t E) {
+  const double used = (double)E * -std::expm1((double)R * std::log1p(-1.0 / (double)(E > 1 ? E : 2)));
+  const double some = E > 1 ? (used > 1 ? used : 1) : 1;
+  return pick_shape(
+      [&](int rows) {
+        const double t = (double)R / rows + some / 2;
+        return t > some ? t : some;
+      },
+      (double)R / some, K, N, true);
 }
 
-hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, const int32_t* row_index,
-                                     const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
+// Row tiles of a grouped product: every expert with rows has at most one that is not full.
+static int64_t row_tile_bound(int64_t R, int64_t E, int rows) { return R / rows + (E < R ? E : R); }
+
+int64_t grouped_row_tiles(int64_t R, int64_t E) { return row_tile_bound(R, E, kShapes[0].rows); }
+
+hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, int64_t N,
+                                     const int32_t* row_index, const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
                                      hipStream_t stream) {
   TilePlan t;
   t.offsets = offsets;
   t.E = (int)E;
   t.R = (int)R;
-  t.tm = grouped_tile(R, E);
-  t.cap = (int)grouped_row_tiles(R, E);
+  t.tm = kShapes[grouped_shape(R, K, N, E)].rows;
+  t.cap = (int)row_tile_bound(R, E, t.tm);
   t.count = tiles;
   t.tiles = reinterpret_cast<RowTile*>(tiles) + 1;
   return row_index ? launch_quant_rows<false, true, true>(x, rows_x, R, K, nullptr, row_index, xq, xs, t, stream)
@@ -714,11 +795,8 @@ hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int
   p.K = (int)K;
   p.count = tiles;
   p.tiles = reinterpret_cast<const RowTile*>(tiles) + 1;
-  const int64_t cap = grouped_row_tiles(R, E);
-  if (grouped_tile(R, E) == 16) return launch_direct<1, 1, 8, 2, true>(p, cap, ep, y, stream);
-  if (grouped_tile(R, E) == 64) return launch_direct<4, 4, 4, 1, true>(p, cap, ep, y, stream);
-  if (grouped_tile(R, E) == 128) return launch_staged<2, 2, 4, true>(p, cap, ep, y, stream);
-  return launch_staged<4, 4, 2, true>(p, cap, ep, y, stream);
+  const int v = grouped_shape(R, K, N, E);
+  return launch_shape<true>(v, p, row_tile_bound(R, E, kShapes[v].rows), ep, y, stream);
 }
 
 }  // namespace qpl

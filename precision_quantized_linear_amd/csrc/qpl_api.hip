@@ -737,7 +737,7 @@ qpl_status grouped_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, in
   float* xs = reinterpret_cast<float*>(ws + L.xs);
   int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
   const qpl_status s = launched(Timed(QPL_KERNEL_QUANT_INT8, st)(
-      qpl::launch_quant_int8_grouped(x, M, R, K, row_index, offsets, E, xq, xs, tiles, st)));
+      qpl::launch_quant_int8_grouped(x, M, R, K, N, row_index, offsets, E, xq, xs, tiles, st)));
   if (s != QPL_OK) return s;
   return launched(Timed(QPL_KERNEL_GEMM_INT8_GROUPED, st)(
       qpl::launch_gemm_int8_grouped(xq, xs, weight, weight_scale, R, K, N, E, tiles, ep, y, st)));

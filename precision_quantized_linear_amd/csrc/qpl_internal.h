@@ -127,8 +127,8 @@ hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, 
 // x[row_index[i]], or x[i] without row_index) and, from offsets [E + 1], the list of
 // row tiles that the product walks: 16 (1 + grouped_row_tiles(R, E)) bytes.
 int64_t grouped_row_tiles(int64_t R, int64_t E);
-hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, const int32_t* row_index,
-                                     const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
+hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, int64_t N,
+                                     const int32_t* row_index, const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
                                      hipStream_t stream);
 hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t R,
                                     int64_t K, int64_t N, int64_t E, const int32_t* tiles, const Epilogue& ep,
