@@ -316,8 +316,8 @@ qpl_status qlinear_mlp_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t H,
  * qlinear_int8: y[m,n] = bf16_rne((sum_k q_x q_w) s_x[m] weight_scale[n]), the sum
  *   exact in int32, with q_x, s_x from quant_act_int8(x, smooth).
  *   weight int8 [N,K], any codes in [-128, 127]; weight_scale float [N]; ws of at
- *   least qlinear_workspace_bytes(QPL_INT8, M, K, N, 0), which after the call holds
- *   the quantized activation: x_q, then (from byte 256 ceil(M K / 256)) x_scale.
+ *   least qlinear_workspace_bytes(QPL_INT8, M, K, N, 0) bytes (its contents after the
+ *   call are unspecified: a few rows are quantized inside the product's kernel).
  * qlinear_int8_ex: the same with an epilogue (see qlinear_fp8r_ex).
  * All pointers 16-byte aligned.  K <= 2^17 for the linears (QPL_ERR_SHAPE beyond).
  */

@@ -10,17 +10,29 @@ namespace {
 // ---------------------------------------------------------------------------
 // Plan: a stable counting sort of n choices ids[i] in [0, E) without atomics or a
 // workspace.  Workgroup e serves expert e: it counts the choices below e (the
-// expert's first place) and its own, then hands out its places in order of i.
+// expert's first place) and lists its own, then hands out its places in order of i.
 // Each wavefront owns a contiguous run of choices, so a place is the expert's first +
-// the counts of earlier wavefronts + a ballot prefix.  Workgroup E serves the ids outside
-// [0, E): slot -1, and row_index -1 behind the last place.  Every workgroup reads
-// all choices (from L2), which costs less than a second launch.
+// the counts of earlier wavefronts + a ballot prefix.  A wavefront lists up to LIST
+// choices in LDS; one that finds more reads its run again.  Workgroup E serves the ids
+// outside [0, E): slot -1, and row_index -1 behind the last place.  Every workgroup
+// reads all choices (from L2), which costs less than a second launch.
 // ---------------------------------------------------------------------------
+constexpr int LIST = 256;
+
+// i / topk for 0 <= i < 2^31: mul is ceil(2^shift / topk) with shift = 31 + ceil(log2 topk), so
+// mul topk exceeds 2^shift by at most topk and the quotient is exact.
+struct Divider {
+  uint64_t mul;
+  int shift;
+  __device__ __forceinline__ int operator()(int i) const { return (int)(((uint64_t)(uint32_t)i * mul) >> shift); }
+};
+
 template <int W, int B>
-__global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ ids, int n, int topk, int E,
+__global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ ids, int n, Divider token, int E,
                                                         int* __restrict__ row_index, int* __restrict__ slot,
                                                         int* __restrict__ offsets) {
   __shared__ int below_s[W], own_s[W];
+  __shared__ int list[W][LIST];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int run = (n / (256 * W) + 1) * 256;  // choices per wavefront, a multiple of 256
   const int64_t first = (int64_t)wv * run;
@@ -43,25 +55,44 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
       }
     }
   };
-  for (int64_t e64 = blockIdx.x; e64 <= E; e64 += gridDim.x) {
-    const int e = (int)e64;
-    int below = 0, own = 0;
+  // found(i, r) for the run's r-th choice i of expert e, in order; returns their number
+  auto scan = [&](int e, auto count, auto found) {
+    int own = 0;
     for (int i0 = lo; i0 < hi; i0 += 256 * B) {
       int v[B][4];
       load(i0, v);
 #pragma unroll
-      for (int u = 0; u < B; ++u)
+      for (int u = 0; u < B; ++u) {
+        uint64_t b[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          below += v[u][c] >= 0 && v[u][c] < e;
-          own += v[u][c] == e;
+          count(v[u][c]);
+          b[c] = __ballot(v[u][c] == e);
         }
-    }
+        if ((b[0] | b[1] | b[2] | b[3]) == 0) continue;
+        int at = own;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      below += __shfl_xor(below, d, 64);
-      own += __shfl_xor(own, d, 64);
+        for (int c = 0; c < 4; ++c) {
+          at += __popcll(b[c] & before);
+          own += __popcll(b[c]);
+        }
+        const int i = i0 + 256 * u + 4 * lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (v[u][c] == e) found(i + c, at++);
+      }
     }
+    return own;
+  };
+  for (int e = blockIdx.x; e <= E; e += gridDim.x) {
+    int below = 0;
+    const int own = scan(
+        e, [&](int v) { below += (uint32_t)v < (uint32_t)e; },
+        [&](int i, int r) {
+          if (r < LIST) list[wv][r] = i;
+        });
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) below += __shfl_xor(below, d, 64);
     if (lane == 0) {
       below_s[wv] = below;
       own_s[wv] = own;
@@ -73,34 +104,22 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
     if (e < E) {
       int place = base;
       for (int w = 0; w < wv; ++w) place += own_s[w];
-      if (own_s[wv] != 0) {
-        for (int i0 = lo; i0 < hi; i0 += 256 * B) {
-          int v[B][4];
-          load(i0, v);
-#pragma unroll
-          for (int u = 0; u < B; ++u) {
-            uint64_t b[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) b[c] = __ballot(v[u][c] == e);
-            if ((b[0] | b[1] | b[2] | b[3]) == 0) continue;
-            int at = place;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              at += __popcll(b[c] & before);
-              place += __popcll(b[c]);
-            }
-            const int i = i0 + 256 * u + 4 * lane;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (v[u][c] == e) {
-                slot[i + c] = at;
-                row_index[at] = (i + c) / topk;
-                ++at;
-              }
-          }
+      if (own <= LIST) {
+        for (int r = lane; r < own; r += 64) {
+          const int i = list[wv][r];
+          slot[i] = place + r;
+          row_index[place + r] = token(i);
         }
+      } else {
+        scan(
+            e, [](int) {},
+            [&](int i, int r) {
+              slot[i] = place + r;
+              row_index[place + r] = token(i);
+            });
       }
     } else {
+      // an id outside [0, E) is E itself, counted as this workgroup's own, or above, or negative
       for (int i0 = lo; i0 < hi; i0 += 256 * B) {
         int v[B][4];
         load(i0, v);
@@ -109,7 +128,7 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int i = i0 + 256 * u + 4 * lane + c;
-            if (i < hi && (v[u][c] < 0 || v[u][c] >= E)) slot[i] = -1;
+            if (i < hi && (uint32_t)v[u][c] >= (uint32_t)E) slot[i] = -1;
           }
       }
       for (int64_t i = (int64_t)base + threadIdx.x; i < n; i += 64 * W) row_index[i] = -1;
@@ -166,11 +185,16 @@ __global__ __launch_bounds__(256) void k_expert_combine(const uint16_t* __restri
 hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
                               int32_t* slot, int32_t* offsets, hipStream_t stream) {
   const dim3 grid((unsigned)(E + 1));
+  Divider token;
+  token.shift = 31;
+  while ((int64_t{1} << (token.shift - 31)) < topk) ++token.shift;
+  token.mul = ((uint64_t{1} << token.shift) + (uint64_t)topk - 1) / (uint64_t)topk;
+  // 4 wavefronts per expert while each still has at most 1024 choices, else 16
   if (n <= 4096)
-    hipLaunchKernelGGL((k_expert_plan<4, 4>), grid, dim3(256), 0, stream, ids, (int)n, (int)topk, (int)E, row_index, slot,
+    hipLaunchKernelGGL((k_expert_plan<4, 2>), grid, dim3(256), 0, stream, ids, (int)n, token, (int)E, row_index, slot,
                        offsets);
   else
-    hipLaunchKernelGGL((k_expert_plan<16, 8>), grid, dim3(1024), 0, stream, ids, (int)n, (int)topk, (int)E, row_index,
+    hipLaunchKernelGGL((k_expert_plan<16, 8>), grid, dim3(1024), 0, stream, ids, (int)n, token, (int)E, row_index,
                        slot, offsets);
   return hipGetLastError();
 }

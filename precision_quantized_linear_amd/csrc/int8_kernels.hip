@@ -13,8 +13,9 @@ namespace qpl {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Row quantizer: one wavefront per row, four rows per workgroup (VPT 16-byte vectors
-// per lane stay in registers between the two passes; VPT == 0 streams the row twice).
+// Row quantizer: one wavefront per row and four rows per workgroup, or (SPLIT) a workgroup
+// per row when there are too few rows to fill the chip; VPT 16-byte vectors per lane stay in
+// registers between the two passes (VPT == 0 streams the row twice).
 //
 // The code is rint of the exact quotient 127 x / a.  x = i 2^p and a = j 2^q have 8-bit
 // integers i, j, so 127 x / a either is a tie (k + 1/2, at most 8 significant bits) or
@@ -74,56 +75,63 @@ __device__ __forceinline__ u32x4 smooth_vec(const u32x4& v, const float* __restr
                smooth_pair(v.w, b[2], b[3])};
 }
 
-// GATHER: row i is x[row_index[i]] (a row of zeros for an index outside x).
-template <int VPT, bool SMOOTH, bool GATHER>
+// GATHER: row i is x[row_index[i]] (a row of zeros for an index outside x).  SPLIT: the
+// workgroup's four wavefronts share the row.
+template <int VPT, bool SMOOTH, bool GATHER, bool SPLIT>
 __device__ __forceinline__ void quant_row(const uint16_t* __restrict__ x, int64_t rows_x, int64_t row, int64_t K,
                                           const float* __restrict__ lam, const int* __restrict__ row_index,
                                           int8_t* __restrict__ xq, float* __restrict__ xs) {
-  const int lane = threadIdx.x & 63;
+  constexpr int STEP = SPLIT ? 256 : 64;
+  const int first = SPLIT ? threadIdx.x : threadIdx.x & 63;
   const int64_t nv = K >> 3;
   u32x2* qr = reinterpret_cast<u32x2*>(xq + row * K);
   int64_t src = row;
   if constexpr (GATHER) {
     src = row_index[row];
     if (src < 0 || src >= rows_x) {
-      for (int64_t j = lane; j < nv; j += 64) qr[j] = u32x2{0u, 0u};
-      if (lane == 0) xs[row] = 0.0f;
+      for (int64_t j = first; j < nv; j += STEP) qr[j] = u32x2{0u, 0u};
+      if (first == 0) xs[row] = 0.0f;
       return;
     }
   }
   const u32x4* xr = reinterpret_cast<const u32x4*>(x + src * K);
+  auto load = [&](int64_t j) {
+    const u32x4 v = GATHER ? xr[j] : __builtin_nontemporal_load(xr + j);
+    return SMOOTH ? smooth_vec(v, lam + 8 * j) : v;
+  };
+  auto row_max = [&](uint32_t am) {
+    float a = wave_max(absmax_value(am));
+    if constexpr (SPLIT) {
+      __shared__ float part[4];
+      __syncthreads();  // the row before is done with part
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+      __syncthreads();
+      a = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    }
+    return a;
+  };
   uint32_t am = 0;
   if constexpr (VPT > 0) {
     u32x4 v[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t j = lane + 64 * i;
-      if (j < nv) {
-        v[i] = GATHER ? xr[j] : __builtin_nontemporal_load(xr + j);
-        if constexpr (SMOOTH) v[i] = smooth_vec(v[i], lam + 8 * j);
-        am = vec_absmax8(v[i], am);
-      }
+      const int64_t j = first + STEP * i;
+      v[i] = j < nv ? load(j) : u32x4{0u, 0u, 0u, 0u};
     }
-    const RowCode d = row_code(wave_max(absmax_value(am)));
-    if (lane == 0) xs[row] = d.s;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) am = vec_absmax8(v[i], am);
+    const RowCode d = row_code(row_max(am));
+    if (first == 0) xs[row] = d.s;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t j = lane + 64 * i;
+      const int64_t j = first + STEP * i;
       if (j < nv) qr[j] = code_vec(v[i], d);
     }
   } else {
-    for (int64_t j = lane; j < nv; j += 64) {
-      u32x4 v = xr[j];
-      if constexpr (SMOOTH) v = smooth_vec(v, lam + 8 * j);
-      am = vec_absmax8(v, am);
-    }
-    const RowCode d = row_code(wave_max(absmax_value(am)));
-    if (lane == 0) xs[row] = d.s;
-    for (int64_t j = lane; j < nv; j += 64) {
-      u32x4 v = xr[j];
-      if constexpr (SMOOTH) v = smooth_vec(v, lam + 8 * j);
-      qr[j] = code_vec(v, d);
-    }
+    for (int64_t j = first; j < nv; j += STEP) am = vec_absmax8(load(j), am);
+    const RowCode d = row_code(row_max(am));
+    if (first == 0) xs[row] = d.s;
+    for (int64_t j = first; j < nv; j += STEP) qr[j] = code_vec(load(j), d);
   }
 }
 
@@ -176,7 +184,7 @@ struct TilePlan {
   RowTile* tiles;
 };
 
-template <int VPT, bool SMOOTH, bool GROUPED, bool GATHER>
+template <int VPT, bool SMOOTH, bool GROUPED, bool GATHER, bool SPLIT>
 __global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__ x, int64_t rows_x, int64_t rows,
                                                     int64_t K, const float* __restrict__ lam,
                                                     const int* __restrict__ row_index, int8_t* __restrict__ xq,
@@ -191,27 +199,44 @@ __global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__
     blk -= 1;
     nblk -= 1;
   }
-  for (int64_t row = blk * 4 + (threadIdx.x >> 6); row < rows; row += nblk * 4)
-    quant_row<VPT, SMOOTH, GATHER>(x, rows_x, row, K, lam, row_index, xq, xs);
+  constexpr int ROWS = SPLIT ? 1 : 4;  // rows of a workgroup
+  for (int64_t row = blk * ROWS + (SPLIT ? 0 : threadIdx.x >> 6); row < rows; row += nblk * ROWS)
+    quant_row<VPT, SMOOTH, GATHER, SPLIT>(x, rows_x, row, K, lam, row_index, xq, xs);
 }
 
 constexpr int64_t kQuantBlocks = int64_t(1) << 22;  // workgroups stride over rows past this many
 
-template <bool SMOOTH, bool GROUPED, bool GATHER>
+template <bool SMOOTH, bool GROUPED, bool GATHER, bool SPLIT>
 hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, const float* lam,
                              const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
-  const int64_t per_lane = (K / 8 + 63) / 64;
-  const int64_t blocks = (rows + 3) / 4;
+  const int64_t per_lane = SPLIT ? (K / 8 + 255) / 256 : (K / 8 + 63) / 64;
+  const int64_t blocks = SPLIT ? rows : (rows + 3) / 4;
   const dim3 grid((unsigned)((blocks < kQuantBlocks ? blocks : kQuantBlocks) + (GROUPED ? 1 : 0))), block(256);
-#define QPL_CASE(V)                                                                                          \
-  if (per_lane <= V || V == 0) {                                                                             \
-    hipLaunchKernelGGL((k_quant_int8<V, SMOOTH, GROUPED, GATHER>), grid, block, 0, stream, x, rows_x, rows, K, lam, \
-                       row_index, xq, xs, plan);                                                             \
-    return hipGetLastError();                                                                                \
+#define QPL_CASE(V)                                                                                                   \
+  if (per_lane <= V || V == 0) {                                                                                      \
+    hipLaunchKernelGGL((k_quant_int8<V, SMOOTH, GROUPED, GATHER, SPLIT>), grid, block, 0, stream, x, rows_x, rows, K, \
+                       lam, row_index, xq, xs, plan);                                                                 \
+    return hipGetLastError();                                                                                         \
   }
-  QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(16) QPL_CASE(24) QPL_CASE(0)
+  if constexpr (SPLIT) {
+    QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(0)
+  } else {
+    QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(16) QPL_CASE(24) QPL_CASE(0)
+  }
 #undef QPL_CASE
   return hipErrorInvalidValue;
+}
+
+// A workgroup per row up to kSplitRows rows.
+constexpr int64_t kSplitRows = 2048;
+
+template <bool SMOOTH, bool GROUPED, bool GATHER>
+hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, const float* lam,
+                        const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
+  return rows <= kSplitRows && K > 512
+             ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(x, rows_x, rows, K, lam, row_index, xq, xs, plan, stream)
+             : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(x, rows_x, rows, K, lam, row_index, xq, xs, plan,
+                                                                 stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -248,6 +273,29 @@ __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off)
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, (int)kRawBufferWord3);
+}
+
+// Outputs (m, n .. n + 3) of the sums, if m < m1, as far as n < N.
+template <int EPI>
+__device__ __forceinline__ void store_four(uint16_t* __restrict__ y, int64_t m, int64_t m1, int64_t n, int64_t N,
+                                           const i32x4& sum, float sx, const float* __restrict__ ws,
+                                           const EpiArgs& e) {
+  if (m >= m1 || n >= N) return;
+  float o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[k] = ((float)sum[k] * sx) * ws[n + k < N ? n + k : n];
+    if constexpr ((EPI & EPI_GELU) != 0) o[k] = gelu_tanh(o[k]);
+  }
+  uint16_t* dst = out_ptr<EPI>(y, m, n, N, e);
+  const uint32_t w0 = pack_bf16(o[0], o[1]), w1 = pack_bf16(o[2], o[3]);
+  if (n + 4 <= N) {
+    reinterpret_cast<Segment4*>(dst)->v = u32x2{w0, w1};
+  } else {
+    dst[0] = (uint16_t)w0;
+    if (n + 1 < N) dst[1] = (uint16_t)(w0 >> 16);
+    if (n + 2 < N) dst[2] = (uint16_t)w1;
+  }
 }
 
 // U: pieces of a wavefront in flight together.
@@ -329,25 +377,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
       for (int k = 1; k < W; ++k) sum += red[k][tile][l];
       const int64_t m = m0 + 16 * (tile / NT) + (l & 15);
       const int64_t n = n0 + 16 * (tile % NT) + 4 * (l >> 4);
-      if (m < m1 && n < p.N) {
-        const float sx = p.xs[m];
-        float o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[k] = ((float)sum[k] * sx) * wsc[n + k < p.N ? n + k : n];
-          if constexpr ((EPI & EPI_GELU) != 0) o[k] = gelu_tanh(o[k]);
-        }
-        uint16_t* dst = out_ptr<EPI>(Y, m, n, p.N, e);
-        const uint32_t w0 = pack_bf16(o[0], o[1]), w1 = pack_bf16(o[2], o[3]);
-        if (n + 4 <= p.N) {
-          reinterpret_cast<Segment4*>(dst)->v = u32x2{w0, w1};
-        } else {
-          dst[0] = (uint16_t)w0;
-          if (n + 1 < p.N) dst[1] = (uint16_t)(w0 >> 16);
-          if (n + 2 < p.N) dst[2] = (uint16_t)w1;
-          if (n + 3 < p.N) dst[3] = (uint16_t)(w1 >> 16);
-        }
-      }
+      store_four<EPI>(Y, m, m1, n, p.N, sum, m < m1 ? p.xs[m] : 0.0f, wsc, e);
     }
     __syncthreads();
   }
@@ -377,6 +407,128 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// A few rows (single tokens) in one launch: as the direct kernel, but every workgroup quantizes
+// the M <= 4 rows itself, into LDS, while its first weight bytes are on their way.  The
+// quantizer's launch and the wait for it cost more than the repeated work: at 1 x 4096 x 4096 the two
+// launches take 6.1 + 5.5 us.
+// SLOTS vectors of 8 elements per thread: row and part of a row.
+// ---------------------------------------------------------------------------
+constexpr int TOKEN_W = 16, TOKEN_SLOTS = 4, TOKEN_BYTES = TOKEN_SLOTS * 64 * TOKEN_W * 8;
+
+template <int NT, bool SMOOTH, int EPI>
+__global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __restrict__ x,
+                                                             const float* __restrict__ lam, Int8Args p,
+                                                             uint16_t* __restrict__ Y, EpiArgs e) {
+  constexpr int W = TOKEN_W, U = 2;
+  __shared__ __attribute__((aligned(16))) uint8_t codes[TOKEN_BYTES];  // [M, K]
+  __shared__ i32x4 red[W][NT][64];
+  __shared__ float part[TOKEN_SLOTS][W];
+  __shared__ float scale[TOKEN_SLOTS];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int r16 = lane & 15, q = lane >> 4;
+  const int M = (int)p.M, nv = p.K >> 3;
+  const int parts = (nv + 64 * W - 1) / (64 * W);  // slots per row
+  const int pieces = (p.K + 127) >> 7;
+  int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
+  __amdgpu_buffer_rsrc_t dw;
+  i32x4 fw[U][2][NT];
+  auto rows_of = [&](int64_t n) {
+    const int64_t nr = p.N - n < 16 * NT ? p.N - n : 16 * NT;
+    dw = make_rsrc(p.w + n * p.K, nr * p.K);
+  };
+  auto load_w = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int k = (c + u * W) * 128 + 64 * s + 16 * q;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          fw[u][s][j] = load16(dw, k < p.K ? (uint32_t)((16 * j + r16) * p.K + k) : kOutOfRange);
+      }
+  };
+  // the rows' vectors, then (behind them, so that they do not wait for it) the first weight bytes
+  u32x4 v[TOKEN_SLOTS];
+  int row = 0, sub = 0;
+#pragma unroll
+  for (int t = 0; t < TOKEN_SLOTS; ++t) {
+    const int j = sub * 64 * W + (int)threadIdx.x;
+    const bool in = row < M && j < nv;
+    v[t] = in ? reinterpret_cast<const u32x4*>(x + (int64_t)row * p.K)[j] : u32x4{0u, 0u, 0u, 0u};
+    if (SMOOTH && in) v[t] = smooth_vec(v[t], lam + 8 * (int64_t)j);
+    if (++sub == parts) {
+      sub = 0;
+      ++row;
+    }
+  }
+  rows_of(n0);
+  load_w(wv);
+#pragma unroll
+  for (int t = 0; t < TOKEN_SLOTS; ++t) {
+    const float a = wave_max(absmax_value(vec_absmax8(v[t], 0u)));
+    if (lane == 0) part[t][wv] = a;
+  }
+  __syncthreads();
+  row = 0;
+  sub = 0;
+#pragma unroll
+  for (int t = 0; t < TOKEN_SLOTS; ++t) {
+    const int j = sub * 64 * W + (int)threadIdx.x;
+    if (row >= M) break;
+    float a = 0.0f;
+    for (int i = row * parts; i < (row + 1) * parts; ++i) a = fmaxf(a, part[i][r16]);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor(a, d, 64));
+    const RowCode rc = row_code(a);
+    if (threadIdx.x == 0) scale[row] = rc.s;
+    if (j < nv) reinterpret_cast<u32x2*>(codes + row * p.K)[j] = code_vec(v[t], rc);
+    if (++sub == parts) {
+      sub = 0;
+      ++row;
+    }
+  }
+  __syncthreads();
+  for (;;) {
+    i32x4 acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = i32x4{0, 0, 0, 0};
+    for (int c = wv; c < pieces; c += W * U) {
+      if (c != wv) load_w(c);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int k = (c + u * W) * 128 + 64 * s + 16 * q;
+          i32x4 fx{0, 0, 0, 0};
+          if (r16 < M && k < p.K) fx = *reinterpret_cast<const i32x4*>(codes + r16 * p.K + k);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx, acc[j], 0, 0, 0);
+        }
+    }
+    asm volatile("s_nop 15" ::: "memory");  // as behind the direct kernel's loop
+#pragma unroll
+    for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[j]));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) red[wv][j][lane] = acc[j];
+    __syncthreads();
+    if ((int)threadIdx.x < NT * 64) {
+      const int j = threadIdx.x >> 6;
+      i32x4 sum = red[0][j][lane];
+#pragma unroll
+      for (int k = 1; k < W; ++k) sum += red[k][j][lane];
+      store_four<EPI>(Y, r16, M, n0 + 16 * j + 4 * q, p.N, sum, r16 < M ? scale[r16] : 0.0f, p.ws, e);
+    }
+    n0 += (int64_t)gridDim.x * 16 * NT;
+    if (n0 >= p.N) break;
+    __syncthreads();
+    rows_of(n0);
+    load_w(wv);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -660,8 +812,8 @@ hipError_t launch_staged(const Int8Args& g, int64_t row_tiles, const Epilogue& e
 hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const float* lam, int8_t* xq, float* xs,
                              hipStream_t stream) {
   const TilePlan none{};
-  return lam ? launch_quant_rows<true, false, false>(x, M, M, K, lam, nullptr, xq, xs, none, stream)
-             : launch_quant_rows<false, false, false>(x, M, M, K, nullptr, nullptr, xq, xs, none, stream);
+  return lam ? launch_quant<true, false, false>(x, M, M, K, lam, nullptr, xq, xs, none, stream)
+             : launch_quant<false, false, false>(x, M, M, K, nullptr, nullptr, xq, xs, none, stream);
 }
 
 namespace {
@@ -734,6 +886,47 @@ hipError_t launch_shape(int v, const Int8Args& p, int64_t row_tiles, const Epilo
 
 }  // namespace
 
+namespace {
+
+template <int NT, bool SMOOTH>
+hipError_t launch_token(const uint16_t* x, const float* lam, const Int8Args& p, const Epilogue& ep, uint16_t* y,
+                        hipStream_t stream) {
+  const int64_t n = (p.N + 16 * NT - 1) / (16 * NT);
+  const dim3 grid((unsigned)(n < kDirectColumns ? n : kDirectColumns)), block(64 * TOKEN_W);
+  EpiArgs e;
+  switch (epi_kind(ep, e)) {
+    case 0: hipLaunchKernelGGL((k_int8_token<NT, SMOOTH, 0>), grid, block, 0, stream, x, lam, p, y, e); break;
+    case EPI_GELU:
+      hipLaunchKernelGGL((k_int8_token<NT, SMOOTH, EPI_GELU>), grid, block, 0, stream, x, lam, p, y, e);
+      break;
+    case EPI_QKV:
+      hipLaunchKernelGGL((k_int8_token<NT, SMOOTH, EPI_QKV>), grid, block, 0, stream, x, lam, p, y, e);
+      break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool int8_token_fits(int64_t M, int64_t K) {
+  return M <= TOKEN_SLOTS && M * ((K / 8 + 64 * TOKEN_W - 1) / (64 * TOKEN_W)) <= TOKEN_SLOTS;
+}
+
+hipError_t launch_int8_token(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* w, const float* ws,
+                             const float* lam, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
+  Int8Args p{};
+  p.w = w;
+  p.ws = ws;
+  p.M = M;
+  p.N = N;
+  p.K = (int)K;
+  // 32 columns per workgroup where 16 would need more than two workgroups per CU
+  if (N > 512 * 16)
+    return lam ? launch_token<2, true>(x, lam, p, ep, y, stream) : launch_token<2, false>(x, lam, p, ep, y, stream);
+  return lam ? launch_token<1, true>(x, lam, p, ep, y, stream) : launch_token<1, false>(x, lam, p, ep, y, stream);
+}
+
 hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,
                             int64_t N, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
   Int8Args p{};
@@ -778,8 +971,8 @@ hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t 
   t.cap = (int)row_tile_bound(R, E, t.tm);
   t.count = tiles;
   t.tiles = reinterpret_cast<RowTile*>(tiles) + 1;
-  return row_index ? launch_quant_rows<false, true, true>(x, rows_x, R, K, nullptr, row_index, xq, xs, t, stream)
-                   : launch_quant_rows<false, true, false>(x, rows_x, R, K, nullptr, nullptr, xq, xs, t, stream);
+  return row_index ? launch_quant<false, true, true>(x, rows_x, R, K, nullptr, row_index, xq, xs, t, stream)
+                   : launch_quant<false, true, false>(x, rows_x, R, K, nullptr, nullptr, xq, xs, t, stream);
 }
 
 hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t R,

@@ -687,6 +687,9 @@ qpl_status int8_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const
   if (ws_bytes < L.total) return QPL_ERR_WORKSPACE;
   if ((s = check_device()) != QPL_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (qpl::int8_token_fits(M, K))
+    return launched(Timed(gemm_kind(ep, QPL_KERNEL_GEMM_INT8), st)(
+        qpl::launch_int8_token(x, M, K, N, weight, weight_scale, smooth, ep, y, st)));
   uint8_t* base = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(base + L.off[0]);
   float* xs = reinterpret_cast<float*>(base + L.off[1]);

@@ -123,6 +123,10 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const floa
                              hipStream_t stream);
 hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,
                             int64_t N, const Epilogue& ep, uint16_t* y, hipStream_t stream);
+// Quantizer and product of a few rows in one launch (int8_token_fits).
+bool int8_token_fits(int64_t M, int64_t K);
+hipError_t launch_int8_token(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* w, const float* ws,
+                             const float* lam, const Epilogue& ep, uint16_t* y, hipStream_t stream);
 // Grouped by expert: the quantizer writes the R product rows (row i from
 // x[row_index[i]], or x[i] without row_index) and, from offsets [E + 1], the list of
 // row tiles that the product walks: 16 (1 + grouped_row_tiles(R, E)) bytes.
