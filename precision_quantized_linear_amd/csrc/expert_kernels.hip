@@ -17,7 +17,7 @@ namespace {
 // outside [0, E): slot -1, and row_index -1 behind the last place.  Every workgroup
 // reads all choices (from L2), which costs less than a second launch.
 // ---------------------------------------------------------------------------
-constexpr int LIST = 256;
+constexpr int LIST = 512;
 
 // i / topk for 0 <= i < 2^31: mul is ceil(2^shift / topk) with shift = 31 + ceil(log2 topk), so
 // mul topk exceeds 2^shift by at most topk and the quotient is exact.
@@ -34,54 +34,36 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
   __shared__ int below_s[W], own_s[W];
   __shared__ int list[W][LIST];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int run = (n / (256 * W) + 1) * 256;  // choices per wavefront, a multiple of 256
+  const int run = (n / (64 * W) + 1) * 64;  // choices per wavefront, a multiple of 64
   const int64_t first = (int64_t)wv * run;
   const int lo = first < n ? (int)first : n;
   const int hi = first + run < n ? (int)(first + run) : n;
   const uint64_t before = (1ull << lane) - 1ull;
-  // B times four consecutive choices of a lane, 256 apart, in flight together; behind the end
-  // an id that is nobody's (INT_MIN is outside [0, E), but its place is never written)
-  auto load = [&](int i0, int (&v)[B][4]) {
+  // use(v, i) with choice i of the run for each lane, 64 at a time in order: batches of B loads
+  // in flight together, then single ones.  Behind the end stands an id that is nobody's (INT_MIN
+  // is outside [0, E)).
+  auto each = [&](auto use) {
+    int i0 = lo + lane;
+    for (; i0 - lane + 64 * B <= hi; i0 += 64 * B) {
+      int v[B];
 #pragma unroll
-    for (int u = 0; u < B; ++u) {
-      const int i = i0 + 256 * u + 4 * lane;
-      if (i + 4 <= hi) {
-        const i32x4 t = *reinterpret_cast<const i32x4*>(ids + i);
+      for (int u = 0; u < B; ++u) v[u] = ids[i0 + 64 * u];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[u][c] = t[c];
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[u][c] = i + c < hi ? ids[i + c] : INT32_MIN;
-      }
+      for (int u = 0; u < B; ++u) use(v[u], i0 + 64 * u);
     }
+    for (; i0 - lane < hi; i0 += 64) use(i0 < hi ? ids[i0] : INT32_MIN, i0);
   };
   // found(i, r) for the run's r-th choice i of expert e, in order; returns their number
   auto scan = [&](int e, auto count, auto found) {
     int own = 0;
-    for (int i0 = lo; i0 < hi; i0 += 256 * B) {
-      int v[B][4];
-      load(i0, v);
-#pragma unroll
-      for (int u = 0; u < B; ++u) {
-        uint64_t b[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          count(v[u][c]);
-          b[c] = __ballot(v[u][c] == e);
-        }
-        if ((b[0] | b[1] | b[2] | b[3]) == 0) continue;
-        int at = own;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          at += __popcll(b[c] & before);
-          own += __popcll(b[c]);
-        }
-        const int i = i0 + 256 * u + 4 * lane;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (v[u][c] == e) found(i + c, at++);
+    each([&](int v, int i) {
+      count(v);
+      const uint64_t b = __ballot(v == e);
+      if (b != 0) {
+        if (v == e) found(i, own + __popcll(b & before));
+        own += __popcll(b);
       }
-    }
+    });
     return own;
   };
   for (int e = blockIdx.x; e <= E; e += gridDim.x) {
@@ -120,17 +102,9 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
       }
     } else {
       // an id outside [0, E) is E itself, counted as this workgroup's own, or above, or negative
-      for (int i0 = lo; i0 < hi; i0 += 256 * B) {
-        int v[B][4];
-        load(i0, v);
-#pragma unroll
-        for (int u = 0; u < B; ++u)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int i = i0 + 256 * u + 4 * lane + c;
-            if (i < hi && (uint32_t)v[u][c] >= (uint32_t)E) slot[i] = -1;
-          }
-      }
+      each([&](int v, int i) {
+        if (i < hi && (uint32_t)v >= (uint32_t)E) slot[i] = -1;
+      });
       for (int64_t i = (int64_t)base + threadIdx.x; i < n; i += 64 * W) row_index[i] = -1;
     }
     __syncthreads();
@@ -191,10 +165,10 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64
   token.mul = ((uint64_t{1} << token.shift) + (uint64_t)topk - 1) / (uint64_t)topk;
   // 4 wavefronts per expert while each still has at most 1024 choices, else 16
   if (n <= 4096)
-    hipLaunchKernelGGL((k_expert_plan<4, 2>), grid, dim3(256), 0, stream, ids, (int)n, token, (int)E, row_index, slot,
+    hipLaunchKernelGGL((k_expert_plan<4, 8>), grid, dim3(256), 0, stream, ids, (int)n, token, (int)E, row_index, slot,
                        offsets);
   else
-    hipLaunchKernelGGL((k_expert_plan<16, 8>), grid, dim3(1024), 0, stream, ids, (int)n, token, (int)E, row_index,
+    hipLaunchKernelGGL((k_expert_plan<16, 16>), grid, dim3(1024), 0, stream, ids, (int)n, token, (int)E, row_index,
                        slot, offsets);
   return hipGetLastError();
 }
