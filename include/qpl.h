@@ -342,7 +342,9 @@ qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N,
  *   row_index   int32 [T topk]   out: the token of each place in expert order; -1 behind the last
  *   slot        int32 [T, topk]  out: the place of each choice, -1 for no expert
  *   offsets     int32 [E + 1]    out: expert e has the places offsets[e] .. offsets[e+1] - 1
- *   Places of one expert are in order of (token, choice).  No workspace, no atomics.
+ *   Places of one expert are in order of (token, choice).
+ *   ws          at least expert_plan_workspace_bytes(T, topk, E) bytes (0 for few choices or very
+ *               many experts: ws may then be NULL)
  *
  * qlinear_grouped_int8: product row i of R, offsets[e] <= i < offsets[e+1], is
  *   y[i] = bf16_rne(act((sum_k q_x q_w[e]) s_x weight_scale[e]))
@@ -372,7 +374,9 @@ qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N,
  * of range, QPL_ERR_ARG for an unknown act.
  */
 qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E,
-                       int32_t* row_index, int32_t* slot, int32_t* offsets, void* stream);
+                       int32_t* row_index, int32_t* slot, int32_t* offsets,
+                       void* ws, size_t ws_bytes, void* stream);
+size_t expert_plan_workspace_bytes(int64_t T, int64_t topk, int64_t E);
 size_t qlinear_grouped_int8_workspace_bytes(int64_t R, int64_t K, int64_t N, int64_t E);
 qpl_status qlinear_grouped_int8(const uint16_t* x, int64_t M, int64_t K, int64_t N, int64_t E,
                                 const int8_t* weight, const float* weight_scale,

@@ -22,7 +22,8 @@ EXPORTS = ("quant_act_fp8_row", "quant_act_nvfp4", "qlinear_fp8r", "qlinear_nvfp
            "qlinear_nvfp4_ex", "qlinear_int4_ex", "qlinear_mlp_nvfp4", "qlinear_mlp_nvfp4_workspace_bytes",
            "qlinear_workspace_bytes", "qpl_amax_bf16", "qpl_nvfp4_global_scale", "qpl_status_str",
            "qpl_timing_enable", "qpl_timing_select", "qpl_timing_collect", "qlinear_fp8r_noalloc",
-           "quant_act_int8", "qlinear_int8", "qlinear_int8_ex", "expert_plan", "qlinear_grouped_int8",
+           "quant_act_int8", "qlinear_int8", "qlinear_int8_ex", "expert_plan", "expert_plan_workspace_bytes",
+           "qlinear_grouped_int8",
            "qlinear_grouped_int8_workspace_bytes", "expert_combine", "qlinear_moe_int8",
            "qlinear_moe_int8_workspace_bytes")
 
@@ -87,7 +88,7 @@ def load():
         "quant_act_int8": [P, I64, I64, P, P, P, P],
         "qlinear_int8": [P, I64, I64, I64, P, P, P, P, P, SZ, P],
         "qlinear_int8_ex": [P, I64, I64, I64, P, P, P, P, P, P, SZ, P],
-        "expert_plan": [P, I64, I64, I64, P, P, P, P],
+        "expert_plan": [P, I64, I64, I64, P, P, P, P, SZ, P],
         "qlinear_grouped_int8": [P, I64, I64, I64, I64, P, P, P, I64, P, ctypes.c_int, P, P, SZ, P],
         "expert_combine": [P, I64, I64, P, P, I64, I64, P, P],
         "qlinear_moe_int8": [P, I64, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
@@ -100,6 +101,8 @@ def load():
     lib.qlinear_workspace_bytes.restype = SZ
     lib.qlinear_mlp_nvfp4_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64]
     lib.qlinear_mlp_nvfp4_workspace_bytes.restype = SZ
+    lib.expert_plan_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.expert_plan_workspace_bytes.restype = SZ
     lib.qlinear_grouped_int8_workspace_bytes.argtypes = [I64, I64, I64, I64]
     lib.qlinear_grouped_int8_workspace_bytes.restype = SZ
     lib.qlinear_moe_int8_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64]
@@ -447,7 +450,11 @@ def qlinear_int8(x, weight, weight_scale, y=None, workspace=None, stream=None, s
     return out
 
 
-def expert_plan(expert_ids, num_experts, row_index=None, slot=None, offsets=None, stream=None):
+def expert_plan_workspace_bytes(T, topk, num_experts):
+    return int(load().expert_plan_workspace_bytes(T, topk, num_experts))
+
+
+def expert_plan(expert_ids, num_experts, row_index=None, slot=None, offsets=None, workspace=None, stream=None):
     """Router choices int32 [T, topk] sorted by expert -> (row_index int32 [T topk]: the token of
     each place; slot int32 [T, topk]: the place of each choice; offsets int32 [num_experts + 1]:
     the experts' first places).  An id outside [0, num_experts) gets slot -1; row_index is -1
@@ -460,10 +467,12 @@ def expert_plan(expert_ids, num_experts, row_index=None, slot=None, offsets=None
     row_index = _new((T * topk,), torch.int32, expert_ids, stream) if row_index is None else row_index
     slot = _new((T, topk), torch.int32, expert_ids, stream) if slot is None else slot
     offsets = _new((E + 1,), torch.int32, expert_ids, stream) if offsets is None else offsets
+    need = expert_plan_workspace_bytes(T, topk, E)
+    ws, nbytes = (None, 0) if need == 0 else _scratch(workspace, need, expert_ids, dev, stream)
     _check("expert_plan", load().expert_plan(
         _addr(expert_ids, torch.int32, (T, topk), dev, "expert_ids"), T, topk, E,
         _addr(row_index, torch.int32, (T * topk,), dev, "row_index"), _addr(slot, torch.int32, (T, topk), dev, "slot"),
-        _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), _queue(stream, dev)))
+        _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), _ptr(ws), nbytes, _queue(stream, dev)))
     return row_index, slot, offsets
 
 

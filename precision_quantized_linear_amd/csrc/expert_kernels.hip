@@ -112,6 +112,127 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
+// Plan of many choices for up to PLAN_E experts, in two launches over chunks of them: every
+// workgroup of the second would have to read all choices to know the counts before its chunk,
+// so the first writes counts[chunk][expert] (order-free integer atomics in LDS).  The
+// second sums the columns of that matrix (an expert's first place, and what earlier chunks
+// take of it) and hands out its chunk's places: each wavefront owns a contiguous run of the
+// chunk, and of 64 choices those of one expert find each other by ballots over the id's bits.
+// 131072 choices of 256 experts: the form above reads them 257 times (19 us).
+// ---------------------------------------------------------------------------
+constexpr int PLAN_E = 1024, PLAN_W = 16;
+
+__global__ __launch_bounds__(64 * PLAN_W) void k_expert_count(const int* __restrict__ ids, int n, int chunk, int E,
+                                                              int* __restrict__ counts) {
+  __shared__ int own[PLAN_E];
+  for (int e = threadIdx.x; e < E; e += 64 * PLAN_W) own[e] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * chunk;
+  const int64_t hi = lo + chunk < n ? lo + chunk : n;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += 64 * PLAN_W) {
+    const uint32_t v = (uint32_t)ids[i];
+    if (v < (uint32_t)E) atomicAdd(&own[v], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 64 * PLAN_W) counts[(int64_t)blockIdx.x * E + e] = own[e];
+}
+
+__global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restrict__ ids, int n, int chunk,
+                                                              Divider token, int E, int bits,
+                                                              const int* __restrict__ counts,
+                                                              int* __restrict__ row_index, int* __restrict__ slot,
+                                                              int* __restrict__ offsets) {
+  constexpr int THREADS = 64 * PLAN_W;
+  __shared__ int next[PLAN_W][PLAN_E];  // a wavefront's next place of each expert
+  __shared__ int before[PLAN_E], total[PLAN_E], wave_sum[PLAN_W];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, c = blockIdx.x;
+  for (int e = threadIdx.x; e < E; e += THREADS) before[e] = total[e] = 0;
+  for (int i = threadIdx.x; i < PLAN_W * PLAN_E; i += THREADS) next[0][i] = 0;
+  __syncthreads();
+  // counts of this wavefront's run
+  const int64_t lo = (int64_t)c * chunk + (int64_t)wv * (chunk / PLAN_W);
+  const int64_t end = lo + chunk / PLAN_W;
+  const int64_t hi = end < n ? end : n;
+  for (int64_t i = lo + lane; i < hi; i += 64) {
+    const uint32_t v = (uint32_t)ids[i];
+    if (v < (uint32_t)E) atomicAdd(&next[wv][v], 1);
+  }
+  // column sums, THREADS / 2^bits rows of the matrix at a time
+  const int e0 = threadIdx.x & ((1 << bits) - 1), step = THREADS >> bits;
+  if (e0 < E) {
+    int b = 0, t = 0;
+#pragma unroll 16
+    for (int r = threadIdx.x >> bits; r < (int)gridDim.x; r += step) {
+      const int k = counts[(int64_t)r * E + e0];
+      t += k;
+      b += r < c ? k : 0;
+    }
+    atomicAdd(&total[e0], t);
+    atomicAdd(&before[e0], b);
+  }
+  __syncthreads();
+  // exclusive sum of the totals: thread e for expert e (E <= THREADS)
+  const int e = threadIdx.x;
+  const int mine = e < E ? total[e] : 0;
+  int sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(sum, d, 64);
+    if (lane >= d) sum += o;
+  }
+  if (lane == 63) wave_sum[wv] = sum;
+  __syncthreads();
+  int first = sum - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < PLAN_W; ++w) {
+    if (w < wv) first += wave_sum[w];
+    all += wave_sum[w];
+  }
+  if (e < E) {
+    if (c == 0) offsets[e] = first;
+    int place = first + before[e];
+#pragma unroll
+    for (int w = 0; w < PLAN_W; ++w) {
+      const int k = next[w][e];
+      next[w][e] = place;
+      place += k;
+    }
+  }
+  if (c == 0 && threadIdx.x == 0) offsets[E] = all;
+  __syncthreads();
+  const uint64_t earlier = (1ull << lane) - 1ull;
+  for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const int v = i < hi ? ids[i] : -1;
+    const bool valid = (uint32_t)v < (uint32_t)E;
+    uint64_t peers = __ballot(valid);
+    for (int k = 0; k < bits; ++k) {
+      const bool set = (v >> k) & 1;
+      const uint64_t b = __ballot(set);
+      peers &= set ? b : ~b;
+    }
+    if (valid) {
+      const int place = next[wv][v] + __popcll(peers & earlier);
+      slot[i] = place;
+      row_index[place] = token((int)i);
+      if ((peers & earlier) == 0) atomicAdd(&next[wv][v], __popcll(peers));
+    } else if (i < hi) {
+      slot[i] = -1;
+    }
+  }
+  for (int64_t i = (int64_t)all + (int64_t)c * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS)
+    row_index[i] = -1;
+}
+
+// Choices of a chunk: 2048, or what makes at most 256 chunks.
+int plan_chunk(int64_t n) {
+  const int64_t c = (n + 255) / 256;
+  return c <= 2048 ? 2048 : (int)((c + 1023) / 1024 * 1024);
+}
+
+bool plan_in_chunks(int64_t n, int64_t E) { return n >= 32768 && E <= PLAN_E; }
+
+// ---------------------------------------------------------------------------
 // Combine: out[t] = bf16(sum_j weight[t, j] y[slot[t, j]]), fp32, j ascending; a slot
 // outside [0, R) adds nothing.  VEC columns per thread (8: one 16-byte load per
 // row; 1 where rows are not 16-byte aligned).
@@ -156,13 +277,29 @@ __global__ __launch_bounds__(256) void k_expert_combine(const uint16_t* __restri
 
 }  // namespace
 
+size_t expert_plan_bytes(int64_t n, int64_t E) {
+  return plan_in_chunks(n, E) ? (size_t)(4 * E * ((n + plan_chunk(n) - 1) / plan_chunk(n))) : 0;
+}
+
 hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
-                              int32_t* slot, int32_t* offsets, hipStream_t stream) {
+                              int32_t* slot, int32_t* offsets, int32_t* counts, hipStream_t stream) {
   const dim3 grid((unsigned)(E + 1));
   Divider token;
   token.shift = 31;
   while ((int64_t{1} << (token.shift - 31)) < topk) ++token.shift;
   token.mul = ((uint64_t{1} << token.shift) + (uint64_t)topk - 1) / (uint64_t)topk;
+  if (plan_in_chunks(n, E)) {
+    const int chunk = plan_chunk(n);
+    const dim3 chunks((unsigned)((n + chunk - 1) / chunk)), block(64 * PLAN_W);
+    int bits = 0;
+    while ((int64_t{1} << bits) < E) ++bits;
+    hipLaunchKernelGGL(k_expert_count, chunks, block, 0, stream, ids, (int)n, chunk, (int)E, counts);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(k_expert_place, chunks, block, 0, stream, ids, (int)n, chunk, token, (int)E, bits, counts,
+                       row_index, slot, offsets);
+    return hipGetLastError();
+  }
   // 4 wavefronts per expert while each still has at most 1024 choices, else 16
   if (n <= 4096)
     hipLaunchKernelGGL((k_expert_plan<4, 8>), grid, dim3(256), 0, stream, ids, (int)n, token, (int)E, row_index, slot,

@@ -749,7 +749,7 @@ qpl_status grouped_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, in
 // Workspace of the MLP of experts: the arrays of the plan, h, the experts' outputs, and the
 // workspace of either product (they run one after the other).
 struct MoeLayout {
-  size_t row_index = 0, slot = 0, offsets = 0, h = 0, out = 0, ws = 0, total = 0;
+  size_t row_index = 0, slot = 0, offsets = 0, counts = 0, h = 0, out = 0, ws = 0, total = 0;
 };
 
 MoeLayout moe_layout(int64_t R, int64_t K, int64_t H, int64_t N, int64_t E) {
@@ -757,7 +757,8 @@ MoeLayout moe_layout(int64_t R, int64_t K, int64_t H, int64_t N, int64_t E) {
   const size_t ints = round256(size_t(4) * size_t(R));
   L.slot = L.row_index + ints;
   L.offsets = L.slot + ints;
-  L.h = L.offsets + round256(size_t(4) * size_t(E + 1));
+  L.counts = L.offsets + round256(size_t(4) * size_t(E + 1));
+  L.h = L.counts + round256(qpl::expert_plan_bytes(R, E));
   L.out = L.h + round256(size_t(2) * size_t(R) * size_t(H));
   L.ws = L.out + round256(size_t(2) * size_t(R) * size_t(N));
   const size_t w1 = grouped_layout(R, K, E).total, w2 = grouped_layout(R, H, E).total;
@@ -787,17 +788,26 @@ QPL_EXPORT qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, i
   return int8_linear(x, M, K, N, weight, weight_scale, smooth, epi, y, ws, ws_bytes, stream);
 }
 
+QPL_EXPORT size_t expert_plan_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
+  if (check_choices(T, topk) != QPL_OK || E < 1 || E > kMaxExperts) return 0;
+  return qpl::expert_plan_bytes(T * topk, E);
+}
+
 QPL_EXPORT qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E, int32_t* row_index,
-                                  int32_t* slot, int32_t* offsets, void* stream) {
+                                  int32_t* slot, int32_t* offsets, void* ws, size_t ws_bytes, void* stream) {
   if (!expert_ids || !row_index || !slot || !offsets) return QPL_ERR_NULL;
-  if (!aligned16(expert_ids) || !aligned16(row_index) || !aligned16(slot) || !aligned16(offsets)) return QPL_ERR_ALIGN;
+  if (!aligned16(expert_ids) || !aligned16(row_index) || !aligned16(slot) || !aligned16(offsets) || !aligned16(ws))
+    return QPL_ERR_ALIGN;
   qpl_status s = check_choices(T, topk);
   if (s != QPL_OK) return s;
   if (E < 1 || E > kMaxExperts) return QPL_ERR_SHAPE;
+  const size_t need = qpl::expert_plan_bytes(T * topk, E);
+  if (need > 0 && !ws) return QPL_ERR_NULL;
+  if (ws_bytes < need) return QPL_ERR_WORKSPACE;
   if ((s = check_device()) != QPL_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(
-      qpl::launch_expert_plan(expert_ids, T * topk, topk, E, row_index, slot, offsets, st)));
+  return launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(qpl::launch_expert_plan(
+      expert_ids, T * topk, topk, E, row_index, slot, offsets, static_cast<int32_t*>(ws), st)));
 }
 
 QPL_EXPORT size_t qlinear_grouped_int8_workspace_bytes(int64_t R, int64_t K, int64_t N, int64_t E) {
@@ -866,10 +876,11 @@ QPL_EXPORT qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, 
   int32_t* row_index = reinterpret_cast<int32_t*>(base + L.row_index);
   int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot);
   int32_t* offsets = reinterpret_cast<int32_t*>(base + L.offsets);
+  int32_t* counts = reinterpret_cast<int32_t*>(base + L.counts);
   uint16_t* h = reinterpret_cast<uint16_t*>(base + L.h);
   uint16_t* out = reinterpret_cast<uint16_t*>(base + L.out);
   if ((s = launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(
-           qpl::launch_expert_plan(expert_ids, R, topk, E, row_index, slot, offsets, st)))) != QPL_OK)
+           qpl::launch_expert_plan(expert_ids, R, topk, E, row_index, slot, offsets, counts, st)))) != QPL_OK)
     return s;
   qpl::Epilogue gelu, plain;
   gelu.gelu = true;

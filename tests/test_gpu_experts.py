@@ -33,7 +33,9 @@ def choices(T, topk, E, seed=0, kind="random"):
 PLANS = [(1, 1, 1, "random"), (1, 8, 64, "random"), (3, 1, 5, "none"), (7, 3, 4, "invalid"), (63, 2, 9, "skewed"),
          (64, 4, 16, "one"), (85, 3, 300, "random"), (257, 4, 8, "invalid"), (1024, 4, 64, "random"),
          (1025, 4, 64, "skewed"), (4097, 1, 3, "random"), (5000, 7, 33, "invalid"), (16384, 8, 256, "skewed"),
-         (40, 256, 65536, "random"), (20000, 2, 2, "none")]
+         (40, 256, 65536, "random"), (20000, 2, 2, "none"), (8192, 4, 1, "random"), (33000, 1, 1000, "invalid"),
+         (20011, 5, 1024, "skewed"), (32768, 1, 64, "one"), (70001, 3, 1025, "random"), (300000, 2, 100, "invalid"),
+         (600000, 1, 7, "skewed")]
 
 
 @pytest.mark.parametrize("T,topk,E,kind", PLANS)

@@ -63,11 +63,16 @@ def test_linear_refusals(lib):
 
 
 def test_plan_and_combine_refusals(lib):
-    assert lib.expert_plan(None, 4, 2, 3, B, C, D, None) == NULL
-    assert lib.expert_plan(A, 4, 2, 3, B, C, None, None) == NULL
-    assert lib.expert_plan(A, 4, 2, 3, MIS, C, D, None) == ALIGN
+    assert lib.expert_plan(None, 4, 2, 3, B, C, D, None, 0, None) == NULL
+    assert lib.expert_plan(A, 4, 2, 3, B, C, None, None, 0, None) == NULL
+    assert lib.expert_plan(A, 4, 2, 3, MIS, C, D, None, 0, None) == ALIGN
+    assert lib.expert_plan(A, 4, 2, 3, B, C, D, MIS, 0, None) == ALIGN
+    need = qpl.expert_plan_workspace_bytes(1 << 16, 2, 300)
+    assert need > 0 and qpl.expert_plan_workspace_bytes(4, 2, 3) == qpl.expert_plan_workspace_bytes(0, 2, 3) == 0
+    assert lib.expert_plan(A, 1 << 16, 2, 300, B, C, D, None, 0, None) == NULL
+    assert lib.expert_plan(A, 1 << 16, 2, 300, B, C, D, E, need - 1, None) == WORKSPACE
     for T, k, n in ((0, 2, 3), (4, 0, 3), (4, 257, 3), (4, 2, 0), (4, 2, 65537), (PLACES // 2, 2, 3)):
-        assert lib.expert_plan(A, T, k, n, B, C, D, None) == SHAPE, (T, k, n)
+        assert lib.expert_plan(A, T, k, n, B, C, D, E, WS, None) == SHAPE, (T, k, n)
     assert lib.expert_combine(A, 8, 16, B, None, 4, 2, D, None) == NULL
     assert lib.expert_combine(A, 8, 16, MIS, C, 4, 2, D, None) == ALIGN
     for R, N, T, k in ((0, 16, 4, 2), (8, 0, 4, 2), (8, 16, 0, 2), (8, 16, 4, 0), (PLACES, 16, 4, 2), (8, 16, 4, 257)):
@@ -104,7 +109,7 @@ def test_moe_refusals(lib):
 def test_good_calls_reach_the_device_check(lib):
     assert lib.quant_act_int8(A, 4, 16, None, B, C, None) == DEVICE
     assert lib.qlinear_int8(A, 4, 32, 8, B, C, None, D, E, WS, None) == DEVICE
-    assert lib.expert_plan(A, 4, 2, 3, B, C, D, None) == DEVICE
+    assert lib.expert_plan(A, 4, 2, 3, B, C, D, None, 0, None) == DEVICE
     assert lib.expert_combine(A, 8, 16, B, C, 4, 2, D, None) == DEVICE
     assert lib.qlinear_grouped_int8(A, 8, 32, 16, 4, B, C, None, 8, D, 1, E, F, WS, None) == DEVICE
     assert lib.qlinear_moe_int8(A, 4, 32, 16, 8, 4, 2, B, C, A, B, C, D, E, F, WS, None) == DEVICE
