@@ -599,13 +599,27 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     int64_t m0, n0;
     int rows, e;
   };
+  // The tiles of a last round that is at most half (a quarter) full are cut into parts of
+  // XR / 2 (/ 4) rows, one for each workgroup: units [0, full) are whole tiles, the ones behind them parts.
+  const int full = ntiles - ntiles % a.nwg, tail = ntiles - full;
+  const int parts = NJM >= 4 && 4 * tail <= a.nwg ? 4 : NJM >= 2 && 2 * tail <= a.nwg ? 2 : 1;
+  const int units = full + tail * parts;
+  // This workgroup's i-th unit (units: none).  Workgroups are dealt to the 8 XCDs in turn; in
+  // every round, the last and shorter one too, an XCD's workgroups take a contiguous run of units.
   auto position = [&](int i) {
-    return (a.nwg & 7) == 0 ? i * a.nwg + (b & 7) * (a.nwg >> 3) + (b >> 3) : i * a.nwg + b;
+    const int base = i * a.nwg, left = min(units - base, a.nwg);
+    if (left <= 0) return units;
+    const int each = (left + 7) >> 3, at = (b & 7) * each + (b >> 3);
+    if ((a.nwg & 7) != 0) return b < left ? base + b : units;
+    return (b >> 3) < each && at < left ? base + at : units;
   };
   auto tile = [&](int i) {
     Tile t;
     int tm, tn;
-    walk(position(i), tiles_m, a.tiles_n, tm, tn);
+    const int u = position(i);
+    const bool whole = u < full;
+    const int cut = whole ? 0 : (u - full) % parts;
+    walk(whole ? u : full + (u - full) / parts, tiles_m, a.tiles_n, tm, tn);
     t.n0 = (int64_t)tn * WR;
     if constexpr (GROUPED) {
       const RowTile rt = p.tiles[tm];
@@ -617,10 +631,16 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
       t.rows = (int)(p.M - t.m0 < XR ? p.M - t.m0 : XR);
       t.e = 0;
     }
+    if (!whole && parts > 1) {
+      const int first = XR / parts * cut;
+      t.m0 += first;
+      t.rows = min(t.rows - first, XR / parts);
+    }
     return t;
   };
   int nt = 0;
-  while (position(nt) < ntiles) ++nt;
+  while (position(nt) < units) ++nt;
+  if (nt > 0 && tile(nt - 1).rows <= 0) --nt;  // a part behind its tile's last row
 
   // load q of an operand: rows (rows / 4) wv + 8 q .. + 7; lane l fills row + l / 8, stage
   // chunk l % 8, with the row's chunk (l % 8) ^ (l / 8)
@@ -790,7 +810,7 @@ hipError_t launch_staged(const Int8Args& g, int64_t row_tiles, const Epilogue& e
   a.g = g;
   a.tiles_m = (int)row_tiles;
   a.tiles_n = (int)((g.N + 64 * NI - 1) / (64 * NI));
-  const int64_t n = row_tiles * a.tiles_n, most = 256 * staged_per_cu<NI, NJM, S>();
+  const int64_t n = row_tiles * a.tiles_n * NJM, most = 256 * staged_per_cu<NI, NJM, S>();
   a.nwg = (int)(n < most ? n : most);
   const dim3 grid((unsigned)a.nwg), block(256);
   EpiArgs e;
@@ -825,24 +845,25 @@ namespace {
 // time is taken.  The direct kernel's piece is its bytes at 42 KB/us (operand rows that do not
 // exist cost nothing), the staged kernel's was measured for each tile: about 60 KB/us of
 // operands up to 128 x 128, MFMAs and LDS reads above.  Measured, the best shape against the next ones (us):
-//   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 256x128 256x256
+//   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 128x256 256x256
 //   1    4096 4096   5.3   7.0
 //   1    2048 6144   5.7   5.0   5.1   7.5
 //   16   4096 12288  16.9  15.7        14.3
 //   64   4096 4096   13    12.1  10.2  12.4
 //   64   8192 1024   9.6   12.7  16.4  21.1
-//   128  2048 6144                     7.9   9.1    13
-//   512  4096 4096                     18.6  17.6   22.9
-//   1024 4096 4096                           27.2   24.4    30.8
-//   512  4096 12288                                 40.4    33.9    51
-//   4096 4096 12288                                 220     210     183
+//   256  1024 6144                     7.7   6.8    8.0     9.0
+//   515  2080 5003                     18.4  18.8   16.7    19.4
+//   512  4096 12288                                 40.4    35.6    51
+//   1025 4096 4096                           36.3   39.2    32.6
+//   1536 4096 12288                                 104     94.5    95.9
+//   4608 4096 12288                                 258     245     223
 // ---------------------------------------------------------------------------
 struct Shape {
   int rows, cols;
   double piece, tile;
 };
-constexpr Shape kShapes[] = {{16, 16, 0, 0.3},      {16, 32, 0, 0.5},       {32, 32, 0, 0.5},       {64, 64, 0.28, 0.5},
-                             {64, 128, 0.46, 0.8},  {128, 128, 0.62, 2.0},  {256, 128, 0.87, 3.7},  {256, 256, 1.6, 8}};
+constexpr Shape kShapes[] = {{16, 16, 0, 0.25},    {16, 32, 0, 0.5},      {32, 32, 0, 0.5},      {64, 64, 0.28, 0.5},
+                             {64, 128, 0.46, 1.0}, {128, 128, 0.62, 2.0}, {128, 256, 1.0, 3.7}, {256, 256, 1.6, 8}};
 constexpr int kNumShapes = 8;
 
 // tiles_m(rows): row tiles of that height; rows_each: rows that a row tile has at most; part:
@@ -854,7 +875,9 @@ int pick_shape(const F& tiles_m, double rows_each, int64_t K, int64_t N, bool pa
   for (int v = 0; v < kNumShapes; ++v) {
     const Shape& s = kShapes[v];
     const double tiles = tiles_m(s.rows) * (double)((N + s.cols - 1) / s.cols) / 256;
-    const double rounds = part ? (tiles + 0.5 > 1 ? tiles + 0.5 : 1) : __builtin_ceil(tiles);
+    const double left = tiles - __builtin_floor(tiles);  // of the last round; staged tiles are cut in it
+    const double last = left == 0 ? 0 : s.rows >= 256 && left <= 0.25 ? 0.6 : s.rows >= 128 && left <= 0.5 ? 0.8 : 1;
+    const double rounds = part ? (tiles + 0.4 > 1 ? tiles + 0.4 : 1) : tiles - left + last;
     const double piece = s.piece > 0 ? s.piece : ((rows_each < s.rows ? rows_each : s.rows) + s.cols) * 128 / 42e3;
     const double t = rounds * ((double)((K + 127) / 128) * piece + s.tile);
     if (v == 0 || t < least) {
@@ -882,7 +905,7 @@ hipError_t launch_shape(int v, const Int8Args& p, int64_t row_tiles, const Epilo
       // K = 2048 take 13.5 against 15.6 us, 384 of them 24.6 against 19.1 us
       if (row_tiles * ((p.N + 127) / 128) <= 256) return launch_staged<2, 2, 4, GROUPED>(p, row_tiles, ep, y, stream);
       return launch_staged<2, 2, 2, GROUPED>(p, row_tiles, ep, y, stream);
-    case 6: return launch_staged<2, 4, 3, GROUPED>(p, row_tiles, ep, y, stream);
+    case 6: return launch_staged<4, 2, 3, GROUPED>(p, row_tiles, ep, y, stream);
     default: return launch_staged<4, 4, 2, GROUPED>(p, row_tiles, ep, y, stream);
   }
 }
