@@ -316,8 +316,8 @@ qpl_status qlinear_mlp_nvfp4(const uint16_t* x, int64_t M, int64_t K, int64_t H,
  * qlinear_int8: y[m,n] = bf16_rne((sum_k q_x q_w) s_x[m] weight_scale[n]), the sum
  *   exact in int32, with q_x, s_x from quant_act_int8(x, smooth).
  *   weight int8 [N,K], any codes in [-128, 127]; weight_scale float [N]; ws of at
- *   least qlinear_workspace_bytes(QPL_INT8, M, K, N, 0) bytes (its contents after the
- *   call are unspecified: a few rows are quantized inside the product's kernel).
+ *   least qlinear_workspace_bytes(QPL_INT8, M, K, N, 0) bytes, which is 0 for a few rows
+ *   (they are quantized inside the product's kernel; ws may then be NULL).
  * qlinear_int8_ex: the same with an epilogue (see qlinear_fp8r_ex).
  * All pointers 16-byte aligned.  K <= 2^17 for the linears (QPL_ERR_SHAPE beyond).
  */
@@ -369,9 +369,9 @@ qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N,
  *   the experts' outputs are bf16.  ws of at least
  *   qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E).
  *
- * expert_ids, row_index, slot, offsets and weights need 16-byte alignment as all other
- * pointers do.  Errors as for the linears: QPL_ERR_SHAPE for E, topk or a size out
- * of range, QPL_ERR_ARG for an unknown act.
+ * expert_ids, row_index, slot, offsets and the choices' weights need 4-byte alignment
+ * (QPL_ERR_ALIGN), the other pointers 16-byte as usual.  Errors as for the linears:
+ * QPL_ERR_SHAPE for E, topk or a size out of range, QPL_ERR_ARG for an unknown act.
  */
 qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E,
                        int32_t* row_index, int32_t* slot, int32_t* offsets,

@@ -390,18 +390,22 @@ def _queue(stream, dev):
 def _new(shape, dtype, like, stream):
     """A tensor on like's GPU that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _scratch(ws, need, like, dev, stream):
-    """(workspace, its bytes): the caller's, or a new one (need 0: sizes that the call refuses)."""
+    """(workspace, its address, its bytes): the caller's, or a new one if any is needed (need is 0 too
+    for sizes that the call refuses)."""
     if ws is None:
-        return _new((max(need, 1),), torch.uint8, like, stream), max(need, 1)
+        if need == 0:
+            return None, 0, 0
+        ws = _new((need,), torch.uint8, like, stream)
+        return ws, ws.data_ptr(), need
     if not ws.is_contiguous() or ws.get_device() != dev:
         raise ValueError(f"workspace: expected a contiguous tensor on the current GPU ({dev}), got {ws.device}")
-    return ws, ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _act_code(act):
@@ -441,12 +445,12 @@ def qlinear_int8(x, weight, weight_scale, y=None, workspace=None, stream=None, s
     else:
         for t, name in zip(qkv[:3], ("q", "k", "v")):
             _addr(t, torch.bfloat16, _dims(qkv[0], 3, "q"), dev, name)
-    ws, nbytes = _scratch(workspace, qlinear_workspace_bytes(QPL_INT8, M, K, N), x, dev, stream)
+    ws, wa, nbytes = _scratch(workspace, qlinear_workspace_bytes(QPL_INT8, M, K, N), x, dev, stream)
     if act_code == QPL_ACT_NONE and qkv is None:
-        _check("qlinear_int8", load().qlinear_int8(*args, ya, ws.data_ptr(), nbytes, _queue(stream, dev)))
+        _check("qlinear_int8", load().qlinear_int8(*args, ya, wa, nbytes, _queue(stream, dev)))
         return y
     e, _, out = _epilogue(act, qkv, M, N, y, x.device)
-    _check("qlinear_int8_ex", load().qlinear_int8_ex(*args, _ref(e), ya, ws.data_ptr(), nbytes, _queue(stream, dev)))
+    _check("qlinear_int8_ex", load().qlinear_int8_ex(*args, _ref(e), ya, wa, nbytes, _queue(stream, dev)))
     return out
 
 
@@ -467,12 +471,11 @@ def expert_plan(expert_ids, num_experts, row_index=None, slot=None, offsets=None
     row_index = _new((T * topk,), torch.int32, expert_ids, stream) if row_index is None else row_index
     slot = _new((T, topk), torch.int32, expert_ids, stream) if slot is None else slot
     offsets = _new((E + 1,), torch.int32, expert_ids, stream) if offsets is None else offsets
-    need = expert_plan_workspace_bytes(T, topk, E)
-    ws, nbytes = (None, 0) if need == 0 else _scratch(workspace, need, expert_ids, dev, stream)
+    ws, wa, nbytes = _scratch(workspace, expert_plan_workspace_bytes(T, topk, E), expert_ids, dev, stream)
     _check("expert_plan", load().expert_plan(
         _addr(expert_ids, torch.int32, (T, topk), dev, "expert_ids"), T, topk, E,
         _addr(row_index, torch.int32, (T * topk,), dev, "row_index"), _addr(slot, torch.int32, (T, topk), dev, "slot"),
-        _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), _ptr(ws), nbytes, _queue(stream, dev)))
+        _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), wa, nbytes, _queue(stream, dev)))
     return row_index, slot, offsets
 
 
@@ -492,13 +495,13 @@ def qlinear_grouped_int8(x, weight, weight_scale, offsets, row_index=None, y=Non
     R = M if row_index is None else _dims(row_index, 1, "row_index")[0]
     act_code = _act_code(act)
     y = _new((R, N), torch.bfloat16, x, stream) if y is None else y
-    ws, nbytes = _scratch(workspace, qlinear_grouped_int8_workspace_bytes(R, K, N, E), x, dev, stream)
+    ws, wa, nbytes = _scratch(workspace, qlinear_grouped_int8_workspace_bytes(R, K, N, E), x, dev, stream)
     _check("qlinear_grouped_int8", load().qlinear_grouped_int8(
         _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, N, E, _addr(weight, torch.int8, (E, N, K), dev, "weight"),
         _addr(weight_scale, torch.float32, (E, N), dev, "weight_scale"),
         _addr(row_index, torch.int32, (R,), dev, "row_index"), R,
         _addr(offsets, torch.int32, (E + 1,), dev, "offsets"), act_code, _addr(y, torch.bfloat16, (R, N), dev, "y"),
-        ws.data_ptr(), nbytes, _queue(stream, dev)))
+        wa, nbytes, _queue(stream, dev)))
     return y
 
 
@@ -530,7 +533,7 @@ def qlinear_moe_int8(x, expert_ids, expert_weights, fc1, fc2, y=None, workspace=
     dev = _current(x, 2, "x")
     T, K = x.shape
     y = _new((T, N), torch.bfloat16, x, stream) if y is None else y
-    ws, nbytes = _scratch(workspace, qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E), x, dev, stream)
+    ws, wa, nbytes = _scratch(workspace, qlinear_moe_int8_workspace_bytes(T, topk, K, H, N, E), x, dev, stream)
     _check("qlinear_moe_int8", load().qlinear_moe_int8(
         _addr(x, torch.bfloat16, (T, K), dev, "x"), T, K, H, N, E, topk,
         _addr(expert_ids, torch.int32, (T, topk), dev, "expert_ids"),
@@ -539,7 +542,7 @@ def qlinear_moe_int8(x, expert_ids, expert_weights, fc1, fc2, y=None, workspace=
         _addr(fc1["weight_scale"], torch.float32, (E, H), dev, "fc1.weight_scale"),
         _addr(fc2["weight"], torch.int8, (E, N, H), dev, "fc2.weight"),
         _addr(fc2["weight_scale"], torch.float32, (E, N), dev, "fc2.weight_scale"),
-        _addr(y, torch.bfloat16, (T, N), dev, "y"), ws.data_ptr(), nbytes, _queue(stream, dev)))
+        _addr(y, torch.bfloat16, (T, N), dev, "y"), wa, nbytes, _queue(stream, dev)))
     return y
 
 

@@ -83,7 +83,8 @@ size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int64_t rank_pad(int64_t R) { return (R + 31) / 32 * 32; }
 
-// Workspace layout.  fp8r and INT8: [xq: M*K bytes][xs: 4*M bytes].  nvfp4: [xq: M*K/2 packed
+// Workspace layout.  fp8r and INT8: [xq: M*K bytes][xs: 4*M bytes] (nothing for INT8 rows so few
+// that one launch quantizes and multiplies them).  nvfp4: [xq: M*K/2 packed
 // E2M1 codes][xs: 8*M*S block scales slab-major [S, M, 8]], S = ceil(K/128), and, as
 // part 5, [wsl: 8*N*S] the weight's block scales in the same layout.  INT4:
 // [xq: M*K][w8: N*K] (code values as E4M3 bytes) and, as parts 5 and 6, the
@@ -98,6 +99,7 @@ struct Layout {
 Layout layout(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R) {
   Layout L;
   size_t parts[7] = {0, 0, 0, 0, 0, 0, 0};
+  if (scheme == QPL_INT8 && qpl::int8_token_fits(M, K)) return L;
   if (scheme == QPL_FP8R || scheme == QPL_INT8) {
     parts[0] = size_t(M) * size_t(K);
     parts[1] = size_t(4) * size_t(M);
@@ -674,7 +676,7 @@ namespace {
 qpl_status int8_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* weight,
                        const float* weight_scale, const float* smooth, const qpl_epilogue* epi, uint16_t* y, void* ws,
                        size_t ws_bytes, void* stream) {
-  if (!x || !weight || !weight_scale || !ws) return QPL_ERR_NULL;
+  if (!x || !weight || !weight_scale) return QPL_ERR_NULL;
   if (!aligned16(x) || !aligned16(weight) || !aligned16(weight_scale) || !aligned16(y) || !aligned16(ws) ||
       !aligned16(smooth))
     return QPL_ERR_ALIGN;
@@ -684,6 +686,7 @@ qpl_status int8_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const
   qpl::Epilogue ep;
   if ((s = epilogue_of(epi, M, N, y, ep)) != QPL_OK) return s;
   const Layout L = layout(QPL_INT8, M, K, N, 0);
+  if (L.total > 0 && !ws) return QPL_ERR_NULL;
   if (ws_bytes < L.total) return QPL_ERR_WORKSPACE;
   if ((s = check_device()) != QPL_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -712,6 +715,9 @@ qpl_status check_grouped(int64_t R, int64_t K, int64_t N, int64_t E) {
   if (N > kMaxElems / K / E) return QPL_ERR_SHAPE;
   return check_gemm_k(QPL_INT8, R, K, 0);
 }
+
+// Index arrays and the choices' weights are read element by element, so slices of them will do.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 qpl_status check_choices(int64_t T, int64_t topk) {
   if (T < 1 || topk < 1 || topk > kMaxTopk || T >= kMaxPlaces / topk) return QPL_ERR_SHAPE;
@@ -796,7 +802,7 @@ QPL_EXPORT size_t expert_plan_workspace_bytes(int64_t T, int64_t topk, int64_t E
 QPL_EXPORT qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t topk, int64_t E, int32_t* row_index,
                                   int32_t* slot, int32_t* offsets, void* ws, size_t ws_bytes, void* stream) {
   if (!expert_ids || !row_index || !slot || !offsets) return QPL_ERR_NULL;
-  if (!aligned16(expert_ids) || !aligned16(row_index) || !aligned16(slot) || !aligned16(offsets) || !aligned16(ws))
+  if (!aligned4(expert_ids) || !aligned4(row_index) || !aligned4(slot) || !aligned4(offsets) || !aligned16(ws))
     return QPL_ERR_ALIGN;
   qpl_status s = check_choices(T, topk);
   if (s != QPL_OK) return s;
@@ -820,8 +826,8 @@ QPL_EXPORT qpl_status qlinear_grouped_int8(const uint16_t* x, int64_t M, int64_t
                                            int64_t R, const int32_t* offsets, qpl_act act, uint16_t* y, void* ws,
                                            size_t ws_bytes, void* stream) {
   if (!x || !weight || !weight_scale || !offsets || !y || !ws) return QPL_ERR_NULL;
-  if (!aligned16(x) || !aligned16(weight) || !aligned16(weight_scale) || !aligned16(row_index) ||
-      !aligned16(offsets) || !aligned16(y) || !aligned16(ws))
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(weight_scale) || !aligned4(row_index) ||
+      !aligned4(offsets) || !aligned16(y) || !aligned16(ws))
     return QPL_ERR_ALIGN;
   qpl_status s = check_dims(M, K);
   if (s != QPL_OK) return s;
@@ -839,7 +845,7 @@ QPL_EXPORT qpl_status qlinear_grouped_int8(const uint16_t* x, int64_t M, int64_t
 QPL_EXPORT qpl_status expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot,
                                      const float* weights, int64_t T, int64_t topk, uint16_t* out, void* stream) {
   if (!y || !slot || !weights || !out) return QPL_ERR_NULL;
-  if (!aligned16(y) || !aligned16(slot) || !aligned16(weights) || !aligned16(out)) return QPL_ERR_ALIGN;
+  if (!aligned16(y) || !aligned4(slot) || !aligned4(weights) || !aligned16(out)) return QPL_ERR_ALIGN;
   qpl_status s = check_choices(T, topk);
   if (s != QPL_OK) return s;
   if (R < 1 || R >= kMaxPlaces || N < 1 || N >= kMaxDim || R > kMaxElems / N || T > kMaxElems / N)
@@ -862,7 +868,7 @@ QPL_EXPORT qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, 
                                        const float* fc2_scale, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
   if (!x || !expert_ids || !expert_weights || !fc1_weight || !fc1_scale || !fc2_weight || !fc2_scale || !y || !ws)
     return QPL_ERR_NULL;
-  if (!aligned16(x) || !aligned16(expert_ids) || !aligned16(expert_weights) || !aligned16(fc1_weight) ||
+  if (!aligned16(x) || !aligned4(expert_ids) || !aligned4(expert_weights) || !aligned16(fc1_weight) ||
       !aligned16(fc1_scale) || !aligned16(fc2_weight) || !aligned16(fc2_scale) || !aligned16(y) || !aligned16(ws))
     return QPL_ERR_ALIGN;
   qpl_status s = check_moe(T, topk, K, H, N, E);

@@ -167,6 +167,19 @@ def test_moe_is_its_parts(T, topk, E, K, H, N, kind):
         assert not bool(y.any())
 
 
+def test_slices_of_the_choices():
+    """A part of a batch: choices, weights and slots that start at any element."""
+    x, ids, wt, f1, f2 = moe_inputs(23, 3, 5, 64, 32, 40)
+    whole = qpl.qlinear_moe_int8(x, ids, wt, f1, f2)
+    part = qpl.qlinear_moe_int8(x[7:20], ids[7:20], wt[7:20], f1, f2)
+    assert torch.equal(part, whole[7:20])
+    row_index, slot, offsets = qpl.expert_plan(ids[7:20], 5)
+    assert np.array_equal(host(slot), plan_ref(host(ids)[7:20], 5)[1])
+    y = torch.randn((69, 40), device="cuda").to(torch.bfloat16)
+    out = qpl.expert_combine(y, ids[7:20], wt[7:20])
+    assert torch.equal(out, qpl.expert_combine(y, ids[7:20].clone(), wt[7:20].clone()))
+
+
 def test_moe_against_the_oracle():
     """One token at a time in 64 bits from the GPU's own h, so that no code of h is open."""
     T, topk, E, K, H, N = 20, 3, 5, 96, 64, 56
