@@ -456,7 +456,7 @@ typedef enum {
   QPL_KERNEL_QUANT_INT8 = 18,       /* quant_act_int8, and the quantize inside the 8-bit integer linears */
   QPL_KERNEL_GEMM_INT8 = 19,
   QPL_KERNEL_GEMM_INT8_GROUPED = 20,
-  QPL_KERNEL_EXPERT_PLAN = 21,
+  QPL_KERNEL_EXPERT_PLAN = 21,       /* expert_plan; in qlinear_moe_int8 with few choices also fc1's quantize */
   QPL_KERNEL_EXPERT_COMBINE = 22,
   QPL_KERNEL_COUNT = 23
 } qpl_kernel;

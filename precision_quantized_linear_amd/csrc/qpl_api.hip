@@ -737,19 +737,36 @@ GroupedLayout grouped_layout(int64_t R, int64_t K, int64_t E) {
   return L;
 }
 
+// The parts of that workspace.
+struct GroupedOperands {
+  int8_t* xq;
+  float* xs;
+  int32_t* tiles;
+};
+
+GroupedOperands grouped_operands(uint8_t* ws, int64_t R, int64_t K, int64_t E) {
+  const GroupedLayout L = grouped_layout(R, K, E);
+  return {reinterpret_cast<int8_t*>(ws), reinterpret_cast<float*>(ws + L.xs),
+          reinterpret_cast<int32_t*>(ws + L.tiles)};
+}
+
+// A grouped product whose quantized rows and row tiles are in the workspace.
+qpl_status grouped_product(const GroupedOperands& q, int64_t K, int64_t N, int64_t E, const int8_t* weight,
+                           const float* weight_scale, int64_t R, const qpl::Epilogue& ep, uint16_t* y,
+                           hipStream_t st) {
+  return launched(Timed(QPL_KERNEL_GEMM_INT8_GROUPED, st)(
+      qpl::launch_gemm_int8_grouped(q.xq, q.xs, weight, weight_scale, R, K, N, E, q.tiles, ep, y, st)));
+}
+
 // The two launches of a grouped product, arguments checked.
 qpl_status grouped_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, int64_t E, const int8_t* weight,
                           const float* weight_scale, const int32_t* row_index, int64_t R, const int32_t* offsets,
                           const qpl::Epilogue& ep, uint16_t* y, uint8_t* ws, hipStream_t st) {
-  const GroupedLayout L = grouped_layout(R, K, E);
-  int8_t* xq = reinterpret_cast<int8_t*>(ws);
-  float* xs = reinterpret_cast<float*>(ws + L.xs);
-  int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+  const GroupedOperands q = grouped_operands(ws, R, K, E);
   const qpl_status s = launched(Timed(QPL_KERNEL_QUANT_INT8, st)(
-      qpl::launch_quant_int8_grouped(x, M, R, K, N, row_index, offsets, E, xq, xs, tiles, st)));
+      qpl::launch_quant_int8_grouped(x, M, R, K, N, row_index, offsets, E, q.xq, q.xs, q.tiles, st)));
   if (s != QPL_OK) return s;
-  return launched(Timed(QPL_KERNEL_GEMM_INT8_GROUPED, st)(
-      qpl::launch_gemm_int8_grouped(xq, xs, weight, weight_scale, R, K, N, E, tiles, ep, y, st)));
+  return grouped_product(q, K, N, E, weight, weight_scale, R, ep, y, st);
 }
 
 // Workspace of the MLP of experts: the arrays of the plan, h, the experts' outputs, and the
@@ -885,14 +902,22 @@ QPL_EXPORT qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, 
   int32_t* counts = reinterpret_cast<int32_t*>(base + L.counts);
   uint16_t* h = reinterpret_cast<uint16_t*>(base + L.h);
   uint16_t* out = reinterpret_cast<uint16_t*>(base + L.out);
-  if ((s = launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(
-           qpl::launch_expert_plan(expert_ids, R, topk, E, row_index, slot, offsets, counts, st)))) != QPL_OK)
-    return s;
   qpl::Epilogue gelu, plain;
   gelu.gelu = true;
-  if ((s = grouped_linear(x, T, K, H, E, fc1_weight, fc1_scale, row_index, R, offsets, gelu, h, base + L.ws, st)) !=
-      QPL_OK)
-    return s;
+  if (qpl::moe_front_fits(R, E)) {
+    const GroupedOperands q = grouped_operands(base + L.ws, R, K, E);
+    if ((s = launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(qpl::launch_int8_moe_front(
+             expert_ids, R, topk, x, K, H, E, q.xq, q.xs, slot, offsets, q.tiles, st)))) != QPL_OK)
+      return s;
+    if ((s = grouped_product(q, K, H, E, fc1_weight, fc1_scale, R, gelu, h, st)) != QPL_OK) return s;
+  } else {
+    if ((s = launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(
+             qpl::launch_expert_plan(expert_ids, R, topk, E, row_index, slot, offsets, counts, st)))) != QPL_OK)
+      return s;
+    if ((s = grouped_linear(x, T, K, H, E, fc1_weight, fc1_scale, row_index, R, offsets, gelu, h, base + L.ws, st)) !=
+        QPL_OK)
+      return s;
+  }
   if ((s = grouped_linear(h, R, H, N, E, fc2_weight, fc2_scale, nullptr, R, offsets, plain, out, base + L.ws, st)) !=
       QPL_OK)
     return s;

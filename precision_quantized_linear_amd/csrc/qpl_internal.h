@@ -134,6 +134,12 @@ int64_t grouped_row_tiles(int64_t R, int64_t E);
 hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, int64_t N,
                                      const int32_t* row_index, const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
                                      hipStream_t stream);
+// Plan (slot, offsets) and quantizer of a grouped product with few choices ids [n] in one launch
+// (moe_front_fits): row p is the token x[i / topk] of the choice i whose place is p.
+bool moe_front_fits(int64_t n, int64_t E);
+hipError_t launch_int8_moe_front(const int32_t* ids, int64_t n, int64_t topk, const uint16_t* x, int64_t K, int64_t N,
+                                 int64_t E, int8_t* xq, float* xs, int32_t* slot, int32_t* offsets, int32_t* tiles,
+                                 hipStream_t stream);
 hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t R,
                                     int64_t K, int64_t N, int64_t E, const int32_t* tiles, const Epilogue& ep,
                                     uint16_t* y, hipStream_t stream);

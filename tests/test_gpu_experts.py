@@ -155,7 +155,8 @@ def composed(x, ids, wt, f1, f2):
 
 MOES = [(1, 1, 1, 16, 16, 1, "random"), (1, 2, 8, 128, 64, 40, "random"), (7, 4, 16, 256, 96, 136, "random"),
         (50, 2, 4, 144, 80, 33, "invalid"), (33, 3, 6, 64, 48, 24, "none"), (300, 4, 8, 256, 176, 264, "skewed"),
-        (900, 2, 3, 128, 512, 96, "one")]
+        (900, 2, 3, 128, 512, 96, "one"), (128, 8, 1024, 64, 48, 16, "invalid"), (1024, 1, 7, 528, 32, 20, "skewed"),
+        (64, 16, 1000, 2064, 16, 8, "random"), (205, 5, 4, 96, 32, 24, "skewed")]
 
 
 @pytest.mark.parametrize("T,topk,E,K,H,N,kind", MOES)
