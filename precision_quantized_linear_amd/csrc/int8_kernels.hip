@@ -487,33 +487,36 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
 
 // ---------------------------------------------------------------------------
 // A few rows (single tokens) in one launch: as the direct kernel, but every workgroup quantizes
-// the M <= 4 rows itself, into LDS, while its first weight bytes are on their way.  The
-// quantizer's launch and the wait for it cost more than the repeated work: at 1 x 4096 x 4096 the two
-// launches take 6.1 + 5.5 us.
-// SLOTS vectors of 8 elements per thread: row and part of a row.
+// the M <= 16 rows itself, into LDS, while its first weight bytes are on their way.  The
+// quantizer's launch and the wait for it cost more than the repeated work: 1 x 4096 x 4096 takes
+// 6.2 us, the two launches 6.1 + 5.5 us.
+// A row is parts of 64 vectors of 8 elements; wavefront w takes the parts w, w + 16, ... of all
+// rows, up to TOKEN_SLOTS of them.
 // ---------------------------------------------------------------------------
-constexpr int TOKEN_W = 16, TOKEN_SLOTS = 4, TOKEN_BYTES = TOKEN_SLOTS * 64 * TOKEN_W * 8;
+constexpr int TOKEN_W = 16, TOKEN_SLOTS = 2, TOKEN_PARTS = TOKEN_W * TOKEN_SLOTS, TOKEN_BYTES = TOKEN_PARTS * 512;
 
-template <int NT, bool SMOOTH, int EPI>
+template <bool SMOOTH, int EPI>
 __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __restrict__ x,
                                                              const float* __restrict__ lam, Int8Args p,
                                                              uint16_t* __restrict__ Y, EpiArgs e) {
   constexpr int W = TOKEN_W, U = 2;
   __shared__ __attribute__((aligned(16))) uint8_t codes[TOKEN_BYTES];  // [M, K]
-  __shared__ i32x4 red[W][NT][64];
-  __shared__ float part[TOKEN_SLOTS][W];
-  __shared__ float scale[TOKEN_SLOTS];
+  __shared__ i32x4 red[W][64];
+  __shared__ float part[TOKEN_PARTS];
+  __shared__ float scale[16];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r16 = lane & 15, q = lane >> 4;
   const int M = (int)p.M, nv = p.K >> 3;
-  const int parts = (nv + 64 * W - 1) / (64 * W);  // slots per row
+  const int parts = (nv + 63) >> 6;  // of a row
+  // part / parts by a reciprocal, exact for the numbers up to 32 that occur
+  const int rcp = (65536 + parts - 1) / parts;
   const int pieces = (p.K + 127) >> 7;
-  int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
+  int64_t n0 = (int64_t)blockIdx.x * 16;
   __amdgpu_buffer_rsrc_t dw;
-  i32x4 fw[U][2][NT];
+  i32x4 fw[U][2];
   auto rows_of = [&](int64_t n) {
-    const int64_t nr = p.N - n < 16 * NT ? p.N - n : 16 * NT;
+    const int64_t nr = p.N - n < 16 ? p.N - n : 16;
     dw = make_rsrc(p.w + n * p.K, nr * p.K);
   };
   auto load_w = [&](int c) {
@@ -522,56 +525,37 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __r
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int k = (c + u * W) * 128 + 64 * s + 16 * q;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          fw[u][s][j] = load16(dw, k < p.K ? (uint32_t)((16 * j + r16) * p.K + k) : kOutOfRange);
+        fw[u][s] = load16(dw, k < p.K ? (uint32_t)(r16 * p.K + k) : kOutOfRange);
       }
   };
   // the rows' vectors, then (behind them, so that they do not wait for it) the first weight bytes
   u32x4 v[TOKEN_SLOTS];
-  int row = 0, sub = 0;
 #pragma unroll
   for (int t = 0; t < TOKEN_SLOTS; ++t) {
-    const int j = sub * 64 * W + (int)threadIdx.x;
+    const int u = wv + W * t, row = (u * rcp) >> 16, j = (u - row * parts) * 64 + lane;
     const bool in = row < M && j < nv;
     v[t] = in ? reinterpret_cast<const u32x4*>(x + (int64_t)row * p.K)[j] : u32x4{0u, 0u, 0u, 0u};
     if (SMOOTH && in) v[t] = smooth_vec(v[t], lam + 8 * (int64_t)j);
-    if (++sub == parts) {
-      sub = 0;
-      ++row;
-    }
   }
   rows_of(n0);
   load_w(wv);
 #pragma unroll
   for (int t = 0; t < TOKEN_SLOTS; ++t) {
     const float a = wave_max(absmax_value(vec_absmax8(v[t], 0u)));
-    if (lane == 0) part[t][wv] = a;
+    if (lane == 0) part[wv + W * t] = a;
   }
   __syncthreads();
-  row = 0;
-  sub = 0;
 #pragma unroll
   for (int t = 0; t < TOKEN_SLOTS; ++t) {
-    const int j = sub * 64 * W + (int)threadIdx.x;
+    const int u = wv + W * t, row = (u * rcp) >> 16, sub = u - row * parts, j = sub * 64 + lane;
     if (row >= M) break;
-    float a = 0.0f;
-    for (int i = row * parts; i < (row + 1) * parts; ++i) a = fmaxf(a, part[i][r16]);
-#pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) a = fmaxf(a, __shfl_xor(a, d, 64));
-    const RowCode rc = row_code(a);
-    if (threadIdx.x == 0) scale[row] = rc.s;
+    const RowCode rc = row_code(wave_max(lane < parts ? part[row * parts + lane] : 0.0f));
+    if (sub == 0 && lane == 0) scale[row] = rc.s;
     if (j < nv) reinterpret_cast<u32x2*>(codes + row * p.K)[j] = code_vec(v[t], rc);
-    if (++sub == parts) {
-      sub = 0;
-      ++row;
-    }
   }
   __syncthreads();
   for (;;) {
-    i32x4 acc[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = i32x4{0, 0, 0, 0};
+    i32x4 acc{0, 0, 0, 0};
     for (int c = wv; c < pieces; c += W * U) {
       if (c != wv) load_w(c);
 #pragma unroll
@@ -581,29 +565,28 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __r
           const int k = (c + u * W) * 128 + 64 * s + 16 * q;
           i32x4 fx{0, 0, 0, 0};
           if (r16 < M && k < p.K) fx = *reinterpret_cast<const i32x4*>(codes + r16 * p.K + k);
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx, acc[j], 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s], fx, acc, 0, 0, 0);
         }
     }
     asm volatile("s_nop 15" ::: "memory");  // as behind the direct kernel's loop
-#pragma unroll
-    for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[j]));
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[wv][j][lane] = acc[j];
-    __syncthreads();
-    if ((int)threadIdx.x < NT * 64) {
-      const int j = threadIdx.x >> 6;
-      i32x4 sum = red[0][j][lane];
-#pragma unroll
-      for (int k = 1; k < W; ++k) sum += red[k][j][lane];
-      store_four<EPI>(Y, r16, M, n0 + 16 * j + 4 * q, p.N, sum, r16 < M ? scale[r16] : 0.0f, p.ws, e);
+    asm volatile("" : "+v"(acc));
+    red[wv][lane] = acc;
+    // the next columns' first weight bytes
+    const int64_t next = n0 + (int64_t)gridDim.x * 16;
+    if (next < p.N) {
+      rows_of(next);
+      load_w(wv);
     }
-    n0 += (int64_t)gridDim.x * 16 * NT;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      i32x4 sum = red[0][lane];
+#pragma unroll
+      for (int k = 1; k < W; ++k) sum += red[k][lane];
+      store_four<EPI>(Y, r16, M, n0 + 4 * q, p.N, sum, r16 < M ? scale[r16] : 0.0f, p.ws, e);
+    }
+    n0 = next;
     if (n0 >= p.N) break;
     __syncthreads();
-    rows_of(n0);
-    load_w(wv);
   }
 }
 
@@ -990,19 +973,21 @@ hipError_t launch_shape(int v, const Int8Args& p, int64_t row_tiles, const Epilo
 
 namespace {
 
-template <int NT, bool SMOOTH>
+template <bool SMOOTH>
 hipError_t launch_token(const uint16_t* x, const float* lam, const Int8Args& p, const Epilogue& ep, uint16_t* y,
                         hipStream_t stream) {
-  const int64_t n = (p.N + 16 * NT - 1) / (16 * NT);
-  const dim3 grid((unsigned)(n < kDirectColumns ? n : kDirectColumns)), block(64 * TOKEN_W);
+  // one workgroup per CU at most, which quantizes once and takes 16 columns in each of its turns
+  // (1 x 4096 x 12288: 13.2 us, 16.4 us with a workgroup for every 16 or 32 columns)
+  const int64_t n = (p.N + 15) / 16;
+  const dim3 grid((unsigned)(n < 256 ? n : 256)), block(64 * TOKEN_W);
   EpiArgs e;
   switch (epi_kind(ep, e)) {
-    case 0: hipLaunchKernelGGL((k_int8_token<NT, SMOOTH, 0>), grid, block, 0, stream, x, lam, p, y, e); break;
+    case 0: hipLaunchKernelGGL((k_int8_token<SMOOTH, 0>), grid, block, 0, stream, x, lam, p, y, e); break;
     case EPI_GELU:
-      hipLaunchKernelGGL((k_int8_token<NT, SMOOTH, EPI_GELU>), grid, block, 0, stream, x, lam, p, y, e);
+      hipLaunchKernelGGL((k_int8_token<SMOOTH, EPI_GELU>), grid, block, 0, stream, x, lam, p, y, e);
       break;
     case EPI_QKV:
-      hipLaunchKernelGGL((k_int8_token<NT, SMOOTH, EPI_QKV>), grid, block, 0, stream, x, lam, p, y, e);
+      hipLaunchKernelGGL((k_int8_token<SMOOTH, EPI_QKV>), grid, block, 0, stream, x, lam, p, y, e);
       break;
     default: return hipErrorInvalidValue;
   }
@@ -1011,9 +996,9 @@ hipError_t launch_token(const uint16_t* x, const float* lam, const Int8Args& p, 
 
 }  // namespace
 
-bool int8_token_fits(int64_t M, int64_t K) {
-  return M <= TOKEN_SLOTS && M * ((K / 8 + 64 * TOKEN_W - 1) / (64 * TOKEN_W)) <= TOKEN_SLOTS;
-}
+// Half as many elements again would lose: with four parts per wavefront 16 x 2048 x 6144 took 10.6 us,
+// its two launches 8.3 us; with two, 16 x 1024 x 4096 takes 6.1 us either way.
+bool int8_token_fits(int64_t M, int64_t K) { return M <= 16 && M * ((K / 8 + 63) / 64) <= TOKEN_PARTS; }
 
 hipError_t launch_int8_token(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* w, const float* ws,
                              const float* lam, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
@@ -1023,10 +1008,7 @@ hipError_t launch_int8_token(const uint16_t* x, int64_t M, int64_t K, int64_t N,
   p.M = M;
   p.N = N;
   p.K = (int)K;
-  // 32 columns per workgroup where 16 would need more than two workgroups per CU
-  if (N > 512 * 16)
-    return lam ? launch_token<2, true>(x, lam, p, ep, y, stream) : launch_token<2, false>(x, lam, p, ep, y, stream);
-  return lam ? launch_token<1, true>(x, lam, p, ep, y, stream) : launch_token<1, false>(x, lam, p, ep, y, stream);
+  return lam ? launch_token<true>(x, lam, p, ep, y, stream) : launch_token<false>(x, lam, p, ep, y, stream);
 }
 
 hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,

@@ -68,7 +68,9 @@ def test_quantizer_ignores_rows_around_a_view():
 # ---- linear ---------------------------------------------------------------------------
 SHAPES = [(1, 16, 1), (1, 4096, 257), (2, 48, 16), (15, 80, 33), (16, 128, 64), (17, 144, 63), (31, 2064, 100),
           (33, 64, 8), (64, 400, 65), (65, 272, 1000), (127, 1040, 129), (129, 128, 256), (255, 512, 300),
-          (1, 32768, 100), (2, 16384, 530), (4, 8192, 48), (4, 8208, 33), (3, 2000, 20000), (1, 32784, 9), (5, 64, 70),
+          (1, 32768, 100), (2, 16384, 530), (4, 8192, 48), (4, 8208, 33), (3, 2000, 20000), (1, 32784, 9), (5, 64, 70), (16, 2048, 300),
+          (16, 2064, 50), (8, 4096, 70), (9, 3600, 40), (13, 1008, 8200), (11, 2560, 77),
+          (1, 16384, 90), (1, 16400, 90), (16, 1024, 4100), (16, 1040, 64), (4, 4096, 20000), (5, 3120, 40), (7, 2048, 30),
           (300, 192, 513), (513, 336, 264), (1025, 1200, 1032), (2100, 256, 2050), (4500, 96, 5000), (3, 131072, 20),
           (260, 20000, 40)]
 
@@ -93,7 +95,7 @@ def test_largest_sums_stay_exact():
     assert np.array_equal(bf16_bits(y), qlinear_int8_bits(xq, xs, w, ws))
 
 
-@pytest.mark.parametrize("M", [1, 4, 40, 300, 1100])
+@pytest.mark.parametrize("M", [1, 4, 16, 40, 300, 1100])
 def test_linear_smoothed_and_gelu(M):
     K, N = 512, 1030
     x, w, ws = operands(M, K, N, seed=M)

@@ -55,8 +55,8 @@ def test_linear_refusals(lib):
     assert lib.qlinear_int8(A, 4, 32, 8, B, C, MIS, D, E, WS, None) == ALIGN
     assert lib.qlinear_int8(A, 4, 32, 0, B, C, None, D, E, WS, None) == SHAPE
     assert lib.qlinear_int8(A, 4, KMAX + 16, 8, B, C, None, D, E, WS, None) == SHAPE
-    assert lib.qlinear_int8(A, 8, 32, 8, B, C, None, D, E, 256, None) == WORKSPACE
-    assert lib.qlinear_int8(A, 8, 32, 8, B, C, None, D, None, 0, None) == NULL
+    assert lib.qlinear_int8(A, 20, 32, 8, B, C, None, D, E, 256, None) == WORKSPACE
+    assert lib.qlinear_int8(A, 20, 32, 8, B, C, None, D, None, 0, None) == NULL
     assert lib.qlinear_int8(A, 4, 32, 8, B, C, None, D, MIS, 0, None) == ALIGN
     e = qpl.Epilogue()
     e.act = 7
