@@ -75,17 +75,17 @@ __device__ __forceinline__ u32x4 smooth_vec(const u32x4& v, const float* __restr
                smooth_pair(v.w, b[2], b[3])};
 }
 
-// Codes and scale of the row at `src` (nullptr: a row of zeros) into row `row`.  REUSED: other rows
+// Codes and scale of the row at `src` (nullptr: a row of zeros) into row `row`, `pitch` codes apart.  REUSED: other rows
 // are made of the same source, which should stay in the caches.  SPLIT: the workgroup's four
 // wavefronts share the row.
 template <int VPT, bool SMOOTH, bool REUSED, bool SPLIT>
-__device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int64_t row, int64_t K,
+__device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int64_t row, int64_t K, int64_t pitch,
                                           const float* __restrict__ lam, int8_t* __restrict__ xq,
                                           float* __restrict__ xs) {
   constexpr int STEP = SPLIT ? 256 : 64;
   const int first = SPLIT ? threadIdx.x : threadIdx.x & 63;
   const int64_t nv = K >> 3;
-  u32x2* qr = reinterpret_cast<u32x2*>(xq + row * K);
+  u32x2* qr = reinterpret_cast<u32x2*>(xq + row * pitch);
   if (REUSED && !src) {
     for (int64_t j = first; j < nv; j += STEP) qr[j] = u32x2{0u, 0u};
     if (first == 0) xs[row] = 0.0f;
@@ -185,7 +185,7 @@ struct TilePlan {
 // zeros for an index outside x).
 template <int VPT, bool SMOOTH, bool GROUPED, bool GATHER, bool SPLIT>
 __global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__ x, int64_t rows_x, int64_t rows,
-                                                    int64_t K, const float* __restrict__ lam,
+                                                    int64_t K, int64_t pitch, const float* __restrict__ lam,
                                                     const int* __restrict__ row_index, int8_t* __restrict__ xq,
                                                     float* __restrict__ xs, TilePlan plan) {
   int64_t blk = blockIdx.x, nblk = gridDim.x;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__
       from = row_index[row];
       if (from >= rows_x) from = -1;
     }
-    quant_row<VPT, SMOOTH, GATHER, SPLIT>(from < 0 ? nullptr : x + from * K, row, K, lam, xq, xs);
+    quant_row<VPT, SMOOTH, GATHER, SPLIT>(from < 0 ? nullptr : x + from * K, row, K, pitch, lam, xq, xs);
   }
 }
 
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__
 constexpr int FRONT_N = 1024, FRONT_E = 1024;
 
 __global__ __launch_bounds__(256) void k_int8_moe_front(const int* __restrict__ ids, int n, int topk,
-                                                        const uint16_t* __restrict__ x, int64_t K,
+                                                        const uint16_t* __restrict__ x, int64_t K, int64_t pitch,
                                                         int8_t* __restrict__ xq, float* __restrict__ xs,
                                                         int* __restrict__ slot, int* __restrict__ offsets,
                                                         TilePlan plan) {
@@ -277,13 +277,13 @@ __global__ __launch_bounds__(256) void k_int8_moe_front(const int* __restrict__ 
   __syncthreads();
   const int place = below[0] + below[1] + below[2] + below[3];
   if (threadIdx.x == 0) slot[i] = place;
-  quant_row<0, false, true, true>(x + (int64_t)(i / topk) * K, place, K, nullptr, xq, xs);
+  quant_row<0, false, true, true>(x + (int64_t)(i / topk) * K, place, K, pitch, nullptr, xq, xs);
 }
 
 constexpr int64_t kQuantBlocks = int64_t(1) << 22;  // workgroups stride over rows past this many
 
 template <bool SMOOTH, bool GROUPED, bool GATHER, bool SPLIT>
-hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, const float* lam,
+hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, int64_t pitch, const float* lam,
                              const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
   const int64_t per_lane = SPLIT ? (K / 8 + 255) / 256 : (K / 8 + 63) / 64;
   const int64_t blocks = SPLIT ? rows : (rows + 3) / 4;
@@ -291,7 +291,7 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, in
 #define QPL_CASE(V)                                                                                                   \
   if (per_lane <= V || V == 0) {                                                                                      \
     hipLaunchKernelGGL((k_quant_int8<V, SMOOTH, GROUPED, GATHER, SPLIT>), grid, block, 0, stream, x, rows_x, rows, K, \
-                       lam, row_index, xq, xs, plan);                                                                 \
+                       pitch, lam, row_index, xq, xs, plan);                                                                 \
     return hipGetLastError();                                                                                         \
   }
   if constexpr (SPLIT) {
@@ -307,11 +307,11 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, in
 constexpr int64_t kSplitRows = 2048;
 
 template <bool SMOOTH, bool GROUPED, bool GATHER>
-hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, const float* lam,
+hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, int64_t pitch, const float* lam,
                         const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
   return rows <= kSplitRows && K > 512
-             ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(x, rows_x, rows, K, lam, row_index, xq, xs, plan, stream)
-             : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(x, rows_x, rows, K, lam, row_index, xq, xs, plan,
+             ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream)
+             : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan,
                                                                  stream);
 }
 
@@ -327,12 +327,12 @@ hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t
 // row's, or zeros past the weight's end) irrelevant.
 // ---------------------------------------------------------------------------
 struct Int8Args {
-  const int8_t* x;  // [rows, K]
+  const int8_t* x;  // [rows, K], px apart
   const int8_t* w;  // [N, K], or [E, N, K]
   const float* xs;
   const float* ws;  // [N], or [E, N]
   int64_t M, N;
-  int K;
+  int K, px;
   int64_t tiles_m, tiles_n;
   const int* count;      // grouped: number of row tiles
   const RowTile* tiles;  // grouped: the row tiles
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
       m1 = p.M - m0 < 16 * MT ? p.M : m0 + 16 * MT;
     }
     const int64_t nr = p.N - n0 < 16 * NT ? p.N - n0 : 16 * NT;
-    const __amdgpu_buffer_rsrc_t dx = make_rsrc(p.x + m0 * p.K, (m1 - m0) * p.K);
+    const __amdgpu_buffer_rsrc_t dx = make_rsrc(p.x + m0 * p.px, (m1 - m0) * p.px);
     const __amdgpu_buffer_rsrc_t dw = make_rsrc(w + n0 * p.K, nr * p.K);
     i32x4 acc[MT][NT];
 #pragma unroll
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
             fw[u][s][j] = load16(dw, in ? (uint32_t)((16 * j + r16) * p.K + k) : kOutOfRange);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
-            fx[u][s][i] = load16(dx, in ? (uint32_t)((16 * i + r16) * p.K + k) : kOutOfRange);
+            fx[u][s][i] = load16(dx, in ? (uint32_t)((16 * i + r16) * p.px + k) : kOutOfRange);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -704,7 +704,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   // load q of an operand: rows (rows / 4) wv + 8 q .. + 7; lane l fills row + l / 8, stage
   // chunk l % 8, with the row's chunk (l % 8) ^ (l / 8)
   const int lc = (lane & 7) ^ (lane >> 3);
-  const uint32_t vx = (uint32_t)((XR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
+  const uint32_t vx = (uint32_t)((XR / 4 * wv + (lane >> 3)) * p.px + 16 * lc);
   const uint32_t vw = (uint32_t)((WR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
 
   // The stream of pieces: the descriptors change where it enters a tile, from piece to
@@ -718,7 +718,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   auto enter = [&](int i) {
     const Tile t = tile(i);
     const int rn = (int)(p.N - t.n0 < WR ? p.N - t.n0 : WR);
-    dx = make_desc(p.x + t.m0 * p.K, (int64_t)t.rows * p.K);
+    dx = make_desc(p.x + t.m0 * p.px, (int64_t)t.rows * p.px);
     dw = make_desc(p.w + ((int64_t)t.e * p.N + t.n0) * p.K, (int64_t)rn * p.K);
     const bool row = wv < 2;
     ds = make_desc(row ? p.xs + t.m0 : p.ws + (int64_t)t.e * p.N + t.n0, (row ? t.rows : rn) * 4);
@@ -744,7 +744,7 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     const bool in = s.valid && s.koff + 16 * lc < p.K;
     const int q = d < XL ? d : d - XL;
     const uint32_t dst = lbase + s.stage * STAGE + (d < XL ? XR / 4 * wv + 8 * q : XR + WR / 4 * wv + 8 * q) * PR_ROW;
-    const uint32_t vo = in ? (d < XL ? vx : vw) + (uint32_t)(8 * q * p.K) : kOutOfRange;
+    const uint32_t vo = in ? (d < XL ? vx : vw) + (uint32_t)(8 * q * (d < XL ? p.px : p.K)) : kOutOfRange;
     dma16(dst, vo, d < XL ? dx : dw, s.koff);
   };
   // the tile's output scales, 64 per load: wavefronts 0 and 1 those of x, 2 and 3 those of W; every
@@ -888,11 +888,11 @@ hipError_t launch_staged(const Int8Args& g, int64_t row_tiles, const Epilogue& e
 
 }  // namespace
 
-hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const float* lam, int8_t* xq, float* xs,
-                             hipStream_t stream) {
+hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, int64_t pitch, const float* lam, int8_t* xq,
+                             float* xs, hipStream_t stream) {
   const TilePlan none{};
-  return lam ? launch_quant<true, false, false>(x, M, M, K, lam, nullptr, xq, xs, none, stream)
-             : launch_quant<false, false, false>(x, M, M, K, nullptr, nullptr, xq, xs, none, stream);
+  return lam ? launch_quant<true, false, false>(x, M, M, K, pitch, lam, nullptr, xq, xs, none, stream)
+             : launch_quant<false, false, false>(x, M, M, K, pitch, nullptr, nullptr, xq, xs, none, stream);
 }
 
 namespace {
@@ -1021,6 +1021,7 @@ hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, 
   p.M = M;
   p.N = N;
   p.K = (int)K;
+  p.px = (int)int8_pitch(K);
   const int v = pick_shape([&](int rows) { return (double)((M + rows - 1) / rows); }, (double)M, K, N, false);
   return launch_shape<false>(v, p, (M + kShapes[v].rows - 1) / kShapes[v].rows, ep, y, stream);
 }
@@ -1060,8 +1061,8 @@ hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t 
                                      const int32_t* row_index, const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
                                      hipStream_t stream) {
   const TilePlan t = tile_plan(offsets, R, K, N, E, tiles);
-  return row_index ? launch_quant<false, true, true>(x, rows_x, R, K, nullptr, row_index, xq, xs, t, stream)
-                   : launch_quant<false, true, false>(x, rows_x, R, K, nullptr, nullptr, xq, xs, t, stream);
+  return row_index ? launch_quant<false, true, true>(x, rows_x, R, K, int8_pitch(K), nullptr, row_index, xq, xs, t, stream)
+                   : launch_quant<false, true, false>(x, rows_x, R, K, int8_pitch(K), nullptr, nullptr, xq, xs, t, stream);
 }
 
 bool moe_front_fits(int64_t n, int64_t E) { return n <= FRONT_N && E <= FRONT_E; }
@@ -1070,8 +1071,8 @@ hipError_t launch_int8_moe_front(const int32_t* ids, int64_t n, int64_t topk, co
                                  int64_t E, int8_t* xq, float* xs, int32_t* slot, int32_t* offsets, int32_t* tiles,
                                  hipStream_t stream) {
   const TilePlan t = tile_plan(offsets, n, K, N, E, tiles);
-  hipLaunchKernelGGL(k_int8_moe_front, dim3((unsigned)(n + 1)), dim3(256), 0, stream, ids, (int)n, (int)topk, x, K, xq,
-                     xs, slot, offsets, t);
+  hipLaunchKernelGGL(k_int8_moe_front, dim3((unsigned)(n + 1)), dim3(256), 0, stream, ids, (int)n, (int)topk, x, K,
+                     int8_pitch(K), xq, xs, slot, offsets, t);
   return hipGetLastError();
 }
 
@@ -1086,6 +1087,7 @@ hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int
   p.M = R;
   p.N = N;
   p.K = (int)K;
+  p.px = (int)int8_pitch(K);
   p.count = tiles;
   p.tiles = reinterpret_cast<const RowTile*>(tiles) + 1;
   const int v = grouped_shape(R, K, N, E);

@@ -83,8 +83,8 @@ size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int64_t rank_pad(int64_t R) { return (R + 31) / 32 * 32; }
 
-// Workspace layout.  fp8r and INT8: [xq: M*K bytes][xs: 4*M bytes] (nothing for INT8 rows so few
-// that one launch quantizes and multiplies them).  nvfp4: [xq: M*K/2 packed
+// Workspace layout.  fp8r and INT8: [xq: M*K bytes (INT8: rows int8_pitch(K) apart)][xs: 4*M bytes]
+// (nothing for INT8 rows so few that one launch quantizes and multiplies them).  nvfp4: [xq: M*K/2 packed
 // E2M1 codes][xs: 8*M*S block scales slab-major [S, M, 8]], S = ceil(K/128), and, as
 // part 5, [wsl: 8*N*S] the weight's block scales in the same layout.  INT4:
 // [xq: M*K][w8: N*K] (code values as E4M3 bytes) and, as parts 5 and 6, the
@@ -101,7 +101,7 @@ Layout layout(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R) {
   size_t parts[7] = {0, 0, 0, 0, 0, 0, 0};
   if (scheme == QPL_INT8 && qpl::int8_token_fits(M, K)) return L;
   if (scheme == QPL_FP8R || scheme == QPL_INT8) {
-    parts[0] = size_t(M) * size_t(K);
+    parts[0] = size_t(M) * size_t(scheme == QPL_INT8 ? qpl::int8_pitch(K) : K);
     parts[1] = size_t(4) * size_t(M);
   } else {
     if (scheme == QPL_NVFP4) {
@@ -668,7 +668,7 @@ QPL_EXPORT qpl_status quant_act_int8(const uint16_t* x, int64_t M, int64_t K, co
   if (s != QPL_OK) return s;
   if ((s = check_device()) != QPL_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return launched(Timed(QPL_KERNEL_QUANT_INT8, st)(qpl::launch_quant_int8(x, M, K, smooth, x_q, x_scale, st)));
+  return launched(Timed(QPL_KERNEL_QUANT_INT8, st)(qpl::launch_quant_int8(x, M, K, K, smooth, x_q, x_scale, st)));
 }
 
 namespace {
@@ -696,7 +696,8 @@ qpl_status int8_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const
   uint8_t* base = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(base + L.off[0]);
   float* xs = reinterpret_cast<float*>(base + L.off[1]);
-  if ((s = launched(Timed(QPL_KERNEL_QUANT_INT8, st)(qpl::launch_quant_int8(x, M, K, smooth, xq, xs, st)))) != QPL_OK)
+  if ((s = launched(Timed(QPL_KERNEL_QUANT_INT8, st)(
+           qpl::launch_quant_int8(x, M, K, qpl::int8_pitch(K), smooth, xq, xs, st)))) != QPL_OK)
     return s;
   return launched(Timed(gemm_kind(ep, QPL_KERNEL_GEMM_INT8), st)(
       qpl::launch_gemm_int8(xq, xs, weight, weight_scale, M, K, N, ep, y, st)));
@@ -724,14 +725,14 @@ qpl_status check_choices(int64_t T, int64_t topk) {
   return QPL_OK;
 }
 
-// Workspace of a grouped product: [xq: R K][xs: 4 R][row tiles: 16 (1 + their bound)].
+// Workspace of a grouped product: [xq: R int8_pitch(K)][xs: 4 R][row tiles: 16 (1 + their bound)].
 struct GroupedLayout {
   size_t xs = 0, tiles = 0, total = 0;
 };
 
 GroupedLayout grouped_layout(int64_t R, int64_t K, int64_t E) {
   GroupedLayout L;
-  L.xs = round256(size_t(R) * size_t(K));
+  L.xs = round256(size_t(R) * size_t(qpl::int8_pitch(K)));
   L.tiles = L.xs + round256(size_t(4) * size_t(R));
   L.total = L.tiles + round256(size_t(16) * size_t(1 + qpl::grouped_row_tiles(R, E)));
   return L;

@@ -117,10 +117,13 @@ hipError_t launch_lowrank_prep(const uint16_t* l1, const uint16_t* l2, int64_t K
                                uint16_t* l1t, uint16_t* l2t, hipStream_t stream);
 
 
-// 8-bit integer linears.  Quantizer: codes [M, K] and scales [M] of x (divided by lam
-// [K] first when not nullptr).  GEMM: y = bf16(act((xq w^T) xs ws)).
-hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, const float* lam, int8_t* xq, float* xs,
-                             hipStream_t stream);
+// 8-bit integer linears.  Quantizer: codes [M, K], rows `pitch` apart, and scales [M] of x
+// (divided by lam [K] first when not nullptr).  GEMM: y = bf16(act((xq w^T) xs ws)), the rows
+// of xq int8_pitch(K) apart: whole 128-byte lines for long rows, because a row segment that
+// straddles two lines costs two requests.
+constexpr int64_t int8_pitch(int64_t K) { return K < 512 ? K : (K + 127) / 128 * 128; }
+hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, int64_t pitch, const float* lam, int8_t* xq,
+                             float* xs, hipStream_t stream);
 hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t M, int64_t K,
                             int64_t N, const Epilogue& ep, uint16_t* y, hipStream_t stream);
 // Quantizer and product of a few rows in one launch (int8_token_fits).

@@ -28,6 +28,7 @@ def r256(b):
 
 def test_workspace_sizes():
     assert qpl.qlinear_workspace_bytes(qpl.QPL_INT8, 33, 48, 7) == r256(33 * 48) + r256(4 * 33)
+    assert qpl.qlinear_workspace_bytes(qpl.QPL_INT8, 33, 1040, 7) == r256(33 * 1152) + r256(4 * 33)   # rows of whole lines
     assert qpl.qlinear_workspace_bytes(qpl.QPL_INT8, 4, 32, 4, 1) == 0          # no low rank
     assert qpl.qlinear_workspace_bytes(qpl.QPL_INT8, 8, KMAX, 4) > 0
     assert qpl.qlinear_workspace_bytes(qpl.QPL_INT8, 8, KMAX + 16, 4) == 0      # int32 sums
