@@ -601,8 +601,9 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __r
 //
 // A tile with at most half (a quarter) of its rows present, an expert's last one for
 // instance, runs with NJ = NJM / 2 (/ 4), so that its MFMAs are mostly on rows that
-// exist.  Chunk c of a 128-byte stage row r sits at chunk c ^ (r % 8): the 16-byte
-// operand reads of a wavefront fall on distinct banks.
+// exist.  Chunk c of a 128-byte stage row r sits at chunk c ^ ((r / 2) % 8): two rows fill the
+// 64 banks, and the 16 lanes that read 16 bytes each in a cycle, 16 rows apart by one, hit each
+// bank once (with c ^ (r % 8) rows r and r + 8 meet).
 //
 // Top of a piece: wait for its loads, then a barrier: the piece is in LDS for every
 // wavefront, and every wavefront is done with the piece before, whose stage the next loads fill.
@@ -615,6 +616,8 @@ struct StagedArgs {
   int tiles_m, tiles_n;  // tiles_m unused when grouped
   int nwg;
 };
+
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * PR_ROW + ((c ^ ((r >> 1) & 7)) << 4); }
 
 // Tile (row tile, column tile) at position s of the walk: groups of four row tiles,
 // column by column, so that workgroups of one XCD share operand rows in its L2.
@@ -701,11 +704,11 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   while (position(nt) < units) ++nt;
   if (nt > 0 && tile(nt - 1).rows <= 0) --nt;  // a part behind its tile's last row
 
-  // load q of an operand: rows (rows / 4) wv + 8 q .. + 7; lane l fills row + l / 8, stage
-  // chunk l % 8, with the row's chunk (l % 8) ^ (l / 8)
-  const int lc = (lane & 7) ^ (lane >> 3);
-  const uint32_t vx = (uint32_t)((XR / 4 * wv + (lane >> 3)) * p.px + 16 * lc);
-  const uint32_t vw = (uint32_t)((WR / 4 * wv + (lane >> 3)) * p.K + 16 * lc);
+  // load q of an operand: rows (rows / 4) wv + 8 q .. + 7; lane l fills row + l / 8, stage chunk
+  // l % 8, with the row's chunk (l % 8) ^ ((row / 2) % 8) = lc ^ 4 (q % 2)
+  const int lc = (lane & 7) ^ (lane >> 4);
+  const uint32_t vx = (uint32_t)((XR / 4 * wv + (lane >> 3)) * p.px);
+  const uint32_t vw = (uint32_t)((WR / 4 * wv + (lane >> 3)) * p.K);
 
   // The stream of pieces: the descriptors change where it enters a tile, from piece to
   // piece only the byte offset along K does.
@@ -741,10 +744,11 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     return r;
   };
   auto issue = [&](const Piece& s, int d) {
-    const bool in = s.valid && s.koff + 16 * lc < p.K;
     const int q = d < XL ? d : d - XL;
+    const int byte = 16 * (lc ^ (4 * (q & 1)));
+    const bool in = s.valid && s.koff + byte < p.K;
     const uint32_t dst = lbase + s.stage * STAGE + (d < XL ? XR / 4 * wv + 8 * q : XR + WR / 4 * wv + 8 * q) * PR_ROW;
-    const uint32_t vo = in ? (d < XL ? vx : vw) + (uint32_t)(8 * q * (d < XL ? p.px : p.K)) : kOutOfRange;
+    const uint32_t vo = in ? (d < XL ? vx : vw) + (uint32_t)(8 * q * (d < XL ? p.px : p.K) + byte) : kOutOfRange;
     dma16(dst, vo, d < XL ? dx : dw, s.koff);
   };
   // the tile's output scales, 64 per load: wavefronts 0 and 1 those of x, 2 and 3 those of W; every
@@ -760,8 +764,8 @@ void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     i32x4 lo, hi;
   };
   auto frag = [&](const uint8_t* st, int row, int u) {
-    return Frag{*reinterpret_cast<const i32x4*>(st + proff(row, 4 * u + 2 * h)),
-                *reinterpret_cast<const i32x4*>(st + proff(row, 4 * u + 2 * h + 1))};
+    return Frag{*reinterpret_cast<const i32x4*>(st + chunk_at(row, 4 * u + 2 * h)),
+                *reinterpret_cast<const i32x4*>(st + chunk_at(row, 4 * u + 2 * h + 1))};
   };
   auto mma = [&](const Frag& w, const Frag& x, i32x16 c) {
     c = __builtin_amdgcn_mfma_i32_32x32x32_i8(w.lo, x.lo, c, 0, 0, 0);
