@@ -489,7 +489,7 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
 // A few rows (single tokens) in one launch: as the direct kernel, but every workgroup quantizes
 // the M <= 16 rows itself, into LDS, while its first weight bytes are on their way.  The
 // quantizer's launch and the wait for it cost more than the repeated work: 1 x 4096 x 4096 takes
-// 6.2 us, the two launches 6.1 + 5.5 us.
+// 5.6 us, the two launches 6.1 + 5.5 us.
 // A row is parts of 64 vectors of 8 elements; wavefront w takes the parts w, w + 16, ... of all
 // rows, up to TOKEN_SLOTS of them.
 // ---------------------------------------------------------------------------
