@@ -85,7 +85,7 @@ def grouped_want(xq, xs, w, ws, offsets, f):
 # rows of each expert; K; N
 GROUPS = [([1], 16, 1), ([0, 0, 5], 48, 9), ([3, 0, 16, 17, 1], 80, 40), ([1] * 40, 64, 33), ([0, 200, 0], 144, 100),
           ([100, 3, 64, 65, 0, 1], 272, 130), ([300, 700, 20, 0, 513], 400, 264), ([5] * 300, 128, 16),
-          ([2000, 0, 0, 0, 0, 0, 0, 1], 128, 72), ([1500, 900, 1300], 336, 513), ([256] * 16, 512, 512)]
+          ([0] * 3000 + [2] + [0] * 2000 + [1], 32, 16), ([2000, 0, 0, 0, 0, 0, 0, 1], 128, 72), ([1500, 900, 1300], 336, 513), ([256] * 16, 512, 512)]
 
 
 @pytest.mark.parametrize("rows,K,N", GROUPS)
@@ -156,7 +156,7 @@ def composed(x, ids, wt, f1, f2):
 MOES = [(1, 1, 1, 16, 16, 1, "random"), (1, 2, 8, 128, 64, 40, "random"), (7, 4, 16, 256, 96, 136, "random"),
         (50, 2, 4, 144, 80, 33, "invalid"), (33, 3, 6, 64, 48, 24, "none"), (300, 4, 8, 256, 176, 264, "skewed"),
         (900, 2, 3, 128, 512, 96, "one"), (128, 8, 1024, 64, 48, 16, "invalid"), (1024, 1, 7, 528, 32, 20, "skewed"),
-        (64, 16, 1000, 2064, 16, 8, "random"), (205, 5, 4, 96, 32, 24, "skewed")]
+        (17000, 2, 5, 32, 16, 8, "invalid"), (64, 16, 1000, 2064, 16, 8, "random"), (205, 5, 4, 96, 32, 24, "skewed")]
 
 
 @pytest.mark.parametrize("T,topk,E,K,H,N,kind", MOES)

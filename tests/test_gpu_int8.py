@@ -72,7 +72,7 @@ SHAPES = [(1, 16, 1), (1, 4096, 257), (2, 48, 16), (15, 80, 33), (16, 128, 64), 
           (16, 2064, 50), (8, 4096, 70), (9, 3600, 40), (13, 1008, 8200), (11, 2560, 77),
           (1, 16384, 90), (1, 16400, 90), (16, 1024, 4100), (16, 1040, 64), (4, 4096, 20000), (5, 3120, 40), (7, 2048, 30),
           (300, 192, 513), (513, 336, 264), (1025, 1200, 1032), (2100, 256, 2050), (4500, 96, 5000), (3, 131072, 20),
-          (260, 20000, 40)]
+          (260, 20000, 40), (150, 131072, 130), (2, 4096, 100003)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -127,7 +127,7 @@ def test_zero_rows_give_zeros():
     assert not y[::3].any() and y[1::3].any()
 
 
-@pytest.mark.parametrize("M,N,K", [(33, 67108869, 16), (40000, 65536, 64)])
+@pytest.mark.parametrize("M,N,K", [(16, 134217750, 16), (33, 67108869, 16), (40000, 65536, 64)])
 def test_outputs_past_2_31_elements(M, N, K):
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
