@@ -26,17 +26,15 @@ namespace {
 // rounds to the nearest integer, ties to even, and leaves the code in the low byte.
 // ---------------------------------------------------------------------------
 struct RowCode {
-  float s, r, up;  // scale; 127 / (a up); up = 2^100 for rows whose 127 / a might overflow, else 1
-  bool zero, tiny;
+  float s, r;  // scale; 127 / a, or 127 / (a 2^100) for rows whose 127 / a might overflow
+  bool tiny;   // those rows
 };
 
 __device__ __forceinline__ RowCode row_code(float amax) {
   RowCode d;
   d.s = amax / 127.0f;
-  d.zero = !(amax > 0.0f);
   d.tiny = amax < 0x1p-100f;
-  d.up = d.tiny ? 0x1p100f : 1.0f;
-  d.r = d.zero ? 0.0f : 127.0f / (amax * d.up);
+  d.r = amax > 0.0f ? 127.0f / (d.tiny ? amax * 0x1p100f : amax) : 0.0f;
   return d;
 }
 
@@ -48,13 +46,12 @@ __device__ __forceinline__ uint32_t code_bits(float x, float r) {
 
 // Codes of two bf16 pairs, in order.
 __device__ __forceinline__ uint32_t code_word(uint32_t a, uint32_t b, const RowCode& d) {
-  const float u = d.tiny ? d.up : 1.0f;
   float x0 = bf16_lo(a), x1 = bf16_hi(a), x2 = bf16_lo(b), x3 = bf16_hi(b);
   if (d.tiny) {
-    x0 *= u;
-    x1 *= u;
-    x2 *= u;
-    x3 *= u;
+    x0 *= 0x1p100f;
+    x1 *= 0x1p100f;
+    x2 *= 0x1p100f;
+    x3 *= 0x1p100f;
   }
   const uint32_t lo = __builtin_amdgcn_perm(code_bits(x1, d.r), code_bits(x0, d.r), 0x0C0C0400u);
   const uint32_t hi = __builtin_amdgcn_perm(code_bits(x3, d.r), code_bits(x2, d.r), 0x04000C0Cu);
@@ -75,9 +72,9 @@ __device__ __forceinline__ u32x4 smooth_vec(const u32x4& v, const float* __restr
                smooth_pair(v.w, b[2], b[3])};
 }
 
-// Codes and scale of the row at `src` (nullptr: a row of zeros) into row `row`, `pitch` codes apart.  REUSED: other rows
-// are made of the same source, which should stay in the caches.  SPLIT: the workgroup's four
-// wavefronts share the row.
+// Codes and scale of the row at `src` (nullptr: a row of zeros) into row `row`, rows `pitch`
+// codes apart.  REUSED: other rows are made of the same source, which should stay in the
+// caches.  SPLIT: the workgroup's four wavefronts share the row.
 template <int VPT, bool SMOOTH, bool REUSED, bool SPLIT>
 __device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int64_t row, int64_t K, int64_t pitch,
                                           const float* __restrict__ lam, int8_t* __restrict__ xq,
@@ -138,15 +135,13 @@ struct RowTile {
 };
 
 // The experts' rows cut into tiles of `tm` rows that never cross an expert, in order;
-// count[0] = their number (at most cap).  offsets [E + 1] are clamped into [0, R], so
-// whatever they hold no tile leaves the R rows.  One workgroup.
+// count[0] = their number (at most cap).  offsets [E + 1] are clamped into [0, R] and counted in
+// 64 bits, so whatever they hold no tile leaves the R rows and no write the array.  One workgroup.
 __device__ __forceinline__ void build_row_tiles(const int* offsets, int E, int R, int tm, int cap,
                                                 int* __restrict__ count, RowTile* __restrict__ tiles) {
-  __shared__ int wsum[4];
-  __shared__ int base;
+  __shared__ int64_t wsum[4];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  if (threadIdx.x == 0) base = 0;
-  __syncthreads();
+  int64_t base = 0;
   for (int e0 = 0; e0 < E; e0 += 256) {
     const int e = e0 + (int)threadIdx.x;
     int lo = 0, hi = 0;
@@ -154,24 +149,35 @@ __device__ __forceinline__ void build_row_tiles(const int* offsets, int E, int R
       lo = min(max(offsets[e], 0), R);
       hi = min(max(offsets[e + 1], lo), R);
     }
-    const int n = (int)(((int64_t)hi - lo + tm - 1) / tm);
-    int sum = n;
+    const int n = (hi - lo) / tm + ((hi - lo) % tm != 0);
+    int64_t sum = n;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(sum, d, 64);
+      const int64_t o = __shfl_up(sum, d, 64);
       if (lane >= d) sum += o;
     }
     if (lane == 63) wsum[wv] = sum;
     __syncthreads();
-    int first = base + sum - n;
-    for (int w = 0; w < wv; ++w) first += wsum[w];
-    for (int i = 0; i < n && first + i < cap; ++i)
-      tiles[first + i] = RowTile{lo + i * tm, (int)min((int64_t)hi, (int64_t)lo + (int64_t)(i + 1) * tm), e, 0};
-    __syncthreads();
-    if (threadIdx.x == 0) base += wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    int64_t first = base + sum - n;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wv) first += wsum[w];
+      base += wsum[w];
+    }
+    // each lane the tiles of its expert, or the whole wavefront those of an expert with many
+    if (n <= 4) {
+      for (int i = 0; i < n && first + i < cap; ++i)
+        tiles[first + i] = RowTile{lo + i * tm, i + 1 < n ? lo + (i + 1) * tm : hi, e, 0};
+    }
+    for (uint64_t many = __ballot(n > 4); many != 0; many &= many - 1) {
+      const int l = __ffsll((unsigned long long)many) - 1;
+      const int ln = __shfl(n, l, 64), llo = __shfl(lo, l, 64), lhi = __shfl(hi, l, 64), le = __shfl(e, l, 64);
+      const int64_t lfirst = __shfl(first, l, 64);
+      for (int i = lane; i < ln && lfirst + i < cap; i += 64)
+        tiles[lfirst + i] = RowTile{llo + i * tm, i + 1 < ln ? llo + (i + 1) * tm : lhi, le, 0};
+    }
     __syncthreads();
   }
-  if (threadIdx.x == 0) count[0] = min(base, cap);
+  if (threadIdx.x == 0) count[0] = (int)(base < cap ? base : cap);
 }
 
 struct TilePlan {
@@ -283,15 +289,16 @@ __global__ __launch_bounds__(256) void k_int8_moe_front(const int* __restrict__ 
 constexpr int64_t kQuantBlocks = int64_t(1) << 22;  // workgroups stride over rows past this many
 
 template <bool SMOOTH, bool GROUPED, bool GATHER, bool SPLIT>
-hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, int64_t pitch, const float* lam,
-                             const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
+hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, int64_t pitch,
+                             const float* lam, const int* row_index, int8_t* xq, float* xs, const TilePlan& plan,
+                             hipStream_t stream) {
   const int64_t per_lane = SPLIT ? (K / 8 + 255) / 256 : (K / 8 + 63) / 64;
   const int64_t blocks = SPLIT ? rows : (rows + 3) / 4;
   const dim3 grid((unsigned)((blocks < kQuantBlocks ? blocks : kQuantBlocks) + (GROUPED ? 1 : 0))), block(256);
 #define QPL_CASE(V)                                                                                                   \
   if (per_lane <= V || V == 0) {                                                                                      \
     hipLaunchKernelGGL((k_quant_int8<V, SMOOTH, GROUPED, GATHER, SPLIT>), grid, block, 0, stream, x, rows_x, rows, K, \
-                       pitch, lam, row_index, xq, xs, plan);                                                                 \
+                       pitch, lam, row_index, xq, xs, plan);                                                          \
     return hipGetLastError();                                                                                         \
   }
   if constexpr (SPLIT) {
@@ -303,16 +310,17 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, in
   return hipErrorInvalidValue;
 }
 
-// A workgroup per row up to kSplitRows rows.
+// A workgroup per row up to kSplitRows rows: 24 x 4096 with smoothing 4.7 us, with a wavefront per
+// row 10.6 us; 16384 x 2048 gathered 22.2 and 17.9 us.
 constexpr int64_t kSplitRows = 2048;
 
 template <bool SMOOTH, bool GROUPED, bool GATHER>
 hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, int64_t pitch, const float* lam,
                         const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
-  return rows <= kSplitRows && K > 512
-             ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream)
-             : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan,
-                                                                 stream);
+  return rows <= kSplitRows && K > 512 ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(
+                                             x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream)
+                                       : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(
+                                             x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -323,8 +331,7 @@ hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t
 //
 // The operands are swapped (the MFMA computes y^T), so a lane holds four consecutive
 // columns of one row.  Row r of an operand and bytes 64 s + 16 (l / 16) of the piece go
-// to lane l with l % 16 = r.  x lanes past K read zeros, which makes the weight bytes beside them (the next
-// row's, or zeros past the weight's end) irrelevant.
+// to lane l with l % 16 = r.  Rows past an operand's end and bytes past K read as zeros.
 // ---------------------------------------------------------------------------
 struct Int8Args {
   const int8_t* x;  // [rows, K], px apart
@@ -383,79 +390,80 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
   const int r16 = lane & 15, q = lane >> 4;
   const int64_t tiles_m = GROUPED ? p.count[0] : p.tiles_m;
   const int pieces = (p.K + 127) >> 7;
-  for (int64_t tm = blockIdx.y; tm < tiles_m; tm += gridDim.y)
-  for (int64_t tn = blockIdx.x; tn < p.tiles_n; tn += gridDim.x) {
-    const int64_t n0 = tn * 16 * NT;
-    int64_t m0, m1;
-    const int8_t* w = p.w;
-    const float* wsc = p.ws;
-    if constexpr (GROUPED) {
-      const RowTile rt = p.tiles[tm];
-      m0 = rt.m0;
-      m1 = rt.m1;
-      w += (int64_t)rt.e * p.N * p.K;
-      wsc += (int64_t)rt.e * p.N;
-    } else {
-      m0 = tm * 16 * MT;
-      m1 = p.M - m0 < 16 * MT ? p.M : m0 + 16 * MT;
-    }
-    const int64_t nr = p.N - n0 < 16 * NT ? p.N - n0 : 16 * NT;
-    const __amdgpu_buffer_rsrc_t dx = make_rsrc(p.x + m0 * p.px, (m1 - m0) * p.px);
-    const __amdgpu_buffer_rsrc_t dw = make_rsrc(w + n0 * p.K, nr * p.K);
-    i32x4 acc[MT][NT];
+  for (int64_t tm = blockIdx.y; tm < tiles_m; tm += gridDim.y) {
+    for (int64_t tn = blockIdx.x; tn < p.tiles_n; tn += gridDim.x) {
+      const int64_t n0 = tn * 16 * NT;
+      int64_t m0, m1;
+      const int8_t* w = p.w;
+      const float* wsc = p.ws;
+      if constexpr (GROUPED) {
+        const RowTile rt = p.tiles[tm];
+        m0 = rt.m0;
+        m1 = rt.m1;
+        w += (int64_t)rt.e * p.N * p.K;
+        wsc += (int64_t)rt.e * p.N;
+      } else {
+        m0 = tm * 16 * MT;
+        m1 = p.M - m0 < 16 * MT ? p.M : m0 + 16 * MT;
+      }
+      const int64_t nr = p.N - n0 < 16 * NT ? p.N - n0 : 16 * NT;
+      const __amdgpu_buffer_rsrc_t dx = make_rsrc(p.x + m0 * p.px, (m1 - m0) * p.px);
+      const __amdgpu_buffer_rsrc_t dw = make_rsrc(w + n0 * p.K, nr * p.K);
+      i32x4 acc[MT][NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    for (int c = wv; c < pieces; c += W * U) {
-      i32x4 fx[U][2][MT], fw[U][2][NT];
+        for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+      for (int c = wv; c < pieces; c += W * U) {
+        i32x4 fx[U][2][MT], fw[U][2][NT];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int k = (c + u * W) * 128 + 64 * s + 16 * q;
-          const bool in = k < p.K;
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            fw[u][s][j] = load16(dw, in ? (uint32_t)((16 * j + r16) * p.K + k) : kOutOfRange);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            fx[u][s][i] = load16(dx, in ? (uint32_t)((16 * i + r16) * p.px + k) : kOutOfRange);
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int s = 0; s < 2; ++s) {
+            const int k = (c + u * W) * 128 + 64 * s + 16 * q;
+            const bool in = k < p.K;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx[u][s][i], acc[i][j], 0, 0, 0);
+              fw[u][s][j] = load16(dw, in ? (uint32_t)((16 * j + r16) * p.K + k) : kOutOfRange);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+              fx[u][s][i] = load16(dx, in ? (uint32_t)((16 * i + r16) * p.px + k) : kOutOfRange);
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx[u][s][i], acc[i][j], 0, 0, 0);
+      }
+      // The last MFMA's result is stored to LDS right behind the loop.  The wait states in
+      // between are spelled out: a build of this kernel had none on the path out of the loop,
+      // and stored sums without the last MFMA's share.
+      asm volatile("s_nop 15" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) red[wv][i * NT + j][lane] = acc[i][j];
+      __syncthreads();
+      // vector v: tile v / 64 (row block i, column block j), lane v % 64's four columns
+      for (int v = threadIdx.x; v < MT * NT * 64; v += 64 * W) {
+        const int tile = v >> 6, l = v & 63;
+        i32x4 sum = red[0][tile][l];
+#pragma unroll
+        for (int k = 1; k < W; ++k) sum += red[k][tile][l];
+        const int64_t m = m0 + 16 * (tile / NT) + (l & 15);
+        const int64_t n = n0 + 16 * (tile % NT) + 4 * (l >> 4);
+        store_four<EPI>(Y, m, m1, n, p.N, sum, m < m1 ? p.xs[m] : 0.0f, wsc, e);
+      }
+      __syncthreads();
     }
-    // The last MFMA's result is stored to LDS right behind the loop.  The wait states in
-    // between are spelled out: a build of this kernel had none on the path out of the loop,
-    // and stored sums without the last MFMA's share.
-    asm volatile("s_nop 15" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) red[wv][i * NT + j][lane] = acc[i][j];
-    __syncthreads();
-    // vector v: tile v / 64 (row block i, column block j), lane v % 64's four columns
-    for (int v = threadIdx.x; v < MT * NT * 64; v += 64 * W) {
-      const int tile = v >> 6, l = v & 63;
-      i32x4 sum = red[0][tile][l];
-#pragma unroll
-      for (int k = 1; k < W; ++k) sum += red[k][tile][l];
-      const int64_t m = m0 + 16 * (tile / NT) + (l & 15);
-      const int64_t n = n0 + 16 * (tile % NT) + 4 * (l >> 4);
-      store_four<EPI>(Y, m, m1, n, p.N, sum, m < m1 ? p.xs[m] : 0.0f, wsc, e);
-    }
-    __syncthreads();
   }
 }
 
@@ -637,8 +645,8 @@ template <int NI, int NJM, int S>
 constexpr int staged_per_cu() { return (160 << 10) / (64 * (NI + NJM) * (PR_ROW + 4) * S + 256); }
 
 template <int NI, int NJM, int S, int EPI, bool GROUPED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu((staged_per_cu<NI, NJM, S>()), (staged_per_cu<NI, NJM, S>()))))
-void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(
+    (staged_per_cu<NI, NJM, S>()), (staged_per_cu<NI, NJM, S>())))) void k_int8_staged(StagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
   constexpr int XR = 64 * NJM, WR = 64 * NI;     // rows of x and of W per stage
   constexpr int STAGE = (XR + WR) * PR_ROW;
   constexpr int XL = 2 * NJM, LOADS = XL + 2 * NI;  // loads per wavefront per piece: x, all
@@ -879,7 +887,9 @@ hipError_t launch_staged(const Int8Args& g, int64_t row_tiles, const Epilogue& e
   EpiArgs e;
   switch (epi_kind(ep, e)) {
     case 0: hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, 0, GROUPED>), grid, block, 0, stream, a, y, e); break;
-    case EPI_GELU: hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, EPI_GELU, GROUPED>), grid, block, 0, stream, a, y, e); break;
+    case EPI_GELU:
+      hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, EPI_GELU, GROUPED>), grid, block, 0, stream, a, y, e);
+      break;
     case EPI_QKV:
       if constexpr (!GROUPED) {
         hipLaunchKernelGGL((k_int8_staged<NI, NJM, S, EPI_QKV, false>), grid, block, 0, stream, a, y, e);
@@ -1062,11 +1072,12 @@ static TilePlan tile_plan(const int32_t* offsets, int64_t R, int64_t K, int64_t 
 }
 
 hipError_t launch_quant_int8_grouped(const uint16_t* x, int64_t rows_x, int64_t R, int64_t K, int64_t N,
-                                     const int32_t* row_index, const int32_t* offsets, int64_t E, int8_t* xq, float* xs, int32_t* tiles,
-                                     hipStream_t stream) {
+                                     const int32_t* row_index, const int32_t* offsets, int64_t E, int8_t* xq,
+                                     float* xs, int32_t* tiles, hipStream_t stream) {
   const TilePlan t = tile_plan(offsets, R, K, N, E, tiles);
-  return row_index ? launch_quant<false, true, true>(x, rows_x, R, K, int8_pitch(K), nullptr, row_index, xq, xs, t, stream)
-                   : launch_quant<false, true, false>(x, rows_x, R, K, int8_pitch(K), nullptr, nullptr, xq, xs, t, stream);
+  const int64_t pitch = int8_pitch(K);
+  return row_index ? launch_quant<false, true, true>(x, rows_x, R, K, pitch, nullptr, row_index, xq, xs, t, stream)
+                   : launch_quant<false, true, false>(x, rows_x, R, K, pitch, nullptr, nullptr, xq, xs, t, stream);
 }
 
 bool moe_front_fits(int64_t n, int64_t E) { return n <= FRONT_N && E <= FRONT_E; }

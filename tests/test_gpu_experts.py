@@ -138,6 +138,21 @@ def test_bad_offsets_stay_inside_the_rows(offsets):
     assert bool((whole[:10] == 7).all()) and bool((whole[10 + R:] == 7).all())
 
 
+def test_many_lying_offsets_stay_inside_the_tile_list():
+    # every other expert claims all 2^24 rows: 2^33 and more tiles, the list holds a few hundred thousand
+    E, R = 65536, 1 << 24
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = R
+    x = torch.ones((R, 16), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((E, 1, 16), dtype=torch.int8, device="cuda")
+    y = torch.full((R + 64, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    need = qpl.qlinear_grouped_int8_workspace_bytes(R, 16, 1, E)
+    work = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    qpl.qlinear_grouped_int8(x, w, torch.ones((E, 1), device="cuda"), offsets, y=y[:R], workspace=work[:need])
+    torch.cuda.synchronize()
+    assert bool((y[R:] == 7).all()) and bool((work[need:] == 0x5A).all())
+
+
 def moe_inputs(T, topk, E, K, H, N, kind="random"):
     rng = np.random.default_rng(T + E)
     x = bf16_round(rng.standard_normal((T, K)).astype(np.float32))

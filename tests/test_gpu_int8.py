@@ -42,7 +42,8 @@ def test_quantizer_every_significand_pair():
     i = np.arange(128, 256, dtype=np.float64)
     small = np.concatenate([i * 2.0 ** -p for p in range(1, 10)])
     for e in (-120, 0, 100):
-        rows = [np.concatenate([np.minimum(i, j), small, -np.minimum(i, j), -small]) * 2.0 ** e for j in range(128, 256)]
+        rows = [np.concatenate([np.minimum(i, j), small, -np.minimum(i, j), -small]) * 2.0 ** e
+                for j in range(128, 256)]
         x = bf16_round(np.stack(rows).astype(np.float32))
         q, s = qpl.quant_act_int8(to_dev_bf16(x))
         wq, ws = quant_int8(x)
@@ -68,7 +69,8 @@ def test_quantizer_ignores_rows_around_a_view():
 # ---- linear ---------------------------------------------------------------------------
 SHAPES = [(1, 16, 1), (1, 4096, 257), (2, 48, 16), (15, 80, 33), (16, 128, 64), (17, 144, 63), (31, 2064, 100),
           (33, 64, 8), (64, 400, 65), (65, 272, 1000), (127, 1040, 129), (129, 128, 256), (255, 512, 300),
-          (1, 32768, 100), (2, 16384, 530), (4, 8192, 48), (4, 8208, 33), (3, 2000, 20000), (1, 32784, 9), (5, 64, 70), (16, 2048, 300),
+          (1, 32768, 100), (2, 16384, 530), (4, 8192, 48), (4, 8208, 33), (3, 2000, 20000), (1, 32784, 9),
+          (5, 64, 70), (16, 2048, 300),
           (16, 2064, 50), (8, 4096, 70), (9, 3600, 40), (13, 1008, 8200), (11, 2560, 77),
           (1, 16384, 90), (1, 16400, 90), (16, 1024, 4100), (16, 1040, 64), (4, 4096, 20000), (5, 3120, 40), (7, 2048, 30),
           (300, 192, 513), (513, 336, 264), (1025, 1200, 1032), (2100, 256, 2050), (4500, 96, 5000), (3, 131072, 20),
