@@ -358,6 +358,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, (int)kRawBufferWord3);
 }
 
+// The wait states between the last MFMAs and the first reader of their results (8 for 16 x 16, 12
+// for 32 x 32).  They are spelled out: a build of the direct kernel had none on the path out of its
+// loop, and stored sums without the last MFMA's share.  The empty statements take and return the
+// accumulators and, like the s_nop, stay in order, so the MFMAs come before it and the readers behind it.
+template <int MT, int NT>
+__device__ __forceinline__ void settle(i32x4 (&acc)[MT][NT]) {
+  auto pass = [&]() {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+  };
+  pass();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  pass();
+}
+
 // Outputs (m, n .. n + 3) of the sums, if m < m1, as far as n < N.
 template <int EPI>
 __device__ __forceinline__ void store_four(uint16_t* __restrict__ y, int64_t m, int64_t m1, int64_t n, int64_t N,
@@ -439,14 +458,7 @@ __global__ __launch_bounds__(64 * W) void k_int8_direct(Int8Args p, uint16_t* __
               for (int j = 0; j < NT; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s][j], fx[u][s][i], acc[i][j], 0, 0, 0);
       }
-      // The last MFMA's result is stored to LDS right behind the loop.  The wait states in
-      // between are spelled out: a build of this kernel had none on the path out of the loop,
-      // and stored sums without the last MFMA's share.
-      asm volatile("s_nop 15" ::: "memory");
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+      settle(acc);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -563,7 +575,7 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __r
   }
   __syncthreads();
   for (;;) {
-    i32x4 acc{0, 0, 0, 0};
+    i32x4 acc[1][1] = {{i32x4{0, 0, 0, 0}}};
     for (int c = wv; c < pieces; c += W * U) {
       if (c != wv) load_w(c);
 #pragma unroll
@@ -573,12 +585,11 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __r
           const int k = (c + u * W) * 128 + 64 * s + 16 * q;
           i32x4 fx{0, 0, 0, 0};
           if (r16 < M && k < p.K) fx = *reinterpret_cast<const i32x4*>(codes + r16 * p.K + k);
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s], fx, acc, 0, 0, 0);
+          acc[0][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][s], fx, acc[0][0], 0, 0, 0);
         }
     }
-    asm volatile("s_nop 15" ::: "memory");  // as behind the direct kernel's loop
-    asm volatile("" : "+v"(acc));
-    red[wv][lane] = acc;
+    settle(acc);
+    red[wv][lane] = acc[0][0];
     // the next columns' first weight bytes
     const int64_t next = n0 + (int64_t)gridDim.x * 16;
     if (next < p.N) {
@@ -853,7 +864,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
       for (int y = 0; y < NJ; ++y) acc[x][y] = i32x16{};
     for (int k = 0; k < np; ++k) piece(acc, nj);
-    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");  // as behind the direct kernel's loop
+    // as in settle, but 64 to 256 accumulator registers are not passed through a statement: nothing is
+    // scheduled across the two barriers, and every reader stands behind the branch into an output path
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     const float* ls = reinterpret_cast<const float*>(lsc + buf * SBUF);
     buf = buf == S - 1 ? 0 : buf + 1;
