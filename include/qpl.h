@@ -425,11 +425,16 @@ float qpl_nvfp4_global_scale(float amax);
 /*
  * Per-kernel timing (a profiling aid, off by default).  While enabled, every kernel
  * launch of the library is bracketed by two HIP events recorded on the launch's
- * stream.  qpl_timing_collect waits for all recorded events, writes per kernel
- * kind the number of launches and their summed duration in milliseconds since
- * the previous collect (arrays of QPL_KERNEL_COUNT entries, caller-owned host
- * memory), and clears the records.  Events are created by the library on first
- * use and reused.  Not thread-safe with respect to concurrent collect calls.
+ * stream.  qpl_timing_collect_n waits for all recorded events, writes for each of the
+ * first `count` kernel kinds the number of launches and their summed duration in
+ * milliseconds since the previous collect (arrays of `count` entries, caller-owned
+ * host memory; entries past QPL_KERNEL_COUNT become 0), and clears the records of all
+ * kinds.  Events are created by the library on first use and reused.  Not
+ * thread-safe with respect to concurrent collect calls.
+ *   qpl_timing_collect: in source, the same with count = QPL_KERNEL_COUNT.  The exported
+ *   function of that name has no count, so it writes the QPL_TIMING_COLLECT_KINDS kinds
+ *   that it began with: programs built when there were no more have arrays of that size.
+ * Errors: QPL_ERR_NULL, and QPL_ERR_ARG for a negative count.
  */
 typedef enum {
   QPL_KERNEL_QUANT_FP8_ROW = 0,     /* fp8r activation / weight quantize */
@@ -465,7 +470,10 @@ void qpl_timing_enable(int on);
 /* Time only the kernel kinds whose bit (1 << kind) is set in `kinds` (0 = off);
  * an event pair costs a few microseconds of stream time per timed launch. */
 void qpl_timing_select(uint32_t kinds);
+qpl_status qpl_timing_collect_n(int64_t* launches, double* total_ms, int count);
+#define QPL_TIMING_COLLECT_KINDS 18
 qpl_status qpl_timing_collect(int64_t* launches, double* total_ms);
+#define qpl_timing_collect(launches, total_ms) qpl_timing_collect_n((launches), (total_ms), QPL_KERNEL_COUNT)
 
 /* Static description of a status code. */
 const char* qpl_status_str(qpl_status status);

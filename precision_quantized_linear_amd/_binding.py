@@ -21,7 +21,7 @@ EXPORTS = ("quant_act_fp8_row", "quant_act_nvfp4", "qlinear_fp8r", "qlinear_nvfp
            "quant_weight_awq", "qlinear_awq_w4a16", "quant_act_int4", "qlinear_int4", "qlinear_fp8r_ex",
            "qlinear_nvfp4_ex", "qlinear_int4_ex", "qlinear_mlp_nvfp4", "qlinear_mlp_nvfp4_workspace_bytes",
            "qlinear_workspace_bytes", "qpl_amax_bf16", "qpl_nvfp4_global_scale", "qpl_status_str",
-           "qpl_timing_enable", "qpl_timing_select", "qpl_timing_collect", "qlinear_fp8r_noalloc",
+           "qpl_timing_enable", "qpl_timing_select", "qpl_timing_collect", "qpl_timing_collect_n", "qlinear_fp8r_noalloc",
            "quant_act_int8", "qlinear_int8", "qlinear_int8_ex", "expert_plan", "expert_plan_workspace_bytes",
            "qlinear_grouped_int8",
            "qlinear_grouped_int8_workspace_bytes", "expert_combine", "qlinear_moe_int8",
@@ -117,6 +117,8 @@ def load():
     lib.qpl_timing_select.restype = None
     lib.qpl_timing_collect.argtypes = [P, P]
     lib.qpl_timing_collect.restype = ctypes.c_int
+    lib.qpl_timing_collect_n.argtypes = [P, P, ctypes.c_int]
+    lib.qpl_timing_collect_n.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -614,6 +616,6 @@ def timing_collect():
     n = len(KERNELS)
     launches = (ctypes.c_int64 * n)()
     total = (ctypes.c_double * n)()
-    _check("qpl_timing_collect", load().qpl_timing_collect(ctypes.cast(launches, ctypes.c_void_p),
-                                                           ctypes.cast(total, ctypes.c_void_p)))
+    _check("qpl_timing_collect_n", load().qpl_timing_collect_n(ctypes.cast(launches, ctypes.c_void_p),
+                                                               ctypes.cast(total, ctypes.c_void_p), n))
     return {k: (int(launches[i]), float(total[i])) for i, k in enumerate(KERNELS)}

@@ -369,9 +369,10 @@ QPL_EXPORT void qpl_timing_enable(int on) { g_timing.store(on ? (1u << QPL_KERNE
 
 QPL_EXPORT void qpl_timing_select(uint32_t kinds) { g_timing.store(kinds & ((1u << QPL_KERNEL_COUNT) - 1u)); }
 
-QPL_EXPORT qpl_status qpl_timing_collect(int64_t* launches, double* total_ms) {
+QPL_EXPORT qpl_status qpl_timing_collect_n(int64_t* launches, double* total_ms, int count) {
   if (!launches || !total_ms) return QPL_ERR_NULL;
-  for (int i = 0; i < QPL_KERNEL_COUNT; ++i) {
+  if (count < 0) return QPL_ERR_ARG;
+  for (int i = 0; i < count; ++i) {
     launches[i] = 0;
     total_ms[i] = 0.0;
   }
@@ -382,7 +383,7 @@ QPL_EXPORT qpl_status qpl_timing_collect(int64_t* launches, double* total_ms) {
     if (hipEventSynchronize(r.stop) != hipSuccess || hipEventElapsedTime(&ms, r.start, r.stop) != hipSuccess) {
       (void)hipGetLastError();
       st = QPL_ERR_DEVICE;
-    } else {
+    } else if (r.kind < count) {
       launches[r.kind] += 1;
       total_ms[r.kind] += ms;
     }
@@ -391,6 +392,11 @@ QPL_EXPORT qpl_status qpl_timing_collect(int64_t* launches, double* total_ms) {
   }
   g_recs.clear();
   return st;
+}
+
+#undef qpl_timing_collect
+QPL_EXPORT qpl_status qpl_timing_collect(int64_t* launches, double* total_ms) {
+  return qpl_timing_collect_n(launches, total_ms, QPL_TIMING_COLLECT_KINDS);
 }
 
 QPL_EXPORT const char* qpl_status_str(qpl_status status) {
