@@ -112,31 +112,59 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// Plan of many choices for up to PLAN_E experts, in two launches over chunks of them: every
-// workgroup of the second would have to read all choices to know the counts before its chunk,
-// so the first writes counts[chunk][expert] (order-free integer atomics in LDS).  The
-// second sums the columns of that matrix (an expert's first place, and what earlier chunks
-// take of it) and hands out its chunk's places: each wavefront owns a contiguous run of the
-// chunk, and of 64 choices those of one expert find each other by ballots over the id's bits.
-// 131072 choices of 256 experts: the form above reads them 257 times (19 us).
+// Plan of many choices, in two launches over chunks of them: every workgroup of the second
+// would have to read all choices to know the counts before its chunk, so the first writes
+// counts[chunk][expert] (order-free integer atomics in LDS).  The second sums the columns
+// of that matrix (an expert's first place, and what earlier chunks take of it) and hands out
+// its chunk's places: each wavefront owns a contiguous run of the chunk, and of 64 choices
+// those of one expert find each other by ballots over the id's bits.  131072 choices of 256
+// experts: the form above reads them 257 times (19 us).
+// SLICED, for more than PLAN_E experts: workgroup (c, s) serves the choices of chunk c for the
+// PLAN_E experts from s PLAN_E, so the choices are read three times for each slice, not once for
+// each expert.  The slices' sums for each chunk, which follow counts in the workspace, give the
+// places before a slice.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_E = 1024, PLAN_W = 16;
 
+__device__ __forceinline__ int wave_total(int v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+template <bool SLICED>
 __global__ __launch_bounds__(64 * PLAN_W) void k_expert_count(const int* __restrict__ ids, int n, int chunk, int E,
                                                               int* __restrict__ counts) {
+  constexpr int THREADS = 64 * PLAN_W;
   __shared__ int own[PLAN_E];
-  for (int e = threadIdx.x; e < E; e += 64 * PLAN_W) own[e] = 0;
+  __shared__ int sum;
+  const int slice = SLICED ? blockIdx.y : 0, base = slice * PLAN_E;
+  const int mine = SLICED ? min(E - base, PLAN_E) : E;  // experts of this workgroup
+  for (int e = threadIdx.x; e < mine; e += THREADS) own[e] = 0;
+  if (threadIdx.x == 0) sum = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * chunk;
   const int64_t hi = lo + chunk < n ? lo + chunk : n;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += 64 * PLAN_W) {
-    const uint32_t v = (uint32_t)ids[i];
-    if (v < (uint32_t)E) atomicAdd(&own[v], 1);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += THREADS) {
+    const uint32_t v = (uint32_t)ids[i] - (uint32_t)base;
+    if (v < (uint32_t)mine) atomicAdd(&own[v], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 64 * PLAN_W) counts[(int64_t)blockIdx.x * E + e] = own[e];
+  int part = 0;
+  for (int e = threadIdx.x; e < mine; e += THREADS) {
+    counts[(int64_t)blockIdx.x * E + base + e] = own[e];
+    part += own[e];
+  }
+  if constexpr (SLICED) {
+    part = wave_total(part);
+    if ((threadIdx.x & 63) == 0) atomicAdd(&sum, part);
+    __syncthreads();
+    if (threadIdx.x == 0) counts[(int64_t)gridDim.x * E + (int64_t)blockIdx.x * gridDim.y + slice] = sum;
+  }
 }
 
+// bits: 2^bits >= experts of a slice
+template <bool SLICED>
 __global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restrict__ ids, int n, int chunk,
                                                               Divider token, int E, int bits,
                                                               const int* __restrict__ counts,
@@ -145,35 +173,54 @@ __global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restr
   constexpr int THREADS = 64 * PLAN_W;
   __shared__ int next[PLAN_W][PLAN_E];  // a wavefront's next place of each expert
   __shared__ int before[PLAN_E], total[PLAN_E], wave_sum[PLAN_W];
+  __shared__ int slices_before, slices_all;  // choices of the experts before the slice, and of all
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, c = blockIdx.x;
-  for (int e = threadIdx.x; e < E; e += THREADS) before[e] = total[e] = 0;
+  const int slice = SLICED ? blockIdx.y : 0, base = slice * PLAN_E;
+  const int experts = SLICED ? min(E - base, PLAN_E) : E;
+  for (int e = threadIdx.x; e < experts; e += THREADS) before[e] = total[e] = 0;
   for (int i = threadIdx.x; i < PLAN_W * PLAN_E; i += THREADS) next[0][i] = 0;
+  if (threadIdx.x == 0) slices_before = slices_all = 0;
   __syncthreads();
   // counts of this wavefront's run
   const int64_t lo = (int64_t)c * chunk + (int64_t)wv * (chunk / PLAN_W);
   const int64_t end = lo + chunk / PLAN_W;
   const int64_t hi = end < n ? end : n;
   for (int64_t i = lo + lane; i < hi; i += 64) {
-    const uint32_t v = (uint32_t)ids[i];
-    if (v < (uint32_t)E) atomicAdd(&next[wv][v], 1);
+    const uint32_t v = (uint32_t)ids[i] - (uint32_t)base;
+    if (v < (uint32_t)experts) atomicAdd(&next[wv][v], 1);
   }
   // column sums, THREADS / 2^bits rows of the matrix at a time
   const int e0 = threadIdx.x & ((1 << bits) - 1), step = THREADS >> bits;
-  if (e0 < E) {
+  if (e0 < experts) {
     int b = 0, t = 0;
 #pragma unroll 16
     for (int r = threadIdx.x >> bits; r < (int)gridDim.x; r += step) {
-      const int k = counts[(int64_t)r * E + e0];
+      const int k = counts[(int64_t)r * E + base + e0];
       t += k;
       b += r < c ? k : 0;
     }
     atomicAdd(&total[e0], t);
     atomicAdd(&before[e0], b);
   }
+  if constexpr (SLICED) {
+    const int* sums = counts + (int64_t)gridDim.x * E;
+    const int slices = gridDim.y, cells = (int)gridDim.x * slices;
+    int b = 0, t = 0;
+    for (int i = threadIdx.x; i < cells; i += THREADS) {
+      t += sums[i];
+      b += i % slices < slice ? sums[i] : 0;
+    }
+    t = wave_total(t);
+    b = wave_total(b);
+    if (lane == 0) {
+      atomicAdd(&slices_all, t);
+      atomicAdd(&slices_before, b);
+    }
+  }
   __syncthreads();
-  // exclusive sum of the totals: thread e for expert e (E <= THREADS)
+  // exclusive sum of the totals: thread e for expert e of the slice (at most THREADS)
   const int e = threadIdx.x;
-  const int mine = e < E ? total[e] : 0;
+  const int mine = e < experts ? total[e] : 0;
   int sum = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -188,8 +235,12 @@ __global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restr
     if (w < wv) first += wave_sum[w];
     all += wave_sum[w];
   }
-  if (e < E) {
-    if (c == 0) offsets[e] = first;
+  if constexpr (SLICED) {
+    first += slices_before;
+    all = slices_all;
+  }
+  if (e < experts) {
+    if (c == 0) offsets[base + e] = first;
     int place = first + before[e];
 #pragma unroll
     for (int w = 0; w < PLAN_W; ++w) {
@@ -198,14 +249,16 @@ __global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restr
       place += k;
     }
   }
-  if (c == 0 && threadIdx.x == 0) offsets[E] = all;
+  if (c == 0 && slice == 0 && threadIdx.x == 0) offsets[E] = all;
   __syncthreads();
   const uint64_t earlier = (1ull << lane) - 1ull;
   for (int64_t i0 = lo; i0 < hi; i0 += 64) {
     const int64_t i = i0 + lane;
-    const int v = i < hi ? ids[i] : -1;
-    const bool valid = (uint32_t)v < (uint32_t)E;
+    const uint32_t id = i < hi ? (uint32_t)ids[i] : 0xFFFFFFFFu;  // outside [0, E)
+    const uint32_t v = id - (uint32_t)base;
+    const bool valid = v < (uint32_t)experts;
     uint64_t peers = __ballot(valid);
+    if (SLICED && peers == 0 && slice > 0) continue;
     for (int k = 0; k < bits; ++k) {
       const bool set = (v >> k) & 1;
       const uint64_t b = __ballot(set);
@@ -216,12 +269,13 @@ __global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restr
       slot[i] = place;
       row_index[place] = token((int)i);
       if ((peers & earlier) == 0) atomicAdd(&next[wv][v], __popcll(peers));
-    } else if (i < hi) {
+    } else if (i < hi && slice == 0 && id >= (uint32_t)E) {
       slot[i] = -1;
     }
   }
-  for (int64_t i = (int64_t)all + (int64_t)c * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS)
-    row_index[i] = -1;
+  if (slice == 0)
+    for (int64_t i = (int64_t)all + (int64_t)c * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS)
+      row_index[i] = -1;
 }
 
 // Choices of a chunk: 2048, or what makes at most 256 chunks.
@@ -230,7 +284,17 @@ int plan_chunk(int64_t n) {
   return c <= 2048 ? 2048 : (int)((c + 1023) / 1024 * 1024);
 }
 
-bool plan_in_chunks(int64_t n, int64_t E) { return n >= 32768 && E <= PLAN_E; }
+int plan_slices(int64_t E) { return (int)((E + PLAN_E - 1) / PLAN_E); }
+
+// Which form, with both measured (us in a graph, one launch / chunks):
+//   choices    8 experts   256        1024       2048       4096       16384      65536
+//   1024                   3.8/6.7    4.1/7.2    5.0/8.3    6.9/8.7    17.0/8.9   55.5/8.8
+//   4096       4.4/6.8     4.5/7.6    4.8/8.3    6.3/9.9    8.5/9.9    21.9/9.9   68.8/10.0
+//   8192       5.5/7.2     6.5/8.0    12.3/9.3   18.6/10.5  31.6/10.6  105/10.7   407/11.8
+//   16384      5.3/7.3     6.2/8.3    10.9/10.6  16.5/11.9  27.3/12.1  87.9/12.6  333/21.9
+//   32768      7.4/7.4     9.0/9.0    14.2/9.7   22.0/10.9  36.4/11.0  115/12.3   438/35.5
+//   65536      19.0/7.5    13.9/10.1  21.6/10.9  33.2/12.4  55.1/12.8  172/22.2   659/74.0
+bool plan_in_chunks(int64_t n, int64_t E) { return E <= PLAN_E ? n >= 32768 : n > 4096 || E > 8192; }
 
 // ---------------------------------------------------------------------------
 // Combine: out[t] = bf16(sum_j weight[t, j] y[slot[t, j]]), fp32, j ascending; a slot
@@ -278,7 +342,9 @@ __global__ __launch_bounds__(256) void k_expert_combine(const uint16_t* __restri
 }  // namespace
 
 size_t expert_plan_bytes(int64_t n, int64_t E) {
-  return plan_in_chunks(n, E) ? (size_t)(4 * E * ((n + plan_chunk(n) - 1) / plan_chunk(n))) : 0;
+  if (!plan_in_chunks(n, E)) return 0;
+  const int64_t chunks = (n + plan_chunk(n) - 1) / plan_chunk(n);
+  return (size_t)(4 * chunks * (E + (E > PLAN_E ? plan_slices(E) : 0)));
 }
 
 hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
@@ -290,14 +356,21 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64
   token.mul = ((uint64_t{1} << token.shift) + (uint64_t)topk - 1) / (uint64_t)topk;
   if (plan_in_chunks(n, E)) {
     const int chunk = plan_chunk(n);
-    const dim3 chunks((unsigned)((n + chunk - 1) / chunk)), block(64 * PLAN_W);
+    const dim3 chunks((unsigned)((n + chunk - 1) / chunk), (unsigned)plan_slices(E)), block(64 * PLAN_W);
     int bits = 0;
-    while ((int64_t{1} << bits) < E) ++bits;
-    hipLaunchKernelGGL(k_expert_count, chunks, block, 0, stream, ids, (int)n, chunk, (int)E, counts);
+    while ((int64_t{1} << bits) < (E < PLAN_E ? E : PLAN_E)) ++bits;
+    if (E <= PLAN_E)
+      hipLaunchKernelGGL(k_expert_count<false>, chunks, block, 0, stream, ids, (int)n, chunk, (int)E, counts);
+    else
+      hipLaunchKernelGGL(k_expert_count<true>, chunks, block, 0, stream, ids, (int)n, chunk, (int)E, counts);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(k_expert_place, chunks, block, 0, stream, ids, (int)n, chunk, token, (int)E, bits, counts,
-                       row_index, slot, offsets);
+    if (E <= PLAN_E)
+      hipLaunchKernelGGL(k_expert_place<false>, chunks, block, 0, stream, ids, (int)n, chunk, token, (int)E, bits,
+                         counts, row_index, slot, offsets);
+    else
+      hipLaunchKernelGGL(k_expert_place<true>, chunks, block, 0, stream, ids, (int)n, chunk, token, (int)E, bits,
+                         counts, row_index, slot, offsets);
     return hipGetLastError();
   }
   // 4 wavefronts per expert while each still has at most 1024 choices, else 16
