@@ -126,6 +126,13 @@ __global__ __launch_bounds__(64 * W) void k_expert_plan(const int* __restrict__ 
 // ---------------------------------------------------------------------------
 constexpr int PLAN_E = 1024, PLAN_W = 16;
 
+// LDS accesses of a wavefront's lanes stay on their side of this point.  A wavefront's LDS
+// operations complete in order, so it costs no instruction.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ int wave_total(int v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
@@ -264,14 +271,17 @@ __global__ __launch_bounds__(64 * PLAN_W) void k_expert_place(const int* __restr
       const uint64_t b = __ballot(set);
       peers &= set ? b : ~b;
     }
+    int place = 0;
+    if (valid) place = next[wv][v] + __popcll(peers & earlier);
+    wave_order();  // the peers' reads before the first one's sum
     if (valid) {
-      const int place = next[wv][v] + __popcll(peers & earlier);
       slot[i] = place;
       row_index[place] = token((int)i);
-      if ((peers & earlier) == 0) atomicAdd(&next[wv][v], __popcll(peers));
+      if ((peers & earlier) == 0) next[wv][v] = place + __popcll(peers);
     } else if (i < hi && slice == 0 && id >= (uint32_t)E) {
       slot[i] = -1;
     }
+    wave_order();  // and that before the reads of the next 64
   }
   if (slice == 0)
     for (int64_t i = (int64_t)all + (int64_t)c * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS)
