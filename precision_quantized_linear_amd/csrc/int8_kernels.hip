@@ -4,9 +4,8 @@
 // Quantizer.  a = max_k |x[m, k]|, s = fp32(a / 127), q = rint(127 x / a), ties to even.
 // The sums of products are int32 and exact for K <= 2^17 (127 * 128 * 2^17 < 2^31), so a
 // result does not depend on how K is split over wavefronts or workgroups.
-#include <cmath>
-
 #include "qpl_gemm.h"
+#include "qpl_int8_shape.h"
 
 namespace qpl {
 
@@ -513,7 +512,7 @@ hipError_t launch_direct(Int8Args p, int64_t row_tiles, const Epilogue& ep, uint
 // A row is parts of 64 vectors of 8 elements; wavefront w takes the parts w, w + 16, ... of all
 // rows, up to TOKEN_SLOTS of them.
 // ---------------------------------------------------------------------------
-constexpr int TOKEN_W = 16, TOKEN_SLOTS = 2, TOKEN_PARTS = TOKEN_W * TOKEN_SLOTS, TOKEN_BYTES = TOKEN_PARTS * 512;
+constexpr int TOKEN_W = 16, TOKEN_SLOTS = TOKEN_PARTS / TOKEN_W, TOKEN_BYTES = TOKEN_PARTS * 512;
 
 template <bool SMOOTH, int EPI>
 __global__ __launch_bounds__(64 * TOKEN_W) void k_int8_token(const uint16_t* __restrict__ x,
@@ -925,56 +924,6 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t M, int64_t K, int64_t pi
 
 namespace {
 
-// ---------------------------------------------------------------------------
-// Which kernel multiplies.  A workgroup's time is about
-//   (pieces of 128 bytes of K) * piece + tile   microseconds
-// with the constants below, and the 256 CUs take the tiles in rounds; the shape with the least
-// time is taken.  The direct kernel's piece is its bytes at 42 KB/us (operand rows that do not
-// exist cost nothing), the staged kernel's was measured for each tile: about 60 KB/us of
-// operands up to 128 x 128, MFMAs and LDS reads above.  Measured, the best shape against the next ones (us):
-//   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 128x256 256x256
-//   1    4096 4096   5.3   7.0
-//   1    2048 6144   5.7   5.0   5.1   7.5
-//   16   4096 12288  16.9  15.7        14.3
-//   64   4096 4096   13    12.1  10.2  12.4
-//   64   8192 1024   9.6   12.7  16.4  21.1
-//   256  1024 6144                     7.7   6.8    8.0     9.0
-//   515  2080 5003                     18.4  18.8   16.7    19.4
-//   512  4096 12288                                 40.4    35.6    51
-//   1025 4096 4096                           36.3   39.2    32.6
-//   1536 4096 12288                                 104     94.5    95.9
-//   4608 4096 12288                                 258     245     223
-// ---------------------------------------------------------------------------
-struct Shape {
-  int rows, cols;
-  double piece, tile;
-};
-constexpr Shape kShapes[] = {{16, 16, 0, 0.25},    {16, 32, 0, 0.5},      {32, 32, 0, 0.5},      {64, 64, 0.28, 0.5},
-                             {64, 128, 0.46, 1.0}, {128, 128, 0.62, 2.0}, {128, 256, 1.0, 3.7}, {256, 256, 1.6, 8}};
-constexpr int kNumShapes = 8;
-
-// tiles_m(rows): row tiles of that height; rows_each: rows that a row tile has at most; part:
-// workgroups end at different times (grouped tiles differ in rows), so rounds are not whole.
-template <class F>
-int pick_shape(const F& tiles_m, double rows_each, int64_t K, int64_t N, bool part) {
-  int best = 0;
-  double least = 0;
-  for (int v = 0; v < kNumShapes; ++v) {
-    const Shape& s = kShapes[v];
-    const double tiles = tiles_m(s.rows) * (double)((N + s.cols - 1) / s.cols) / 256;
-    const double left = tiles - __builtin_floor(tiles);  // of the last round; staged tiles are cut in it
-    const double last = left == 0 ? 0 : s.rows >= 256 && left <= 0.25 ? 0.6 : s.rows >= 128 && left <= 0.5 ? 0.8 : 1;
-    const double rounds = part ? (tiles + 0.4 > 1 ? tiles + 0.4 : 1) : tiles - left + last;
-    const double piece = s.piece > 0 ? s.piece : ((rows_each < s.rows ? rows_each : s.rows) + s.cols) * 128 / 42e3;
-    const double t = rounds * ((double)((K + 127) / 128) * piece + s.tile);
-    if (v == 0 || t < least) {
-      best = v;
-      least = t;
-    }
-  }
-  return best;
-}
-
 template <bool GROUPED>
 hipError_t launch_shape(int v, const Int8Args& p, int64_t row_tiles, const Epilogue& ep, uint16_t* y,
                         hipStream_t stream) {
@@ -988,9 +937,7 @@ hipError_t launch_shape(int v, const Int8Args& p, int64_t row_tiles, const Epilo
     case 3: return launch_staged<1, 1, 4, GROUPED>(p, row_tiles, ep, y, stream);
     case 4: return launch_staged<2, 1, 3, GROUPED>(p, row_tiles, ep, y, stream);
     case 5:
-      // one workgroup per CU with four stages, or past 256 tiles two with two stages: 192 tiles of
-      // K = 2048 take 13.5 against 15.6 us, 384 of them 24.6 against 19.1 us
-      if (row_tiles * ((p.N + 127) / 128) <= 256) return launch_staged<2, 2, 4, GROUPED>(p, row_tiles, ep, y, stream);
+      if (four_stages(row_tiles, p.N)) return launch_staged<2, 2, 4, GROUPED>(p, row_tiles, ep, y, stream);
       return launch_staged<2, 2, 2, GROUPED>(p, row_tiles, ep, y, stream);
     case 6: return launch_staged<4, 2, 3, GROUPED>(p, row_tiles, ep, y, stream);
     default: return launch_staged<4, 4, 2, GROUPED>(p, row_tiles, ep, y, stream);
@@ -1024,9 +971,7 @@ hipError_t launch_token(const uint16_t* x, const float* lam, const Int8Args& p, 
 
 }  // namespace
 
-// Half as many elements again would lose: with four parts per wavefront 16 x 2048 x 6144 took 10.6 us,
-// its two launches 8.3 us; with two, 16 x 1024 x 4096 takes 6.1 us either way.
-bool int8_token_fits(int64_t M, int64_t K) { return M <= 16 && M * ((K / 8 + 63) / 64) <= TOKEN_PARTS; }
+bool int8_token_fits(int64_t M, int64_t K) { return token_fits(M, K); }
 
 hipError_t launch_int8_token(const uint16_t* x, int64_t M, int64_t K, int64_t N, const int8_t* w, const float* ws,
                              const float* lam, const Epilogue& ep, uint16_t* y, hipStream_t stream) {
@@ -1050,26 +995,9 @@ hipError_t launch_gemm_int8(const int8_t* xq, const float* xs, const int8_t* w, 
   p.N = N;
   p.K = (int)K;
   p.px = (int)int8_pitch(K);
-  const int v = pick_shape([&](int rows) { return (double)((M + rows - 1) / rows); }, (double)M, K, N, false);
+  const int v = dense_shape(M, K, N);
   return launch_shape<false>(v, p, (M + kShapes[v].rows - 1) / kShapes[v].rows, ep, y, stream);
 }
-
-// The shape of a grouped product.  The host knows the number of rows, not how the experts share
-// them: of E experts that R rows are dealt to, E (1 - (1 - 1/E)^R) have any, and half a tile more
-// than R / rows for each of them is a fair guess.
-static int grouped_shape(int64_t R, int64_t K, int64_t N, int64_t E) {
-  const double used = (double)E * -std::expm1((double)R * std::log1p(-1.0 / (double)(E > 1 ? E : 2)));
-  const double some = E > 1 ? (used > 1 ? used : 1) : 1;
-  return pick_shape(
-      [&](int rows) {
-        const double t = (double)R / rows + some / 2;
-        return t > some ? t : some;
-      },
-      (double)R / some, K, N, true);
-}
-
-// Row tiles of a grouped product: every expert with rows has at most one that is not full.
-static int64_t row_tile_bound(int64_t R, int64_t E, int rows) { return R / rows + (E < R ? E : R); }
 
 int64_t grouped_row_tiles(int64_t R, int64_t E) { return row_tile_bound(R, E, kShapes[0].rows); }
 

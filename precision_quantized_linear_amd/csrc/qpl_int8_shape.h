@@ -1,0 +1,92 @@
+// Which kernel multiplies an 8-bit integer linear: host arithmetic on the sizes alone.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+namespace qpl {
+
+// A few rows in one launch (k_int8_token): up to 16, of up to TOKEN_PARTS parts of 512 elements
+// together.  Half as many elements again would lose: with four parts per wavefront
+// 16 x 2048 x 6144 took 10.6 us, its two launches 8.3 us; with two, 16 x 1024 x 4096 takes
+// 6.1 us either way.
+constexpr int TOKEN_PARTS = 32;
+inline bool token_fits(int64_t M, int64_t K) { return M <= 16 && M * ((K / 8 + 63) / 64) <= TOKEN_PARTS; }
+
+// ---------------------------------------------------------------------------
+// Which kernel multiplies.  A workgroup's time is about
+//   (pieces of 128 bytes of K) * piece + tile   microseconds
+// with the constants below, and the 256 CUs take the tiles in rounds; the shape with the least
+// time is taken.  The direct kernel's piece is its bytes at 42 KB/us (operand rows that do not
+// exist cost nothing), the staged kernel's was measured for each tile: about 60 KB/us of
+// operands up to 128 x 128, MFMAs and LDS reads above.  Measured, the best shape against the next ones (us):
+//   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 128x256 256x256
+//   1    4096 4096   5.3   7.0
+//   1    2048 6144   5.7   5.0   5.1   7.5
+//   16   4096 12288  16.9  15.7        14.3
+//   64   4096 4096   13    12.1  10.2  12.4
+//   64   8192 1024   9.6   12.7  16.4  21.1
+//   256  1024 6144                     7.7   6.8    8.0     9.0
+//   515  2080 5003                     18.4  18.8   16.7    19.4
+//   512  4096 12288                                 40.4    35.6    51
+//   1025 4096 4096                           36.3   39.2    32.6
+//   1536 4096 12288                                 104     94.5    95.9
+//   4608 4096 12288                                 258     245     223
+// ---------------------------------------------------------------------------
+struct Shape {
+  int rows, cols;
+  double piece, tile;
+};
+constexpr Shape kShapes[] = {{16, 16, 0, 0.25},    {16, 32, 0, 0.5},      {32, 32, 0, 0.5},      {64, 64, 0.28, 0.5},
+                             {64, 128, 0.46, 1.0}, {128, 128, 0.62, 2.0}, {128, 256, 1.0, 3.7}, {256, 256, 1.6, 8}};
+constexpr int kNumShapes = 8;
+
+// tiles_m(rows): row tiles of that height; rows_each: rows that a row tile has at most; part:
+// workgroups end at different times (grouped tiles differ in rows), so rounds are not whole.
+template <class F>
+int pick_shape(const F& tiles_m, double rows_each, int64_t K, int64_t N, bool part) {
+  int best = 0;
+  double least = 0;
+  for (int v = 0; v < kNumShapes; ++v) {
+    const Shape& s = kShapes[v];
+    const double tiles = tiles_m(s.rows) * (double)((N + s.cols - 1) / s.cols) / 256;
+    const double left = tiles - __builtin_floor(tiles);  // of the last round; staged tiles are cut in it
+    const double last = left == 0 ? 0 : s.rows >= 256 && left <= 0.25 ? 0.6 : s.rows >= 128 && left <= 0.5 ? 0.8 : 1;
+    const double rounds = part ? (tiles + 0.4 > 1 ? tiles + 0.4 : 1) : tiles - left + last;
+    const double piece = s.piece > 0 ? s.piece : ((rows_each < s.rows ? rows_each : s.rows) + s.cols) * 128 / 42e3;
+    const double t = rounds * ((double)((K + 127) / 128) * piece + s.tile);
+    if (v == 0 || t < least) {
+      best = v;
+      least = t;
+    }
+  }
+  return best;
+}
+
+// Shape of a product of M rows.
+inline int dense_shape(int64_t M, int64_t K, int64_t N) {
+  return pick_shape([&](int rows) { return (double)((M + rows - 1) / rows); }, (double)M, K, N, false);
+}
+
+// The shape of a grouped product.  The host knows the number of rows, not how the experts share
+// them: of E experts that R rows are dealt to, E (1 - (1 - 1/E)^R) have any, and half a tile more
+// than R / rows for each of them is a fair guess.
+inline int grouped_shape(int64_t R, int64_t K, int64_t N, int64_t E) {
+  const double used = (double)E * -std::expm1((double)R * std::log1p(-1.0 / (double)(E > 1 ? E : 2)));
+  const double some = E > 1 ? (used > 1 ? used : 1) : 1;
+  return pick_shape(
+      [&](int rows) {
+        const double t = (double)R / rows + some / 2;
+        return t > some ? t : some;
+      },
+      (double)R / some, K, N, true);
+}
+
+// Row tiles of a grouped product: every expert with rows has at most one that is not full.
+inline int64_t row_tile_bound(int64_t R, int64_t E, int rows) { return R / rows + (E < R ? E : R); }
+
+// 128 x 128 tiles: one workgroup per CU with four stages, or past 256 tiles two with two stages:
+// 192 tiles of K = 2048 take 13.5 against 15.6 us, 384 of them 24.6 against 19.1 us.
+inline bool four_stages(int64_t row_tiles, int64_t N) { return row_tiles * ((N + 127) / 128) <= 256; }
+
+}  // namespace qpl
