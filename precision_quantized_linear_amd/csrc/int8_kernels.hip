@@ -14,7 +14,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // Row quantizer: one wavefront per row and four rows per workgroup, or (SPLIT) a workgroup
 // per row when there are too few rows to fill the chip; VPT 16-byte vectors per lane stay in
-// registers between the two passes (VPT == 0 streams the row twice).
+// registers between the two passes (VPT == 0, for rows that SPLIT does not hold either, streams the row twice).
 //
 // The code is rint of the exact quotient 127 x / a.  x = i 2^p and a = j 2^q have 8-bit
 // integers i, j, so 127 x / a either is a tie (k + 1/2, at most 8 significant bits) or
@@ -303,23 +303,19 @@ hipError_t launch_quant_rows(const uint16_t* x, int64_t rows_x, int64_t rows, in
   if constexpr (SPLIT) {
     QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(0)
   } else {
-    QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(16) QPL_CASE(24) QPL_CASE(0)
+    QPL_CASE(1) QPL_CASE(2) QPL_CASE(4) QPL_CASE(8) QPL_CASE(16) QPL_CASE(24)  // split_rows takes the longer ones
   }
 #undef QPL_CASE
   return hipErrorInvalidValue;
 }
 
-// A workgroup per row up to kSplitRows rows: 24 x 4096 with smoothing 4.7 us, with a wavefront per
-// row 10.6 us; 16384 x 2048 gathered 22.2 and 17.9 us.
-constexpr int64_t kSplitRows = 2048;
-
 template <bool SMOOTH, bool GROUPED, bool GATHER>
 hipError_t launch_quant(const uint16_t* x, int64_t rows_x, int64_t rows, int64_t K, int64_t pitch, const float* lam,
                         const int* row_index, int8_t* xq, float* xs, const TilePlan& plan, hipStream_t stream) {
-  return rows <= kSplitRows && K > 512 ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(
-                                             x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream)
-                                       : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(
-                                             x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream);
+  return split_rows(rows, K, GATHER) ? launch_quant_rows<SMOOTH, GROUPED, GATHER, true>(
+                                           x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream)
+                                     : launch_quant_rows<SMOOTH, GROUPED, GATHER, false>(
+                                           x, rows_x, rows, K, pitch, lam, row_index, xq, xs, plan, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -13,6 +13,27 @@ namespace qpl {
 constexpr int TOKEN_PARTS = 32;
 inline bool token_fits(int64_t M, int64_t K) { return M <= 16 && M * ((K / 8 + 63) / 64) <= TOKEN_PARTS; }
 
+// The row quantizer: a workgroup per row (true) or a wavefront per row.  A wavefront holds rows of up to
+// 12288 elements in registers and would read longer ones twice; below that, a workgroup per row pays
+// while rows are too few to fill the chip, up to more of them the longer they are.  Gathered rows come
+// from the caches and pay sooner by the wavefront.  Measured (us in a graph, wavefront / workgroup):
+//   rows     K 512    1024     2048     4096       8192       16384
+//   16       2.4/2.6  2.7/2.7  3.0/2.7  3.6/2.8    5.0/3.2    14.8/4.0
+//   256      2.6/2.8  3.1/3.1  3.1/2.8  4.1/3.3    6.2/3.8    22.7/5.4
+//   1024     2.7/3.4  2.9/3.4  3.5/3.6  5.3/4.7    8.5/7.4    38.3/11.6
+//   2048     2.8/3.8  3.4/3.9  5.2/5.2  7.8/7.0    12.9/10.8  45.7/19.0
+//   4096     3.6/5.5  4.9/6.4  7.3/8.0  11.5/11.4  21.4/18.6  58.4/35.1
+//   8192     4.8/8.9  7.3/10.5 10.9/13.0 19.0/18.8 36.4/34.0  110.6/62.9
+// gathered, each row four times:
+//   256      2.7/2.9  2.9/2.9  3.2/3.0  3.9/3.2    5.3/3.7    15.6/5.5
+//   1024     2.8/3.2  3.1/3.3  3.5/3.8  4.3/5.1    6.2/7.3    22.1/11.3
+//   4096     3.5/5.6  4.3/6.4  5.4/7.4  9.0/11.4   13.2/17.5  29.7/32.1
+// Smoothed rows take the plain rows' rule: 4096 elements 9.9/6.5 for 1024 rows, 17.8/16.4 for 4096.
+inline bool split_rows(int64_t rows, int64_t K, bool gathered) {
+  if (K > 12288) return true;
+  return K > 512 && rows <= (gathered ? K / 8 : K / 2);
+}
+
 // ---------------------------------------------------------------------------
 // Which kernel multiplies.  A workgroup's time is about
 //   (pieces of 128 bytes of K) * piece + tile   microseconds

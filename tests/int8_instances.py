@@ -26,6 +26,7 @@ extern "C" int grouped(int64_t R, int64_t K, int64_t N, int64_t E) {
   const int v = grouped_shape(R, K, N, E);
   return instance(v, row_tile_bound(R, E, kShapes[v].rows), N);
 }
+extern "C" int split(int64_t rows, int64_t K, int gathered) { return split_rows(rows, K, gathered != 0); }
 """
 
 
@@ -39,6 +40,7 @@ def rule():
         lib = ctypes.CDLL(so)
     lib.dense.argtypes = [ctypes.c_int64] * 3
     lib.grouped.argtypes = [ctypes.c_int64] * 4
+    lib.split.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
     return lib
 
 
@@ -49,3 +51,8 @@ def dense(M, K, N):
 
 def grouped(R, K, N, E):
     return NAMES[rule().grouped(R, K, N, E)]
+
+
+def split(rows, K, gathered):
+    """Does the row quantizer take a workgroup per row (or a wavefront)?"""
+    return bool(rule().split(rows, K, gathered))
