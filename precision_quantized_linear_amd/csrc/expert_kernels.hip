@@ -296,15 +296,23 @@ int plan_chunk(int64_t n) {
 
 int plan_slices(int64_t E) { return (int)((E + PLAN_E - 1) / PLAN_E); }
 
-// Which form, with both measured (us in a graph, one launch / chunks):
-//   choices    8 experts   256        1024       2048       4096       16384      65536
-//   1024                   3.8/6.7    4.1/7.2    5.0/8.3    6.9/8.7    17.0/8.9   55.5/8.8
-//   4096       4.4/6.8     4.5/7.6    4.8/8.3    6.3/9.9    8.5/9.9    21.9/9.9   68.8/10.0
-//   8192       5.5/7.2     6.5/8.0    12.3/9.3   18.6/10.5  31.6/10.6  105/10.7   407/11.8
-//   16384      5.3/7.3     6.2/8.3    10.9/10.6  16.5/11.9  27.3/12.1  87.9/12.6  333/21.9
-//   32768      7.4/7.4     9.0/9.0    14.2/9.7   22.0/10.9  36.4/11.0  115/12.3   438/35.5
-//   65536      19.0/7.5    13.9/10.1  21.6/10.9  33.2/12.4  55.1/12.8  172/22.2   659/74.0
-bool plan_in_chunks(int64_t n, int64_t E) { return E <= PLAN_E ? n >= 32768 : n > 4096 || E > 8192; }
+// Which form.  One launch reads all choices once per expert, chunks cost a second launch.  In the one
+// launch an expert's workgroup has 4 wavefronts, or 16, of which not all workgroups are on the chip
+// at once past some hundred experts.  Measured, us in a graph (4 wavefronts / 16 / chunks):
+//   choices  64 experts      256            512             1024            2048            8192           65536
+//   1024     3.6/3.5/6.5     3.6/3.6/6.8    3.7/4.7/6.9     3.9/6.5/7.3     4.9/9.9/8.4     9.6/31/9.0     55/-/8.8
+//   4096     4.2/4.2/7.0     4.2/4.4/7.6    4.3/6.1/7.9     4.7/8.4/8.6     6.2/13/9.8      12.2/39/10.2   69/-/10.0
+//   8192     5.8/5.5/7.5     5.8/6.2/8.0    5.9/8.9/8.6     6.6/12.3/9.4    8.6/19/10.5     17.3/54/10.6   -/407/11.8
+//   12288    7.2/6.7/7.6     7.5/7.6/8.2    7.5/10.8/8.8    8.2/14.5/10.1   11.1/22/11.2    22/66/11.6
+//   16384    8.7/5.0/7.6     8.8/5.9/8.4    9.0/7.8/9.1     9.7/10.7/10.8   13.4/16.1/12.0  28/47/12.2     -/333/21.9
+//   24576    11.6/7.2/7.7    11.9/8.8/8.7   12.1/11.6/9.7   13.2/16.0/11.6  17.9/23/12.9    38/70/13.6
+//   32768    14.7/6.4/7.8    14.9/7.9/9.0   15.3/10.3/10.2  16.5/14.0/9.7   22/20/10.9      48/61/11.5     -/438/35.5
+//   65536    -/13.1/8.2      -/13.8/10.1                    -/22/10.9       -/33/12.4                      -/659/74.0
+bool plan_in_chunks(int64_t n, int64_t E) {
+  return E <= 256 ? n >= 32768 : E > 8192 || n > 12288 || n * E > int64_t(1) << 24;
+}
+
+bool plan_by_four(int64_t n, int64_t E) { return n <= 4096 || E > 256; }
 
 // ---------------------------------------------------------------------------
 // Combine: out[t] = bf16(sum_j weight[t, j] y[slot[t, j]]), fp32, j ascending; a slot
@@ -383,8 +391,7 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64
                          counts, row_index, slot, offsets);
     return hipGetLastError();
   }
-  // 4 wavefronts per expert while each still has at most 1024 choices, else 16
-  if (n <= 4096)
+  if (plan_by_four(n, E))
     hipLaunchKernelGGL((k_expert_plan<4, 8>), grid, dim3(256), 0, stream, ids, (int)n, token, (int)E, row_index, slot,
                        offsets);
   else

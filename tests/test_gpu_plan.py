@@ -45,14 +45,16 @@ def test_the_sort_is_the_plan():
 
 def test_no_plan_reads_all_choices_for_each_of_many_experts():
     # the form without a workspace reads all choices once per expert: only where that is little
-    for T, topk, E in ((1 << 20, 2, 2049), (1 << 20, 8, 65536), ((1 << 23) - 256, 255, 65536), (4097, 1, 1025),
-                       (1, 1, 65536)):
+    for T, topk, E in ((1 << 20, 2, 2049), (1 << 20, 8, 65536), ((1 << 23) - 256, 255, 65536), (4097, 1, 4096),
+                       (1, 1, 65536), (12289, 1, 257)):
         assert qpl.expert_plan_workspace_bytes(T, topk, E) > 0, (T, topk, E)
-    for T, topk, E in ((4096, 1, 8192), (32767, 1, 1024), (1, 1, 1)):
+    for T, topk, E in ((2048, 1, 8192), (6144, 2, 1024), (8192, 1, 2048), (32767, 1, 256), (1, 1, 1)):
         assert qpl.expert_plan_workspace_bytes(T, topk, E) == 0, (T, topk, E)
 
 
-SIZES = [(1, 1, 65536, "random"), (1, 1, 8193, "last"), (4096, 1, 8192, "invalid"), (4097, 1, 1025, "invalid"),
+SIZES = [(4096, 3, 1024, "invalid"), (12289, 1, 257, "invalid"), (12288, 1, 256, "random"), (6000, 2, 700, "last"),
+         (8192, 1, 2048, "border"), (2048, 1, 8192, "invalid"), (8193, 4, 513, "random"), (15000, 2, 256, "none"),
+         (1, 1, 65536, "random"), (1, 1, 8193, "last"), (4096, 1, 8192, "invalid"), (4097, 1, 1025, "invalid"),
          (4097, 1, 2048, "border"), (2049, 2, 2049, "border"), (33, 7, 9000, "invalid"), (700, 8, 65535, "border"),
          (3000, 3, 4097, "last"), (3000, 3, 4097, "none"), (20011, 5, 1500, "invalid"), (1 << 20, 2, 2049, "invalid"),
          (70000, 8, 65536, "invalid"), (1 << 19, 3, 1025, "border")]
