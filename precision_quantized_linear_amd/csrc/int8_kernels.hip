@@ -217,8 +217,14 @@ __global__ __launch_bounds__(256) void k_quant_int8(const uint16_t* __restrict__
 // ---------------------------------------------------------------------------
 // Plan and first quantizer of the MLP of experts for few choices, in one launch: with up to
 // FRONT_N of them a workgroup finds the place of its choice by looking at all others, and writes
-// that token's codes there.  Workgroup 0 makes the offsets and the row tiles.  28 choices of K = 2048:
-// 4.4 us where the two launches take 3.3 + 3.6 us and the gap between them.
+// that token's codes there.  Workgroup 0 makes the offsets and the row tiles.  The search grows with
+// the square of the choices; measured, us in a graph (this launch / plan and quantizer), for 64 experts:
+//   choices   28       256      1024     2048       4096
+//   K 256     3.3/5.1  3.4/5.5  4.1/6.2  6.0/6.2    11.3/7.3
+//   K 2048    3.3/5.3  3.5/5.7  4.4/6.7  7.1/7.9    13.3/9.6
+//   K 8192    4.4/5.9  4.7/6.5  6.3/8.6  13.3/13.1  28.1/21.7
+// and for 1024 experts 1024 choices of K = 2048 5.9/8.4, 2048 of them 7.0/8.6.  FRONT_E experts are what
+// workgroup 0 sums at four per thread.
 // ---------------------------------------------------------------------------
 constexpr int FRONT_N = 1024, FRONT_E = 1024;
 
