@@ -47,7 +47,7 @@ typedef enum {
   QPL_OK = 0,
   QPL_ERR_NULL = 1,      /* a required pointer is NULL */
   QPL_ERR_SHAPE = 2,     /* M or N < 1, K < 16, K % 16 != 0, R outside [0, 128], or a size overflows */
-  QPL_ERR_ALIGN = 3,     /* a pointer is not 16-byte aligned */
+  QPL_ERR_ALIGN = 3,     /* a pointer is not 16-byte aligned (4-byte for the arrays that say so) */
   QPL_ERR_ARG = 4,       /* a scale is not finite and > 0, unknown scheme, or low-rank pointers inconsistent with R */
   QPL_ERR_WORKSPACE = 5, /* ws_bytes < qlinear_workspace_bytes(...) */
   QPL_ERR_DEVICE = 6,    /* no HIP device, or the current device is not gfx950 */
@@ -407,7 +407,7 @@ qpl_status dequant_weight(qpl_scheme scheme, const uint8_t* weight, const void* 
                           uint16_t* w_bf16, void* stream);
 
 /* Bytes of scratch that the scheme's linear needs for these sizes
- * (0 if the sizes are invalid).  The scratch may be reused between calls that
+ * (0 if the sizes are invalid, and for INT8 also where none is needed).  The scratch may be reused between calls that
  * are ordered on one stream. */
 size_t qlinear_workspace_bytes(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R);
 

@@ -40,19 +40,22 @@ inline bool split_rows(int64_t rows, int64_t K, bool gathered) {
 // with the constants below, and the 256 CUs take the tiles in rounds; the shape with the least
 // time is taken.  The direct kernel's piece is its bytes at 42 KB/us (operand rows that do not
 // exist cost nothing), the staged kernel's was measured for each tile: about 60 KB/us of
-// operands up to 128 x 128, MFMAs and LDS reads above.  Measured, the best shape against the next ones (us):
+// operands up to 128 x 128, MFMAs and LDS reads above.  Measured (us):
 //   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 128x256 256x256
-//   1    4096 4096   5.3   7.0
-//   1    2048 6144   5.7   5.0   5.1   7.5
-//   16   4096 12288  16.9  15.7        14.3
-//   64   4096 4096   13    12.1  10.2  12.4
-//   64   8192 1024   9.6   12.7  16.4  21.1
-//   256  1024 6144                     7.7   6.8    8.0     9.0
-//   515  2080 5003                     18.4  18.8   16.7    19.4
-//   512  4096 12288                                 40.4    35.6    51
-//   1025 4096 4096                           36.3   39.2    32.6
-//   1536 4096 12288                                 104     94.5    95.9
-//   4608 4096 12288                                 258     245     223
+//   1    4096 4096   5.9   7.6   7.9   13.2  15.0   17.5
+//   1    2048 6144   7.3   5.4   5.7   8.6   9.6    11.1
+//   16   4096 12288  19.3  17.8  18.9  14.5  19.4   19.1
+//   64   4096 4096   21.0  13.7  10.5  13.2  15.4   17.6
+//   64   8192 1024   10.2  13.4  17.1  22.5  26.4   29.8
+//   256  1024 6144   50.6  25.5  17.2  8.5   7.4    8.5     10.5    13.2
+//   515  2080 5003   114   56    39.7  18.6  18.6   16.4    19.8    25.0
+//   512  4096 12288  456   258   176   54.5  43.7   41.9    35.6    48.2
+//   1025 4096 4096                     39.4  35.2   31.2    32.0    38.9
+//   1536 4096 12288                    157   109    97.4    93.9    95.5
+//   4096 4096 12288                    381   284    216     207     188
+//   4608 4096 12288                    429   313    249     239     222
+// (a launch in a graph, the weight from HBM where it is larger than the caches).  Of 65 random sizes, dense and grouped, the one taken was
+// within 9 % of the best for 55, and 10 to 23 % behind it for ten.
 // ---------------------------------------------------------------------------
 struct Shape {
   int rows, cols;
