@@ -344,7 +344,8 @@ qpl_status qlinear_int8_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N,
  *   offsets     int32 [E + 1]    out: expert e has the places offsets[e] .. offsets[e+1] - 1
  *   Places of one expert are in order of (token, choice).
  *   ws          at least expert_plan_workspace_bytes(T, topk, E) bytes (0 for few choices of not
- *               too many experts: ws may then be NULL)
+ *               too many experts: ws may then be NULL).  It may also be NULL with T topk < 32768 or
+ *               E > 1024 if T topk E <= 2^35: the plan then reads all choices once per expert
  *
  * qlinear_grouped_int8: product row i of R, offsets[e] <= i < offsets[e+1], is
  *   y[i] = bf16_rne(act((sum_k q_x q_w[e]) s_x weight_scale[e]))

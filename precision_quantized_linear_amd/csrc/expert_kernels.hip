@@ -312,6 +312,12 @@ bool plan_in_chunks(int64_t n, int64_t E) {
   return E <= 256 ? n >= 32768 : E > 8192 || n > 12288 || n * E > int64_t(1) << 24;
 }
 
+// Plans that needed no workspace while one launch was the rule for them still run without one, as far as
+// their n E reads end in some milliseconds (2^32 of them take 0.7).
+bool plan_in_one(int64_t n, int64_t E) {
+  return !plan_in_chunks(n, E) || ((n < 32768 || E > PLAN_E) && n * E <= int64_t(1) << 35);
+}
+
 bool plan_by_four(int64_t n, int64_t E) { return n <= 4096 || E > 256; }
 
 // ---------------------------------------------------------------------------
@@ -365,6 +371,8 @@ size_t expert_plan_bytes(int64_t n, int64_t E) {
   return (size_t)(4 * chunks * (E + (E > PLAN_E ? plan_slices(E) : 0)));
 }
 
+bool expert_plan_needs_none(int64_t n, int64_t E) { return plan_in_one(n, E); }
+
 hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
                               int32_t* slot, int32_t* offsets, int32_t* counts, hipStream_t stream) {
   const dim3 grid((unsigned)(E + 1));
@@ -372,7 +380,7 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64
   token.shift = 31;
   while ((int64_t{1} << (token.shift - 31)) < topk) ++token.shift;
   token.mul = ((uint64_t{1} << token.shift) + (uint64_t)topk - 1) / (uint64_t)topk;
-  if (plan_in_chunks(n, E)) {
+  if (counts && plan_in_chunks(n, E)) {
     const int chunk = plan_chunk(n);
     const dim3 chunks((unsigned)((n + chunk - 1) / chunk), (unsigned)plan_slices(E)), block(64 * PLAN_W);
     int bits = 0;

@@ -832,8 +832,8 @@ QPL_EXPORT qpl_status expert_plan(const int32_t* expert_ids, int64_t T, int64_t 
   if (s != QPL_OK) return s;
   if (E < 1 || E > kMaxExperts) return QPL_ERR_SHAPE;
   const size_t need = qpl::expert_plan_bytes(T * topk, E);
-  if (need > 0 && !ws) return QPL_ERR_NULL;
-  if (ws_bytes < need) return QPL_ERR_WORKSPACE;
+  if (!ws && !qpl::expert_plan_needs_none(T * topk, E)) return QPL_ERR_NULL;
+  if (ws && ws_bytes < need) return QPL_ERR_WORKSPACE;
   if ((s = check_device()) != QPL_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return launched(Timed(QPL_KERNEL_EXPERT_PLAN, st)(qpl::launch_expert_plan(

@@ -146,9 +146,10 @@ hipError_t launch_int8_moe_front(const int32_t* ids, int64_t n, int64_t topk, co
 hipError_t launch_gemm_int8_grouped(const int8_t* xq, const float* xs, const int8_t* w, const float* ws, int64_t R,
                                     int64_t K, int64_t N, int64_t E, const int32_t* tiles, const Epilogue& ep,
                                     uint16_t* y, hipStream_t stream);
-// Routing: choices ids [n] sorted by expert (counts: expert_plan_bytes(n, E) of scratch), and
-// the experts' rows summed per token.
+// Routing: choices ids [n] sorted by expert (counts: expert_plan_bytes(n, E) of scratch, or nullptr
+// where expert_plan_needs_none), and the experts' rows summed per token.
 size_t expert_plan_bytes(int64_t n, int64_t E);
+bool expert_plan_needs_none(int64_t n, int64_t E);
 hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64_t E, int32_t* row_index,
                               int32_t* slot, int32_t* offsets, int32_t* counts, hipStream_t stream);
 hipError_t launch_expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot, const float* weights,

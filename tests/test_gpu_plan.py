@@ -99,3 +99,35 @@ def test_slices_in_a_graph_and_in_the_mlp():
         h = qpl.qlinear_grouped_int8(x, f1["weight"], f1["weight_scale"], offsets, row_index=row_index, act="gelu_tanh")
         y = qpl.expert_combine(qpl.qlinear_grouped_int8(h, f2["weight"], f2["weight_scale"], offsets), slot, wt)
         assert torch.equal(qpl.qlinear_moe_int8(x, ids, wt, f1, f2), y) and bool(y.any())
+
+
+def test_refusals_without_a_workspace():
+    # no device: a call that passes every check before it reports that
+    if torch.cuda.is_available():
+        pytest.skip("forces the no-device status; a GPU is present")
+    import ctypes
+    lib, p = qpl.load(), ctypes.c_void_p(1 << 20)
+    null, device = 1, 6
+    for T, topk, E, want in ((4, 2, 65536, device), (32767, 1, 1024, device), (1 << 19, 1, 65536, device),
+                             ((1 << 19) + 1, 1, 65536, null), (1 << 20, 8, 65536, null), (32768, 1, 1024, null),
+                             (1 << 16, 2, 300, null)):
+        assert lib.expert_plan(p, T, topk, E, p, p, p, None, 0, None) == want, (T, topk, E)
+        need = qpl.expert_plan_workspace_bytes(T, topk, E)
+        assert need > 0 and lib.expert_plan(p, T, topk, E, p, p, p, p, need - 1, None) == 5
+        assert lib.expert_plan(p, T, topk, E, p, p, p, p, need, None) == device
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,topk,E,kind", [(4, 2, 65536, "invalid"), (20011, 1, 700, "invalid"), (9000, 3, 1500, "border"),
+                                           (5000, 2, 4097, "last")])
+def test_plan_without_a_workspace(T, topk, E, kind):
+    assert qpl.expert_plan_workspace_bytes(T, topk, E) > 0
+    ids = draw(T, topk, E, kind)
+    d = to_dev(ids)
+    outs = [torch.full((k,), 7, dtype=torch.int32, device="cuda") for k in (T * topk, T * topk, E + 1)]
+    status = qpl.load().expert_plan(d.data_ptr(), T, topk, E, *(t.data_ptr() for t in outs), None, 0,
+                                    torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == 0
+    for name, got, want in zip(("row_index", "slot", "offsets"), outs, sorted_plan(ids, E)):
+        assert np.array_equal(host(got), want.reshape(-1)), name
