@@ -27,7 +27,7 @@
  * - Size limits of the linears (QPL_ERR_SHAPE beyond them): the GEMMs address a
  *   256-row tile of an operand with 32-bit offsets below 2^30, so K < 2^22 for
  *   fp8r and INT4 (K-byte rows) and K < 2^23 for nvfp4 (K/2-byte rows); INT8 has
- *   K <= 2^17, which keeps its int32 sums exact; with a
+ *   K <= 2^17, which keeps its int32 sums exact, FP8B K < 2^22; with a
  *   low-rank branch (R > 0) K <= 2^21 and the activation's scales (8 M ceil(K/128)
  *   bytes for nvfp4, 4 M K/64 for INT4) below 2^31 bytes.
  * - Inputs must be finite: NaN or infinity in x or W is outside the contract.
@@ -54,7 +54,7 @@ typedef enum {
   QPL_ERR_LAUNCH = 7     /* the HIP runtime rejected a kernel launch */
 } qpl_status;
 
-typedef enum { QPL_FP8R = 0, QPL_NVFP4 = 1, QPL_INT4 = 2, QPL_INT8 = 3 } qpl_scheme;
+typedef enum { QPL_FP8R = 0, QPL_NVFP4 = 1, QPL_INT4 = 2, QPL_INT8 = 3, QPL_FP8B = 4 } qpl_scheme;
 
 /*
  * Row-wise FP8 quantization (guide "BFL (fp8r / nvfp4)", intro bullet on fp8r:
@@ -249,7 +249,7 @@ qpl_status qlinear_awq_w4a16(const uint16_t* x, int64_t M, int64_t K, int64_t N,
  * QPL_ERR_NULL for one or two of q, k, v, or for y NULL without them,
  * QPL_ERR_SHAPE for the QKV shape conditions above.
  */
-typedef enum { QPL_ACT_NONE = 0, QPL_ACT_GELU_TANH = 1 } qpl_act;
+typedef enum { QPL_ACT_NONE = 0, QPL_ACT_GELU_TANH = 1, QPL_ACT_SILU = 2 /* gated blocks only */ } qpl_act;
 
 typedef struct {
   qpl_act act;
@@ -393,6 +393,130 @@ qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, 
                             uint16_t* y, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Block-scaled fp8 (FP8B): E4M3 codes with an fp32 scale for every 128 channels of a row of x and for every
+ * 128 x 128 block of a weight, the form that block-scaled checkpoints carry.
+ *   rule   a = max |v| over the block, s = a / 448 (fp32), codes E4M3(v / s) with a correctly rounded division;
+ *          an all-zero block has s = 0 and signed-zero codes.  A last block holds what is left of K (or N).
+ * quant_act_fp8b:    x bf16 [M,K] -> x_q uint8 [M,K], x_scale float [M, ceil(K/128)].
+ * quant_weight_fp8b: w bf16 [N,K] -> w_q uint8 [N,K], w_scale float [ceil(N/128), ceil(K/128)].
+ * transpose_fp8b:    a quantized weight turned over: weight_t [K,N], weight_t_scale [ceil(K/128), ceil(N/128)]
+ *                    (N % 16 == 0), the same values.  With it the gradient of a linear's input is a linear:
+ *                    dx = qlinear_fp8b(dy, weight_t).
+ * qlinear_fp8b:      y[m,n] = bf16_rne(sum_b x_scale[m,b] weight_scale[n/128,b] sum_{k in b} q_x q_w), with q_x and
+ *                    x_scale from quant_act_fp8b(x).  A block's sum comes from the FP8 matrix instructions (which
+ *                    cut each product below 2^-13 of the largest of its group of eight) and is folded into fp32
+ *                    accumulators.  The product of two scales must not overflow fp32.
+ * qlinear_fp8b_ex:   the same with an epilogue (see qlinear_fp8r_ex).
+ *   ws   at least qlinear_workspace_bytes(QPL_FP8B, M, K, N, 0) bytes, which is 0 for a few rows (they are quantized
+ *        inside the product's kernel; ws may then be NULL).
+ * qlinear_gated_fp8b: a gated feed-forward block's first half in one product,
+ *     g = x Wg^T, u = x Wu^T (as qlinear_fp8b, before their rounding),  h = bf16_rne(act(g) u)
+ *   gate, up  weights [H,K] with scales [ceil(H/128), ceil(K/128)];  H % 16 == 0
+ *   act       QPL_ACT_SILU or QPL_ACT_GELU_TANH, on fp32 values
+ *   h         bf16 [M,H] out
+ *   g, u      bf16 [M,H] out, what the backward pass needs, or both NULL
+ *   ws        at least qlinear_gated_fp8b_workspace_bytes(M, K, H) bytes (0 for a few rows, as above)
+ * qlinear_gated_fp8b_backward: from dh and the saved bf16 g, u (all [M,H]),
+ *     dg = bf16_rne(dh u act'(g)),  du = bf16_rne(dh act(g)),
+ *     dx = bf16_rne(Q(dg) Wg + Q(du) Wu),  Q the rule above over blocks of 128 of H (the rounding of x to its codes
+ *     passes gradients through unchanged)
+ *   gate_t, up_t  the weights turned over (transpose_fp8b): [K,H], scales [ceil(K/128), ceil(H/128)]
+ *   dx            bf16 [M,K] out;  dg, du  bf16 [M,H] out (for qlinear_weight_grad), or both NULL
+ *   ws            at least qlinear_gated_fp8b_backward_workspace_bytes(M, K, H) bytes
+ * qlinear_weight_grad: dw[n,k] = sum_m dy[m,n] x[m,k] of bf16 dy [M,N] and x [M,K], fp32 [N,K], summed in fp32: the
+ *   gradient of any linear's weight.  N % 16 == 0 and K % 16 == 0, both at most 2^23.
+ *
+ * Codes, activations and workspaces need 16-byte alignment, arrays of scales 4-byte.  K < 2^22 (in the backward H
+ * rounded up to 128 below 2^21).
+ */
+typedef struct {
+  const uint8_t* weight;
+  const float* weight_scale;
+} qpl_fp8b_weight;
+
+qpl_status quant_act_fp8b(const uint16_t* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale, void* stream);
+qpl_status quant_weight_fp8b(const uint16_t* w, int64_t N, int64_t K, uint8_t* w_q, float* w_scale, void* stream);
+qpl_status transpose_fp8b(const uint8_t* weight, const float* weight_scale, int64_t N, int64_t K, uint8_t* weight_t,
+                          float* weight_t_scale, void* stream);
+qpl_status qlinear_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* weight,
+                        const float* weight_scale, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+qpl_status qlinear_fp8b_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* weight,
+                           const float* weight_scale, const qpl_epilogue* epi, uint16_t* y, void* ws, size_t ws_bytes,
+                           void* stream);
+size_t qlinear_gated_fp8b_workspace_bytes(int64_t M, int64_t K, int64_t H);
+qpl_status qlinear_gated_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t H, const qpl_fp8b_weight* gate,
+                              const qpl_fp8b_weight* up, qpl_act act, uint16_t* h, uint16_t* g, uint16_t* u, void* ws,
+                              size_t ws_bytes, void* stream);
+size_t qlinear_gated_fp8b_backward_workspace_bytes(int64_t M, int64_t K, int64_t H);
+qpl_status qlinear_gated_fp8b_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M, int64_t K,
+                                       int64_t H, const qpl_fp8b_weight* gate_t, const qpl_fp8b_weight* up_t,
+                                       qpl_act act, uint16_t* dx, uint16_t* dg, uint16_t* du, void* ws,
+                                       size_t ws_bytes, void* stream);
+qpl_status qlinear_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t M, int64_t N, int64_t K, float* dw,
+                               void* stream);
+
+/*
+ * Norm of each head of the queries and keys, and the rotation by their positions, in one pass over what a fused QKV
+ * projection wrote:
+ *     n = x w / sqrt(mean over the head of x^2 + eps)      (norm != 0; w bf16 [head_dim], or NULL for ones)
+ *     (a, b) -> scale (a cos t - b sin t, a sin t + b cos t),  t = position * inv_freq[i]
+ *   for pair i of the first rotary_dim channels: channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ *   interleaved.  The other channels are not rotated.  All in fp32 up to the one rounding of the result; angles in
+ *   fp64, so that far positions keep theirs.
+ * A tensor's element (head, token, channel) lies at head * head_stride + token * token_stride + channel; strides are
+ * multiples of 8 elements.  heads up to 65536, head_dim a multiple of 16 up to 512.  The output may be the input
+ * itself (same pointer and strides); other overlaps are not allowed, and a written view may not hold two elements in
+ * one place (QPL_ERR_SHAPE).  q and k may have different numbers of heads; k may be NULL.
+ *   rope  NULL (or rotary_dim 0): norm only.  positions int32 [tokens, axes]: with more than one axis (up to 4), the
+ *         first sections[0] pairs turn by the first position of a token, the next sections[1] by the second, ... (they
+ *         add up to rotary_dim / 2).  inv_freq float [rotary_dim / 2].  rotary_dim a multiple of 16 up to head_dim.
+ *         scale, finite and > 0, multiplies the rotated channels.
+ * qk_norm_rope_backward: per tensor x the saved input, y its output's gradient, dx (out) the input's gradient,
+ *   dweight (out, float [head_dim], or NULL) the weight's, summed over heads and tokens in a fixed order.  dx may be x
+ *   or y itself.  ws at least qk_norm_rope_backward_workspace_bytes(tokens, head_dim) bytes (may be NULL without any
+ *   dweight).
+ * Errors: QPL_ERR_ARG for eps or scale not finite and > 0, a weight without norm, a dweight without weight, neither
+ * norm nor rotation.
+ * qpl_rope_frequencies (host): base^(-2 i / rotary_dim), scaled for contexts longer than the trained ones:
+ *   LINEAR  divided by factor;   NTK  with base * factor^(rotary_dim / (rotary_dim - 2));
+ *   YARN    channels that turn at most low_turns times over trained_tokens are divided by factor, those that turn at
+ *           least high_turns times are kept, in between linearly mixed, and *scale = 0.1 ln(factor) + 1 (else 1).
+ */
+typedef struct {
+  const uint16_t* x;
+  uint16_t* y;
+  int64_t heads;
+  int64_t x_head_stride, x_token_stride, y_head_stride, y_token_stride;
+  const uint16_t* weight;
+  uint16_t* dx; /* backward only, like the rest */
+  int64_t dx_head_stride, dx_token_stride;
+  float* dweight;
+} qpl_heads;
+
+typedef struct {
+  const int32_t* positions;
+  const float* inv_freq;
+  int64_t rotary_dim, axes;
+  int64_t sections[4];
+  int interleaved;
+  float scale;
+} qpl_rope;
+
+typedef enum { QPL_ROPE_PLAIN = 0, QPL_ROPE_LINEAR = 1, QPL_ROPE_NTK = 2, QPL_ROPE_YARN = 3 } qpl_rope_kind;
+typedef struct {
+  qpl_rope_kind kind;
+  double factor, trained_tokens, low_turns, high_turns;
+} qpl_rope_scaling;
+
+qpl_status qk_norm_rope(const qpl_heads* q, const qpl_heads* k, int64_t tokens, int64_t head_dim, int norm, float eps,
+                        const qpl_rope* rope, void* stream);
+size_t qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t head_dim);
+qpl_status qk_norm_rope_backward(const qpl_heads* q, const qpl_heads* k, int64_t tokens, int64_t head_dim, int norm,
+                                 float eps, const qpl_rope* rope, void* ws, size_t ws_bytes, void* stream);
+qpl_status qpl_rope_frequencies(int64_t rotary_dim, double base, const qpl_rope_scaling* scaling, float* inv_freq,
+                                float* scale);
+
+/*
  * Dequantize a weight to bf16 (guide, "Kernels" section, last paragraph: on other
  * devices the weight is dequantized to compute_dtype on every forward and the
  * layer runs as a regular linear; that linear is the caller's).
@@ -408,7 +532,7 @@ qpl_status dequant_weight(qpl_scheme scheme, const uint8_t* weight, const void* 
                           uint16_t* w_bf16, void* stream);
 
 /* Bytes of scratch that the scheme's linear needs for these sizes
- * (0 if the sizes are invalid, and for INT8 also where none is needed).  The scratch may be reused between calls that
+ * (0 if the sizes are invalid, and for INT8 and FP8B also where none is needed).  The scratch may be reused between calls that
  * are ordered on one stream. */
 size_t qlinear_workspace_bytes(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R);
 
@@ -464,7 +588,14 @@ typedef enum {
   QPL_KERNEL_GEMM_INT8_GROUPED = 20,
   QPL_KERNEL_EXPERT_PLAN = 21,       /* expert_plan; in qlinear_moe_int8 with few choices also fc1's quantize */
   QPL_KERNEL_EXPERT_COMBINE = 22,
-  QPL_KERNEL_COUNT = 23
+  QPL_KERNEL_QUANT_FP8B = 23,        /* quant_act_fp8b, quant_weight_fp8b, and the quantize inside the FP8B linears */
+  QPL_KERNEL_GEMM_FP8B = 24,         /* also the product of the gated backward */
+  QPL_KERNEL_GATED_FP8B = 25,
+  QPL_KERNEL_GATED_BACKWARD = 26,    /* the gradients of both projections and their codes */
+  QPL_KERNEL_TRANSPOSE_FP8B = 27,
+  QPL_KERNEL_WEIGHT_GRAD = 28,
+  QPL_KERNEL_QK_NORM_ROPE = 29,      /* both directions */
+  QPL_KERNEL_COUNT = 30
 } qpl_kernel;
 
 void qpl_timing_enable(int on);

@@ -24,6 +24,9 @@ What it computes, and the page each part follows (all pages are the Diffusers
 * ``int4``      the INT4 variant of svdq_w4a4 (same post and section).
 * ``int8``      the 8-bit integer linear, and the plan and the combination of a mixture of
                 experts.
+* ``fp8b``      block-scaled fp8 (a scale for every block of 128): quantizers, linear, the gated
+                feed-forward block with its backward, the gradient of a weight.
+* ``rope``      the norm of queries and keys per head and their rotation, with gradients.
 * ``epilogue``  GELU (tanh form), the GELU MLP and the fused QKV scatter (same post,
                 "Introducing Nunchaku Lite", first paragraph), with the interval
                 bounds that check outputs passing through GELU and requantization.
@@ -33,4 +36,4 @@ operation IEEE binary32 round-to-nearest-even, division correctly rounded, no
 fused multiply-add, no denormal flush) and float64 for the references.
 Every function is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_*.py``.
 """
-from . import awq, epilogue, formats, int4, int8, quant, reference  # noqa: F401
+from . import awq, epilogue, formats, fp8b, int4, int8, quant, reference, rope  # noqa: F401

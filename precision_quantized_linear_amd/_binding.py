@@ -16,6 +16,7 @@ QPL_FP8R = 0
 QPL_NVFP4 = 1
 QPL_INT4 = 2
 QPL_INT8 = 3
+QPL_FP8B = 4
 
 EXPORTS = ("quant_act_fp8_row", "quant_act_nvfp4", "qlinear_fp8r", "qlinear_nvfp4", "dequant_weight",
            "quant_weight_awq", "qlinear_awq_w4a16", "quant_act_int4", "qlinear_int4", "qlinear_fp8r_ex",
@@ -25,17 +26,24 @@ EXPORTS = ("quant_act_fp8_row", "quant_act_nvfp4", "qlinear_fp8r", "qlinear_nvfp
            "quant_act_int8", "qlinear_int8", "qlinear_int8_ex", "expert_plan", "expert_plan_workspace_bytes",
            "qlinear_grouped_int8",
            "qlinear_grouped_int8_workspace_bytes", "expert_combine", "qlinear_moe_int8",
-           "qlinear_moe_int8_workspace_bytes")
+           "qlinear_moe_int8_workspace_bytes", "quant_act_fp8b", "quant_weight_fp8b", "transpose_fp8b", "qlinear_fp8b",
+           "qlinear_fp8b_ex", "qlinear_gated_fp8b", "qlinear_gated_fp8b_workspace_bytes",
+           "qlinear_gated_fp8b_backward", "qlinear_gated_fp8b_backward_workspace_bytes", "qlinear_weight_grad",
+           "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_bytes", "qpl_rope_frequencies")
 
 # qpl_kernel order of include/qpl.h
 KERNELS = ("quant_fp8_row", "quant_nvfp4", "quant_nvfp4_linear", "gemm_fp8r", "gemm_nvfp4", "gemm_nvfp4_lowrank",
            "lowrank_prep", "dequant", "amax", "nvfp4_prep", "quant_nvfp4_lowrank", "quant_w4g", "gemv_w4a16",
            "quant_int4", "int4_expand", "gemm_int4", "quant_int4_lowrank", "gemm_epilogue", "quant_int8", "gemm_int8",
-           "gemm_int8_grouped", "expert_plan", "expert_combine")
+           "gemm_int8_grouped", "expert_plan", "expert_combine", "quant_fp8b", "gemm_fp8b", "gated_fp8b",
+           "gated_backward", "transpose_fp8b", "weight_grad", "qk_norm_rope")
 
 QPL_ACT_NONE = 0
 QPL_ACT_GELU_TANH = 1
+QPL_ACT_SILU = 2
 _ACTS = {None: QPL_ACT_NONE, "none": QPL_ACT_NONE, "gelu_tanh": QPL_ACT_GELU_TANH}
+
+_GATED_ACTS = {"silu": QPL_ACT_SILU, "gelu_tanh": QPL_ACT_GELU_TANH}
 
 _P, _I64, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float
 
@@ -50,6 +58,31 @@ class Nvfp4Layer(ctypes.Structure):
     """qpl_nvfp4_layer of include/qpl.h."""
     _fields_ = [("weight", _P), ("weight_scale", _P), ("weight_scale_2", _F), ("input_scale", _F),
                 ("smooth", _P), ("lora_down", _P), ("lora_up", _P), ("R", _I64)]
+
+
+class Fp8bWeight(ctypes.Structure):
+    """qpl_fp8b_weight of include/qpl.h."""
+    _fields_ = [("weight", _P), ("weight_scale", _P)]
+
+
+class Heads(ctypes.Structure):
+    """qpl_heads of include/qpl.h."""
+    _fields_ = [("x", _P), ("y", _P), ("heads", _I64), ("x_head_stride", _I64), ("x_token_stride", _I64),
+                ("y_head_stride", _I64), ("y_token_stride", _I64), ("weight", _P), ("dx", _P),
+                ("dx_head_stride", _I64), ("dx_token_stride", _I64), ("dweight", _P)]
+
+
+class Rope(ctypes.Structure):
+    """qpl_rope of include/qpl.h."""
+    _fields_ = [("positions", _P), ("inv_freq", _P), ("rotary_dim", _I64), ("axes", _I64), ("sections", _I64 * 4),
+                ("interleaved", ctypes.c_int), ("scale", _F)]
+
+
+class RopeScaling(ctypes.Structure):
+    """qpl_rope_scaling of include/qpl.h."""
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("trained_tokens", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double)]
+
 
 _lib = None
 
@@ -92,6 +125,17 @@ def load():
         "qlinear_grouped_int8": [P, I64, I64, I64, I64, P, P, P, I64, P, ctypes.c_int, P, P, SZ, P],
         "expert_combine": [P, I64, I64, P, P, I64, I64, P, P],
         "qlinear_moe_int8": [P, I64, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
+        "quant_act_fp8b": [P, I64, I64, P, P, P],
+        "quant_weight_fp8b": [P, I64, I64, P, P, P],
+        "transpose_fp8b": [P, P, I64, I64, P, P, P],
+        "qlinear_fp8b": [P, I64, I64, I64, P, P, P, P, SZ, P],
+        "qlinear_fp8b_ex": [P, I64, I64, I64, P, P, P, P, P, SZ, P],
+        "qlinear_gated_fp8b": [P, I64, I64, I64, P, P, ctypes.c_int, P, P, P, P, SZ, P],
+        "qlinear_gated_fp8b_backward": [P, P, P, I64, I64, I64, P, P, ctypes.c_int, P, P, P, P, SZ, P],
+        "qlinear_weight_grad": [P, P, I64, I64, I64, P, P],
+        "qk_norm_rope": [P, P, I64, I64, ctypes.c_int, F, P, P],
+        "qk_norm_rope_backward": [P, P, I64, I64, ctypes.c_int, F, P, P, SZ, P],
+        "qpl_rope_frequencies": [I64, ctypes.c_double, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -107,6 +151,12 @@ def load():
     lib.qlinear_grouped_int8_workspace_bytes.restype = SZ
     lib.qlinear_moe_int8_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64]
     lib.qlinear_moe_int8_workspace_bytes.restype = SZ
+    lib.qlinear_gated_fp8b_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.qlinear_gated_fp8b_workspace_bytes.restype = SZ
+    lib.qlinear_gated_fp8b_backward_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.qlinear_gated_fp8b_backward_workspace_bytes.restype = SZ
+    lib.qk_norm_rope_backward_workspace_bytes.argtypes = [I64, I64]
+    lib.qk_norm_rope_backward_workspace_bytes.restype = SZ
     lib.qpl_nvfp4_global_scale.argtypes = [F]
     lib.qpl_nvfp4_global_scale.restype = F
     lib.qpl_status_str.argtypes = [ctypes.c_int]
@@ -546,6 +596,275 @@ def qlinear_moe_int8(x, expert_ids, expert_weights, fc1, fc2, y=None, workspace=
         _addr(fc2["weight_scale"], torch.float32, (E, N), dev, "fc2.weight_scale"),
         _addr(y, torch.bfloat16, (T, N), dev, "y"), wa, nbytes, _queue(stream, dev)))
     return y
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def quant_act_fp8b(x, x_q=None, x_scale=None, stream=None):
+    """bf16 [M,K] -> (E4M3 codes uint8 [M,K], fp32 scales [M, ceil(K/128)]), a scale for each 128 channels of a row."""
+    dev = _current(x, 2, "x")
+    M, K = x.shape
+    x_q = _new((M, K), torch.uint8, x, stream) if x_q is None else x_q
+    x_scale = _new((M, _blocks(K)), torch.float32, x, stream) if x_scale is None else x_scale
+    _check("quant_act_fp8b", load().quant_act_fp8b(
+        _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, _addr(x_q, torch.uint8, (M, K), dev, "x_q"),
+        _addr(x_scale, torch.float32, (M, _blocks(K)), dev, "x_scale"), _queue(stream, dev)))
+    return x_q, x_scale
+
+
+def quant_weight_fp8b(w, w_q=None, w_scale=None, stream=None):
+    """bf16 weight [N,K] -> (E4M3 codes uint8 [N,K], fp32 scales [ceil(N/128), ceil(K/128)])."""
+    dev = _current(w, 2, "w")
+    N, K = w.shape
+    w_q = _new((N, K), torch.uint8, w, stream) if w_q is None else w_q
+    w_scale = _new((_blocks(N), _blocks(K)), torch.float32, w, stream) if w_scale is None else w_scale
+    _check("quant_weight_fp8b", load().quant_weight_fp8b(
+        _addr(w, torch.bfloat16, (N, K), dev, "w"), N, K, _addr(w_q, torch.uint8, (N, K), dev, "w_q"),
+        _addr(w_scale, torch.float32, (_blocks(N), _blocks(K)), dev, "w_scale"), _queue(stream, dev)))
+    return w_q, w_scale
+
+
+def transpose_fp8b(weight, weight_scale, weight_t=None, weight_t_scale=None, stream=None):
+    """A quantized weight [N,K] turned over -> (uint8 [K,N], fp32 [ceil(K/128), ceil(N/128)]); N % 16 == 0.  The
+    gradient of a linear's input is the linear of dy with it."""
+    dev = _current(weight, 2, "weight")
+    N, K = weight.shape
+    weight_t = _new((K, N), torch.uint8, weight, stream) if weight_t is None else weight_t
+    if weight_t_scale is None:
+        weight_t_scale = _new((_blocks(K), _blocks(N)), torch.float32, weight, stream)
+    _check("transpose_fp8b", load().transpose_fp8b(
+        _addr(weight, torch.uint8, (N, K), dev, "weight"),
+        _addr(weight_scale, torch.float32, (_blocks(N), _blocks(K)), dev, "weight_scale"), N, K,
+        _addr(weight_t, torch.uint8, (K, N), dev, "weight_t"),
+        _addr(weight_t_scale, torch.float32, (_blocks(K), _blocks(N)), dev, "weight_t_scale"), _queue(stream, dev)))
+    return weight_t, weight_t_scale
+
+
+def qlinear_fp8b(x, weight, weight_scale, y=None, workspace=None, stream=None, act=None, qkv=None):
+    """y[M,N] bf16 = block-scaled fp8 linear of bf16 x [M,K] with E4M3 weight uint8 [N,K] and fp32 weight_scale
+    [ceil(N/128), ceil(K/128)]; act and qkv as in qlinear_fp8r."""
+    N = _dims(weight, 2, "weight")[0]
+    dev = _current(x, 2, "x")
+    M, K = x.shape
+    args = (_addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, N, _addr(weight, torch.uint8, (N, K), dev, "weight"),
+            _addr(weight_scale, torch.float32, (_blocks(N), _blocks(K)), dev, "weight_scale"))
+    act_code = _act_code(act)
+    ya = 0
+    if qkv is None:
+        y = _new((M, N), torch.bfloat16, x, stream) if y is None else y
+        ya = _addr(y, torch.bfloat16, (M, N), dev, "y")
+    else:
+        for t, name in zip(qkv[:3], ("q", "k", "v")):
+            _addr(t, torch.bfloat16, _dims(qkv[0], 3, "q"), dev, name)
+    ws, wa, nbytes = _scratch(workspace, qlinear_workspace_bytes(QPL_FP8B, M, K, N), x, dev, stream)
+    if act_code == QPL_ACT_NONE and qkv is None:
+        _check("qlinear_fp8b", load().qlinear_fp8b(*args, ya, wa, nbytes, _queue(stream, dev)))
+        return y
+    e, _, out = _epilogue(act, qkv, M, N, y, x.device)
+    _check("qlinear_fp8b_ex", load().qlinear_fp8b_ex(*args, _ref(e), ya, wa, nbytes, _queue(stream, dev)))
+    return out
+
+
+def _gated_act(act):
+    if act not in _GATED_ACTS:
+        raise ValueError(f"act: expected one of {sorted(_GATED_ACTS)}, got {act!r}")
+    return _GATED_ACTS[act]
+
+
+def _fp8b_weight(layer, N, K, dev, name):
+    """Fp8bWeight of a dict with weight uint8 [N,K] and weight_scale float32 [ceil(N/128), ceil(K/128)]."""
+    return Fp8bWeight(_addr(layer["weight"], torch.uint8, (N, K), dev, name + ".weight"),
+                      _addr(layer["weight_scale"], torch.float32, (_blocks(N), _blocks(K)), dev,
+                            name + ".weight_scale"))
+
+
+def qlinear_gated_fp8b_workspace_bytes(M, K, H):
+    return int(load().qlinear_gated_fp8b_workspace_bytes(M, K, H))
+
+
+def qlinear_gated_fp8b(x, gate, up, act="silu", h=None, save=False, workspace=None, stream=None):
+    """h [M,H] bf16 = act(x Wg^T) * (x Wu^T) for block-scaled fp8 weights gate and up, dicts with weight uint8 [H,K]
+    and weight_scale float32 [ceil(H/128), ceil(K/128)]; act "silu" or "gelu_tanh".  With save (True, or a pair of
+    bf16 [M,H] tensors to write) the result is (h, g, u) with both projections, which the backward pass needs."""
+    H = _dims(gate["weight"], 2, "gate.weight")[0]
+    dev = _current(x, 2, "x")
+    M, K = x.shape
+    code = _gated_act(act)
+    wg, wu = _fp8b_weight(gate, H, K, dev, "gate"), _fp8b_weight(up, H, K, dev, "up")
+    h = _new((M, H), torch.bfloat16, x, stream) if h is None else h
+    if save is True:
+        save = (_new((M, H), torch.bfloat16, x, stream), _new((M, H), torch.bfloat16, x, stream))
+    g, u = save if save else (None, None)
+    ws, wa, nbytes = _scratch(workspace, qlinear_gated_fp8b_workspace_bytes(M, K, H), x, dev, stream)
+    _check("qlinear_gated_fp8b", load().qlinear_gated_fp8b(
+        _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, H, ctypes.byref(wg), ctypes.byref(wu), code,
+        _addr(h, torch.bfloat16, (M, H), dev, "h"), _addr(g, torch.bfloat16, (M, H), dev, "g"),
+        _addr(u, torch.bfloat16, (M, H), dev, "u"), wa, nbytes, _queue(stream, dev)))
+    return (h, g, u) if save else h
+
+
+def qlinear_gated_fp8b_backward_workspace_bytes(M, K, H):
+    return int(load().qlinear_gated_fp8b_backward_workspace_bytes(M, K, H))
+
+
+def qlinear_gated_fp8b_backward(dh, g, u, gate_t, up_t, act="silu", dx=None, dg=None, du=None, workspace=None,
+                                stream=None):
+    """(dx [M,K], dg [M,H], du [M,H]), all bf16, from dh and the saved g, u (bf16 [M,H]): the gradients of both
+    projections, and of x through the weights turned over (dicts with what transpose_fp8b returns: weight uint8
+    [K,H], weight_scale float32 [ceil(K/128), ceil(H/128)]).  The weights' gradients are
+    qlinear_weight_grad(dg, x) and qlinear_weight_grad(du, x)."""
+    K = _dims(gate_t["weight"], 2, "gate_t.weight")[0]
+    dev = _current(dh, 2, "dh")
+    M, H = dh.shape
+    code = _gated_act(act)
+    wg, wu = _fp8b_weight(gate_t, K, H, dev, "gate_t"), _fp8b_weight(up_t, K, H, dev, "up_t")
+    dx = _new((M, K), torch.bfloat16, dh, stream) if dx is None else dx
+    dg = _new((M, H), torch.bfloat16, dh, stream) if dg is None else dg
+    du = _new((M, H), torch.bfloat16, dh, stream) if du is None else du
+    ws, wa, nbytes = _scratch(workspace, qlinear_gated_fp8b_backward_workspace_bytes(M, K, H), dh, dev, stream)
+    _check("qlinear_gated_fp8b_backward", load().qlinear_gated_fp8b_backward(
+        _addr(dh, torch.bfloat16, (M, H), dev, "dh"), _addr(g, torch.bfloat16, (M, H), dev, "g"),
+        _addr(u, torch.bfloat16, (M, H), dev, "u"), M, K, H, ctypes.byref(wg), ctypes.byref(wu), code,
+        _addr(dx, torch.bfloat16, (M, K), dev, "dx"), _addr(dg, torch.bfloat16, (M, H), dev, "dg"),
+        _addr(du, torch.bfloat16, (M, H), dev, "du"), wa, nbytes, _queue(stream, dev)))
+    return dx, dg, du
+
+
+def qlinear_weight_grad(dy, x, dw=None, stream=None):
+    """dw [N,K] float32 = dy^T x of bf16 dy [M,N] and x [M,K]: the gradient of a linear's weight."""
+    N = _dims(dy, 2, "dy")[1]
+    dev = _current(x, 2, "x")
+    M, K = x.shape
+    dw = _new((N, K), torch.float32, x, stream) if dw is None else dw
+    _check("qlinear_weight_grad", load().qlinear_weight_grad(
+        _addr(dy, torch.bfloat16, (M, N), dev, "dy"), _addr(x, torch.bfloat16, (M, K), dev, "x"), M, N, K,
+        _addr(dw, torch.float32, (N, K), dev, "dw"), _queue(stream, dev)))
+    return dw
+
+
+def _head_view(t, shape, dev, name):
+    """(address, head stride, token stride) of bf16 heads [heads, tokens, head_dim] whose channels are contiguous."""
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != dev or (shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: expected torch.bfloat16 {tuple(shape)} with contiguous channels on the current GPU "
+                         f"({dev}), got {t.dtype} {tuple(t.shape)} strides={t.stride()} device={t.device}")
+    # the stride of a single head or token is never used
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0
+
+
+def _new_heads(like, stream):
+    """New heads in the order of `like`'s (token-major heads stay token-major)."""
+    heads, tokens, dim = like.shape
+    if tokens > 1 and heads > 1 and like.stride(0) < like.stride(1):
+        return _new((tokens, heads, dim), torch.bfloat16, like, stream).transpose(0, 1)
+    return _new((heads, tokens, dim), torch.bfloat16, like, stream)
+
+
+def _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev):
+    if inv_freq is None:
+        return None
+    n = _dims(inv_freq, 1, "inv_freq")[0]
+    if positions is None:
+        raise ValueError("positions: needed with inv_freq")
+    axes = 1 if sections is None else len(sections)
+    if sections is not None and not 1 <= axes <= 4:
+        raise ValueError(f"sections: expected one to four numbers of pairs, got {axes}")
+    shape = (tokens, axes) if positions.dim() == 2 else (tokens,)
+    if axes > 1 and positions.dim() != 2:
+        raise ValueError(f"positions: expected [tokens, {axes}] for {axes} sections, got {tuple(positions.shape)}")
+    r = Rope(_addr(positions, torch.int32, shape, dev, "positions"), _addr(inv_freq, torch.float32, (n,), dev, "inv_freq"),
+             2 * n, axes)
+    for i, v in enumerate(sections or (n,)):
+        r.sections[i] = int(v)
+    r.interleaved, r.scale = int(bool(interleaved)), float(scale)
+    return r
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, norm=True, interleaved=False,
+                 sections=None, scale=1.0, q_out=None, k_out=None, stream=None):
+    """(q, k) normed per head and rotated by their positions, in one pass.  q and k: bf16 [heads, tokens, head_dim],
+    channels contiguous, any strides of heads and tokens in multiples of 8 (token-major callers pass a transposed
+    view); k may be None.  n = x * weight / sqrt(mean(x^2) + eps) over each head (norm False: as it is), then the
+    first 2 len(inv_freq) channels turned by position * inv_freq[i], as pairs (i, i + half) or, interleaved,
+    (2 i, 2 i + 1), times scale.  positions int32 [tokens], or [tokens, len(sections)] with sections pairs for each
+    axis; inv_freq float32 (rope_frequencies), or None for the norm alone.  q_out and k_out may be q and k."""
+    dev = _current(q, 3, "q")
+    tokens, dim = q.shape[1], q.shape[2]
+    r = _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev)
+    outs, sides = [], []
+    for t, w, o, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
+        if t is None:
+            outs.append(None)
+            sides.append(None)
+            continue
+        shape = (_dims(t, 3, name)[0], tokens, dim)
+        xa, xh, xt = _head_view(t, shape, dev, name)
+        o = _new_heads(t, stream) if o is None else o
+        ya, yh, yt = _head_view(o, shape, dev, name + "_out")
+        sides.append(Heads(xa, ya, shape[0], xh, xt, yh, yt, _addr(w, torch.bfloat16, (dim,), dev, name + "_weight")))
+        outs.append(o)
+    _check("qk_norm_rope", load().qk_norm_rope(_ref(sides[0]), _ref(sides[1]), tokens, dim, int(bool(norm)), float(eps),
+                                               _ref(r), _queue(stream, dev)))
+    return tuple(outs)
+
+
+def qk_norm_rope_backward_workspace_bytes(tokens, head_dim):
+    return int(load().qk_norm_rope_backward_workspace_bytes(tokens, head_dim))
+
+
+def qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, norm=True,
+                          interleaved=False, sections=None, scale=1.0, dq_out=None, dk_out=None, workspace=None,
+                          stream=None):
+    """Gradients (of q, of k, of q_weight, of k_weight) from those of qk_norm_rope's outputs and its inputs; the
+    weights' in float32 [head_dim], None where there is no weight.  dq_out and dk_out may be dq and dk (or q and k)."""
+    dev = _current(q, 3, "q")
+    tokens, dim = q.shape[1], q.shape[2]
+    r = _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev)
+    outs, grads, sides = [], [], []
+    for d, t, w, o, name in ((dq, q, q_weight, dq_out, "q"), (dk, k, k_weight, dk_out, "k")):
+        if t is None:
+            outs.append(None)
+            grads.append(None)
+            sides.append(None)
+            continue
+        shape = (_dims(t, 3, name)[0], tokens, dim)
+        xa, xh, xt = _head_view(t, shape, dev, name)
+        da, dh, dt = _head_view(d, shape, dev, "d" + name)
+        o = _new_heads(d, stream) if o is None else o
+        oa, oh, ot = _head_view(o, shape, dev, "d" + name + "_out")
+        gw = None if w is None else _new((dim,), torch.float32, t, stream)
+        sides.append(Heads(xa, da, shape[0], xh, xt, dh, dt, _addr(w, torch.bfloat16, (dim,), dev, name + "_weight"),
+                           oa, oh, ot, _addr(gw, torch.float32, (dim,), dev, "d" + name + "_weight")))
+        outs.append(o)
+        grads.append(gw)
+    need = qk_norm_rope_backward_workspace_bytes(tokens, dim) if any(g is not None for g in grads) else 0
+    ws, wa, nbytes = _scratch(workspace, need, q, dev, stream)
+    _check("qk_norm_rope_backward", load().qk_norm_rope_backward(
+        _ref(sides[0]), _ref(sides[1]), tokens, dim, int(bool(norm)), float(eps), _ref(r), wa, nbytes,
+        _queue(stream, dev)))
+    return (*outs, *grads)
+
+
+_ROPE_KINDS = {"linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained_tokens=0, low_turns=1.0,
+                     high_turns=32.0, device=None):
+    """(inv_freq float32 [rotary_dim / 2], scale) for qk_norm_rope: base^(-2 i / rotary_dim), scaled for longer
+    contexts by scaling "linear" (divided by factor), "ntk" (a larger base) or "yarn" (channels that turn at most
+    low_turns times over trained_tokens are divided by factor, those that turn at least high_turns times are kept,
+    and scale = 0.1 ln(factor) + 1)."""
+    if scaling is not None and scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling: expected one of {sorted(_ROPE_KINDS)}, got {scaling!r}")
+    s = None
+    if scaling is not None:
+        s = RopeScaling(_ROPE_KINDS[scaling], factor, trained_tokens, low_turns, high_turns)
+    out = torch.empty((max(rotary_dim // 2, 1),), dtype=torch.float32)
+    scale = ctypes.c_float()
+    _check("qpl_rope_frequencies", load().qpl_rope_frequencies(rotary_dim, base, _ref(s), _ptr(out),
+                                                               ctypes.byref(scale)))
+    return (out if device is None else out.to(device)), scale.value
 
 
 def quant_weight_awq(w, group=64, w_q=None, w_scale=None, w_zero=None, stream=None):

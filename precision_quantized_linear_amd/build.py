@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqpl.so")
 SOURCES = ["quant_kernels.hip", "gemm_kernels.hip", "w4a16_kernels.hip", "int8_kernels.hip",
-           "expert_kernels.hip", "qpl_api.hip"]
+           "expert_kernels.hip", "fp8b_kernels.hip", "wgrad_kernels.hip", "rope_kernels.hip", "qpl_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 CFLAGS = [
@@ -43,7 +43,7 @@ def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     objs = [os.path.join(BUILD, s.replace(".hip", ".o")) for s in SOURCES]
     cmds = [[HIPCC, *CFLAGS, "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
-    with ThreadPoolExecutor(max_workers=min(6, len(cmds))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
         for err in ex.map(_run, cmds):
             if verbose and err.strip():
                 print(err, file=sys.stderr)

@@ -4,8 +4,8 @@
 // Quantizer.  a = max_k |x[m, k]|, s = fp32(a / 127), q = rint(127 x / a), ties to even.
 // The sums of products are int32 and exact for K <= 2^17 (127 * 128 * 2^17 < 2^31), so a
 // result does not depend on how K is split over wavefronts or workgroups.
-#include "qpl_gemm.h"
 #include "qpl_int8_shape.h"
+#include "qpl_piece.h"
 
 namespace qpl {
 
@@ -346,19 +346,6 @@ struct Int8Args {
   const RowTile* tiles;  // grouped: the row tiles
 };
 
-// Four outputs stored at 2-byte alignment: rows of y may start at any element.
-struct __attribute__((packed, aligned(2))) Segment4 {
-  u32x2 v;
-};
-
-__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, (int)kRawBufferWord3);
-}
-
 // The wait states between the last MFMAs and the first reader of their results (8 for 16 x 16, 12
 // for 32 x 32).  They are spelled out: a build of the direct kernel had none on the path out of its
 // loop, and stored sums without the last MFMA's share.  The empty statements take and return the
@@ -636,21 +623,6 @@ struct StagedArgs {
   int tiles_m, tiles_n;  // tiles_m unused when grouped
   int nwg;
 };
-
-__device__ __forceinline__ int chunk_at(int r, int c) { return r * PR_ROW + ((c ^ ((r >> 1) & 7)) << 4); }
-
-// Tile (row tile, column tile) at position s of the walk: groups of four row tiles,
-// column by column, so that workgroups of one XCD share operand rows in its L2.
-// Tiles number below 2^31: y has at most 2^40 elements and a tile 2^12 of them, and the
-// grouped weights' columns, E N <= 2^36, bound the tiles of experts with few rows.
-__device__ __forceinline__ void walk(int s, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int per_group = GROUP_M * tiles_n;
-  const int g = s / per_group;
-  const int gm = min(tiles_m - g * GROUP_M, GROUP_M);
-  const int r = s - g * per_group;
-  tm = g * GROUP_M + r % gm;
-  tn = r / gm;
-}
 
 // Workgroups that share a CU: as many as its 160 KB of LDS hold.
 template <int NI, int NJM, int S>

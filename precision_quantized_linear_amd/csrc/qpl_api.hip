@@ -19,6 +19,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 40;  // any operand below 2^40 eleme
 constexpr int64_t kMaxRank = 128;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Arrays that are read element by element, so that slices of them will do.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool positive_finite(float v) { return std::isfinite(v) && v > 0.0f; }
 
 qpl_status check_dims(int64_t M, int64_t K) {
@@ -35,6 +37,7 @@ qpl_status check_gemm_dims(int64_t M, int64_t K, int64_t N) {
 }
 
 int64_t nvfp4_slabs(int64_t K) { return (K + 127) / 128; }
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 
 // The GEMMs address a 256-row tile of an operand through one buffer descriptor with
 // 32-bit offsets, and an offset of 2^30 stands for "past the end": 256 rows times
@@ -43,8 +46,11 @@ int64_t nvfp4_slabs(int64_t K) { return (K + 127) / 128; }
 // (2K bytes each) the same way (K <= 2^21) and store their scales through a
 // descriptor below 2^31 bytes.
 constexpr int64_t kMaxKBytePitch = (int64_t(1) << 30) / 256;
+// FP8B: the two halves of a row that the gated backward's product takes are K bytes each.
 // INT8: 2^17 products of at most 127 * 128 stay below 2^31.
 constexpr int64_t kMaxKInt8 = int64_t(1) << 17;
+// A weight's gradient: 32 rows of 2-byte channels below 2^30 bytes.
+constexpr int64_t kMaxGradWidth = int64_t(1) << 23;
 qpl_status check_gemm_k(qpl_scheme scheme, int64_t M, int64_t K, int64_t R) {
   if (scheme == QPL_INT8) return K <= kMaxKInt8 ? QPL_OK : QPL_ERR_SHAPE;
   const int64_t pitch = scheme == QPL_NVFP4 ? K / 2 : K;
@@ -84,7 +90,8 @@ size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 int64_t rank_pad(int64_t R) { return (R + 31) / 32 * 32; }
 
 // Workspace layout.  fp8r and INT8: [xq: M*K bytes (INT8: rows int8_pitch(K) apart)][xs: 4*M bytes]
-// (nothing for INT8 rows so few that one launch quantizes and multiplies them).  nvfp4: [xq: M*K/2 packed
+// (nothing for INT8 rows so few that one launch quantizes and multiplies them).  FP8B the same with rows
+// fp8b_pitch(K) apart and slab-major scales [ceil(K/128), M].  nvfp4: [xq: M*K/2 packed
 // E2M1 codes][xs: 8*M*S block scales slab-major [S, M, 8]], S = ceil(K/128), and, as
 // part 5, [wsl: 8*N*S] the weight's block scales in the same layout.  INT4:
 // [xq: M*K][w8: N*K] (code values as E4M3 bytes) and, as parts 5 and 6, the
@@ -100,7 +107,11 @@ Layout layout(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R) {
   Layout L;
   size_t parts[7] = {0, 0, 0, 0, 0, 0, 0};
   if (scheme == QPL_INT8 && qpl::int8_token_fits(M, K)) return L;
-  if (scheme == QPL_FP8R || scheme == QPL_INT8) {
+  if (scheme == QPL_FP8B) {
+    if (qpl::fp8b_one_launch(M, K)) return L;
+    parts[0] = size_t(M) * size_t(qpl::fp8b_pitch(K));
+    parts[1] = size_t(4) * size_t(M) * size_t(blocks128(K));
+  } else if (scheme == QPL_FP8R || scheme == QPL_INT8) {
     parts[0] = size_t(M) * size_t(scheme == QPL_INT8 ? qpl::int8_pitch(K) : K);
     parts[1] = size_t(4) * size_t(M);
   } else {
@@ -416,10 +427,11 @@ QPL_EXPORT const char* qpl_status_str(qpl_status status) {
 QPL_EXPORT float qpl_nvfp4_global_scale(float amax) { return amax / 2688.0f; }
 
 QPL_EXPORT size_t qlinear_workspace_bytes(qpl_scheme scheme, int64_t M, int64_t K, int64_t N, int64_t R) {
-  if (scheme != QPL_FP8R && scheme != QPL_NVFP4 && scheme != QPL_INT4 && scheme != QPL_INT8) return 0;
+  if (scheme != QPL_FP8R && scheme != QPL_NVFP4 && scheme != QPL_INT4 && scheme != QPL_INT8 && scheme != QPL_FP8B)
+    return 0;
   if (check_gemm_dims(M, K, N) != QPL_OK || R < 0 || R > kMaxRank) return 0;
   if (scheme == QPL_INT4 && K % 64 != 0) return 0;
-  if ((scheme == QPL_FP8R || scheme == QPL_INT8) && R != 0) return 0;
+  if ((scheme == QPL_FP8R || scheme == QPL_INT8 || scheme == QPL_FP8B) && R != 0) return 0;
   if (check_gemm_k(scheme, M, K, R) != QPL_OK) return 0;
   return layout(scheme, M, K, N, R).total;
 }
@@ -723,9 +735,6 @@ qpl_status check_grouped(int64_t R, int64_t K, int64_t N, int64_t E) {
   return check_gemm_k(QPL_INT8, R, K, 0);
 }
 
-// Index arrays and the choices' weights are read element by element, so slices of them will do.
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 qpl_status check_choices(int64_t T, int64_t topk) {
   if (T < 1 || topk < 1 || topk > kMaxTopk || T >= kMaxPlaces / topk) return QPL_ERR_SHAPE;
   return QPL_OK;
@@ -930,6 +939,352 @@ QPL_EXPORT qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, 
     return s;
   return launched(Timed(QPL_KERNEL_EXPERT_COMBINE, st)(
       qpl::launch_expert_combine(out, R, N, slot, expert_weights, T, topk, y, st)));
+}
+
+// ---- block-scaled fp8 ---------------------------------------------------------
+namespace {
+
+// One weight of a block-scaled layer: pointers set and aligned.
+qpl_status check_fp8b_weight(const qpl_fp8b_weight* w) {
+  if (!w || !w->weight || !w->weight_scale) return QPL_ERR_NULL;
+  if (!aligned16(w->weight) || !aligned4(w->weight_scale)) return QPL_ERR_ALIGN;
+  return QPL_OK;
+}
+
+qpl_status fp8b_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* weight,
+                       const float* weight_scale, const qpl_epilogue* epi, uint16_t* y, void* ws, size_t ws_bytes,
+                       void* stream) {
+  if (!x) return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws)) return QPL_ERR_ALIGN;
+  const qpl_fp8b_weight w{weight, weight_scale};
+  qpl_status s = check_fp8b_weight(&w);
+  if (s != QPL_OK) return s;
+  if ((s = check_gemm_dims(M, K, N)) != QPL_OK) return s;
+  if ((s = check_gemm_k(QPL_FP8B, M, K, 0)) != QPL_OK) return s;
+  qpl::Epilogue ep;
+  if ((s = epilogue_of(epi, M, N, y, ep)) != QPL_OK) return s;
+  const Layout L = layout(QPL_FP8B, M, K, N, 0);
+  if (L.total > 0 && !ws) return QPL_ERR_NULL;
+  if (ws_bytes < L.total) return QPL_ERR_WORKSPACE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const qpl::Fp8bWeight kw{weight, weight_scale};
+  const qpl_kernel kind = gemm_kind(ep, QPL_KERNEL_GEMM_FP8B);
+  if (qpl::fp8b_one_launch(M, K)) return launched(Timed(kind, st)(qpl::launch_fp8b_token(x, kw, M, K, N, ep, y, st)));
+  uint8_t* xq = static_cast<uint8_t*>(ws) + L.off[0];
+  float* xs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off[1]);
+  if ((s = launched(Timed(QPL_KERNEL_QUANT_FP8B, st)(
+           qpl::launch_quant_fp8b(x, M, K, qpl::fp8b_pitch(K), true, xq, xs, st)))) != QPL_OK)
+    return s;
+  return launched(Timed(kind, st)(qpl::launch_gemm_fp8b(xq, xs, kw, M, K, N, ep, y, st)));
+}
+
+// K and N of a linear, both of whose operands' rows are K or N long, and the codes turned over.
+qpl_status check_gated(int64_t M, int64_t K, int64_t H) {
+  qpl_status s = check_gemm_dims(M, K, H);
+  if (s != QPL_OK) return s;
+  if (H % 16 != 0) return QPL_ERR_SHAPE;
+  return check_gemm_k(QPL_FP8B, M, K, 0);
+}
+
+qpl_status check_gated_backward(int64_t M, int64_t K, int64_t H) {
+  qpl_status s = check_gated(M, K, H);
+  if (s != QPL_OK) return s;
+  return 2 * 128 * blocks128(H) < kMaxKBytePitch ? QPL_OK : QPL_ERR_SHAPE;
+}
+
+// Workspace of the gated backward: [codes: M rows of dg's and du's blocks][scales: 2 ceil(H/128) rows of M].
+size_t gated_backward_scales(int64_t M, int64_t H) { return round256(size_t(M) * size_t(256 * blocks128(H))); }
+size_t gated_backward_bytes(int64_t M, int64_t H) {
+  return gated_backward_scales(M, H) + round256(size_t(8) * size_t(M) * size_t(blocks128(H)));
+}
+
+}  // namespace
+
+QPL_EXPORT qpl_status quant_act_fp8b(const uint16_t* x, int64_t M, int64_t K, uint8_t* x_q, float* x_scale,
+                                     void* stream) {
+  if (!x || !x_q || !x_scale) return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(x_q) || !aligned4(x_scale)) return QPL_ERR_ALIGN;
+  qpl_status s = check_dims(M, K);
+  if (s != QPL_OK) return s;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_QUANT_FP8B, st)(qpl::launch_quant_fp8b(x, M, K, K, false, x_q, x_scale, st)));
+}
+
+QPL_EXPORT qpl_status quant_weight_fp8b(const uint16_t* w, int64_t N, int64_t K, uint8_t* w_q, float* w_scale,
+                                        void* stream) {
+  if (!w || !w_q || !w_scale) return QPL_ERR_NULL;
+  if (!aligned16(w) || !aligned16(w_q) || !aligned4(w_scale)) return QPL_ERR_ALIGN;
+  qpl_status s = check_dims(N, K);
+  if (s != QPL_OK) return s;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_QUANT_FP8B, st)(qpl::launch_quant_weight_fp8b(w, N, K, w_q, w_scale, st)));
+}
+
+QPL_EXPORT qpl_status transpose_fp8b(const uint8_t* weight, const float* weight_scale, int64_t N, int64_t K,
+                                     uint8_t* weight_t, float* weight_t_scale, void* stream) {
+  if (!weight || !weight_scale || !weight_t || !weight_t_scale) return QPL_ERR_NULL;
+  if (!aligned16(weight) || !aligned4(weight_scale) || !aligned16(weight_t) || !aligned4(weight_t_scale))
+    return QPL_ERR_ALIGN;
+  qpl_status s = check_dims(N, K);
+  if (s != QPL_OK) return s;
+  if ((s = check_dims(K, N)) != QPL_OK) return s;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_TRANSPOSE_FP8B, st)(
+      qpl::launch_transpose_fp8b(weight, weight_scale, N, K, weight_t, weight_t_scale, st)));
+}
+
+QPL_EXPORT qpl_status qlinear_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* weight,
+                                   const float* weight_scale, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  return fp8b_linear(x, M, K, N, weight, weight_scale, nullptr, y, ws, ws_bytes, stream);
+}
+
+QPL_EXPORT qpl_status qlinear_fp8b_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* weight,
+                                      const float* weight_scale, const qpl_epilogue* epi, uint16_t* y, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  return fp8b_linear(x, M, K, N, weight, weight_scale, epi, y, ws, ws_bytes, stream);
+}
+
+QPL_EXPORT size_t qlinear_gated_fp8b_workspace_bytes(int64_t M, int64_t K, int64_t H) {
+  return check_gated(M, K, H) == QPL_OK ? layout(QPL_FP8B, M, K, H, 0).total : 0;
+}
+
+QPL_EXPORT qpl_status qlinear_gated_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t H,
+                                         const qpl_fp8b_weight* gate, const qpl_fp8b_weight* up, qpl_act act,
+                                         uint16_t* h, uint16_t* g, uint16_t* u, void* ws, size_t ws_bytes,
+                                         void* stream) {
+  if (!x || !h || (g == nullptr) != (u == nullptr)) return QPL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(h) || !aligned16(g) || !aligned16(u) || !aligned16(ws)) return QPL_ERR_ALIGN;
+  qpl_status s = check_fp8b_weight(gate);
+  if (s != QPL_OK) return s;
+  if ((s = check_fp8b_weight(up)) != QPL_OK) return s;
+  if ((s = check_gated(M, K, H)) != QPL_OK) return s;
+  if (act != QPL_ACT_SILU && act != QPL_ACT_GELU_TANH) return QPL_ERR_ARG;
+  const Layout L = layout(QPL_FP8B, M, K, H, 0);
+  if (L.total > 0 && !ws) return QPL_ERR_NULL;
+  if (ws_bytes < L.total) return QPL_ERR_WORKSPACE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const qpl::Fp8bWeight w[2] = {{gate->weight, gate->weight_scale}, {up->weight, up->weight_scale}};
+  uint16_t* const save[2] = {g, u};
+  uint8_t* xq = nullptr;
+  float* xs = nullptr;
+  if (L.total > 0) {
+    xq = static_cast<uint8_t*>(ws) + L.off[0];
+    xs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.off[1]);
+    if ((s = launched(Timed(QPL_KERNEL_QUANT_FP8B, st)(
+             qpl::launch_quant_fp8b(x, M, K, qpl::fp8b_pitch(K), true, xq, xs, st)))) != QPL_OK)
+      return s;
+  }
+  return launched(Timed(QPL_KERNEL_GATED_FP8B, st)(
+      qpl::launch_fp8b_gated(x, xq, xs, w, M, K, H, act == QPL_ACT_SILU, h, save, st)));
+}
+
+QPL_EXPORT size_t qlinear_gated_fp8b_backward_workspace_bytes(int64_t M, int64_t K, int64_t H) {
+  return check_gated_backward(M, K, H) == QPL_OK ? gated_backward_bytes(M, H) : 0;
+}
+
+QPL_EXPORT qpl_status qlinear_gated_fp8b_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M,
+                                                  int64_t K, int64_t H, const qpl_fp8b_weight* gate_t,
+                                                  const qpl_fp8b_weight* up_t, qpl_act act, uint16_t* dx, uint16_t* dg,
+                                                  uint16_t* du, void* ws, size_t ws_bytes, void* stream) {
+  if (!dh || !g || !u || !dx || (dg == nullptr) != (du == nullptr) || !ws) return QPL_ERR_NULL;
+  if (!aligned16(dh) || !aligned16(g) || !aligned16(u) || !aligned16(dx) || !aligned16(dg) || !aligned16(du) ||
+      !aligned16(ws))
+    return QPL_ERR_ALIGN;
+  qpl_status s = check_fp8b_weight(gate_t);
+  if (s != QPL_OK) return s;
+  if ((s = check_fp8b_weight(up_t)) != QPL_OK) return s;
+  if ((s = check_gated_backward(M, K, H)) != QPL_OK) return s;
+  if (act != QPL_ACT_SILU && act != QPL_ACT_GELU_TANH) return QPL_ERR_ARG;
+  if (ws_bytes < gated_backward_bytes(M, H)) return QPL_ERR_WORKSPACE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  uint8_t* q = static_cast<uint8_t*>(ws);
+  float* qs = reinterpret_cast<float*>(q + gated_backward_scales(M, H));
+  if ((s = launched(Timed(QPL_KERNEL_GATED_BACKWARD, st)(
+           qpl::launch_gated_backward(dh, g, u, M, H, act == QPL_ACT_SILU, dg, du, q, qs, st)))) != QPL_OK)
+    return s;
+  const qpl::Fp8bWeight w[2] = {{gate_t->weight, gate_t->weight_scale}, {up_t->weight, up_t->weight_scale}};
+  return launched(Timed(QPL_KERNEL_GEMM_FP8B, st)(qpl::launch_gemm_fp8b_pair(q, qs, w, M, H, K, dx, st)));
+}
+
+QPL_EXPORT qpl_status qlinear_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t M, int64_t N, int64_t K,
+                                          float* dw, void* stream) {
+  if (!dy || !x || !dw) return QPL_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(dw)) return QPL_ERR_ALIGN;
+  qpl_status s = check_gemm_dims(M, K, N);
+  if (s != QPL_OK) return s;
+  // a stage of 32 rows is addressed through 32-bit offsets below 2^30
+  if (N < 16 || N % 16 != 0 || K > kMaxGradWidth || N > kMaxGradWidth) return QPL_ERR_SHAPE;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_WEIGHT_GRAD, st)(qpl::launch_weight_grad(dy, x, M, N, K, dw, st)));
+}
+
+// ---- norm and rotation of queries and keys ------------------------------------
+namespace {
+
+constexpr int64_t kMaxHeads = 65536, kMaxHeadDim = 512, kMaxAxes = 4;
+
+// Where the heads of a tensor lie: strides in elements, multiples of 8 (16-byte vectors).  A tensor that is written
+// has no two elements in one place.
+qpl_status check_view(const void* p, int64_t heads, int64_t tokens, int64_t head_dim, int64_t hs, int64_t ts,
+                      bool written) {
+  if (!p) return QPL_ERR_NULL;
+  if (!aligned16(p)) return QPL_ERR_ALIGN;
+  if (hs < 0 || ts < 0 || hs % 8 != 0 || ts % 8 != 0 || hs >= kMaxElems || ts >= kMaxElems) return QPL_ERR_SHAPE;
+  if ((heads > 1 && hs > kMaxElems / heads) || (tokens > 1 && ts > kMaxElems / tokens)) return QPL_ERR_SHAPE;
+  if (!written) return QPL_OK;
+  if ((heads > 1 && hs < head_dim) || (tokens > 1 && ts < head_dim)) return QPL_ERR_SHAPE;
+  if (heads > 1 && tokens > 1 && hs < (tokens - 1) * ts + head_dim && ts < (heads - 1) * hs + head_dim)
+    return QPL_ERR_SHAPE;
+  return QPL_OK;
+}
+
+// The arguments that both directions share, in launcher form.
+qpl_status rope_of(const qpl_rope* rope, int64_t tokens, int64_t head_dim, int norm, float eps, qpl::RopeArgs& r) {
+  r = qpl::RopeArgs{};
+  if (tokens < 1 || tokens >= kMaxDim || head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0)
+    return QPL_ERR_SHAPE;
+  if (norm && !positive_finite(eps)) return QPL_ERR_ARG;
+  r.norm = norm != 0;
+  r.eps = eps;
+  r.scale = 1.0f;
+  for (int i = 0; i < 3; ++i) r.bound[i] = 1 << 30;
+  if (!rope || rope->rotary_dim == 0) return norm ? QPL_OK : QPL_ERR_ARG;
+  if (!rope->positions || !rope->inv_freq) return QPL_ERR_NULL;
+  if (!aligned4(rope->positions) || !aligned4(rope->inv_freq)) return QPL_ERR_ALIGN;
+  if (rope->rotary_dim < 0 || rope->rotary_dim > head_dim || rope->rotary_dim % 16 != 0) return QPL_ERR_SHAPE;
+  if (rope->axes < 1 || rope->axes > kMaxAxes) return QPL_ERR_SHAPE;
+  if (!positive_finite(rope->scale)) return QPL_ERR_ARG;
+  r.positions = rope->positions;
+  r.inv_freq = rope->inv_freq;
+  r.rotary = (int)rope->rotary_dim;
+  r.axes = (int)rope->axes;
+  r.interleaved = rope->interleaved != 0;
+  r.scale = rope->scale;
+  if (rope->axes > 1) {
+    int64_t end = 0;
+    for (int i = 0; i < rope->axes; ++i) {
+      if (rope->sections[i] < 0 || rope->sections[i] > rope->rotary_dim / 2) return QPL_ERR_SHAPE;
+      end += rope->sections[i];
+      if (i + 1 < rope->axes) r.bound[i] = (int)end;
+    }
+    if (end != rope->rotary_dim / 2) return QPL_ERR_SHAPE;
+  }
+  return QPL_OK;
+}
+
+qpl_status side_of(const qpl_heads* t, bool backward, int64_t tokens, int64_t head_dim, int norm, qpl::RopeSide& s) {
+  s = qpl::RopeSide{};
+  if (t->heads < 1 || t->heads > kMaxHeads) return QPL_ERR_SHAPE;
+  qpl_status st = check_view(t->x, t->heads, tokens, head_dim, t->x_head_stride, t->x_token_stride, false);
+  if (st != QPL_OK) return st;
+  if ((st = check_view(t->y, t->heads, tokens, head_dim, t->y_head_stride, t->y_token_stride, !backward)) != QPL_OK)
+    return st;
+  if (t->weight && !norm) return QPL_ERR_ARG;
+  if (!aligned16(t->weight)) return QPL_ERR_ALIGN;
+  s.x = qpl::HeadView{const_cast<uint16_t*>(t->x), t->x_head_stride, t->x_token_stride};
+  s.y = qpl::HeadView{t->y, t->y_head_stride, t->y_token_stride};
+  s.heads = t->heads;
+  s.weight = t->weight;
+  if (!backward) return QPL_OK;
+  if ((st = check_view(t->dx, t->heads, tokens, head_dim, t->dx_head_stride, t->dx_token_stride, true)) != QPL_OK)
+    return st;
+  if (t->dweight && !t->weight) return QPL_ERR_ARG;
+  if (!aligned4(t->dweight)) return QPL_ERR_ALIGN;
+  s.dx = qpl::HeadView{t->dx, t->dx_head_stride, t->dx_token_stride};
+  s.dweight = t->dweight;
+  return QPL_OK;
+}
+
+qpl_status sides_of(const qpl_heads* q, const qpl_heads* k, bool backward, int64_t tokens, int64_t head_dim, int norm,
+                    qpl::RopeSide (&side)[2]) {
+  if (!q) return QPL_ERR_NULL;
+  qpl_status s = side_of(q, backward, tokens, head_dim, norm, side[0]);
+  if (s != QPL_OK) return s;
+  side[1] = qpl::RopeSide{};
+  return k ? side_of(k, backward, tokens, head_dim, norm, side[1]) : QPL_OK;
+}
+
+}  // namespace
+
+QPL_EXPORT qpl_status qk_norm_rope(const qpl_heads* q, const qpl_heads* k, int64_t tokens, int64_t head_dim, int norm,
+                                   float eps, const qpl_rope* rope, void* stream) {
+  if (!q) return QPL_ERR_NULL;
+  qpl::RopeArgs r;
+  qpl_status s = rope_of(rope, tokens, head_dim, norm, eps, r);
+  if (s != QPL_OK) return s;
+  qpl::RopeSide side[2];
+  if ((s = sides_of(q, k, false, tokens, head_dim, norm, side)) != QPL_OK) return s;
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_QK_NORM_ROPE, st)(qpl::launch_qk_norm_rope(side, tokens, (int)head_dim, r, st)));
+}
+
+QPL_EXPORT size_t qk_norm_rope_backward_workspace_bytes(int64_t tokens, int64_t head_dim) {
+  if (tokens < 1 || tokens >= kMaxDim || head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0) return 0;
+  return qpl::qk_backward_bytes(tokens, (int)head_dim);
+}
+
+QPL_EXPORT qpl_status qk_norm_rope_backward(const qpl_heads* q, const qpl_heads* k, int64_t tokens, int64_t head_dim,
+                                            int norm, float eps, const qpl_rope* rope, void* ws, size_t ws_bytes,
+                                            void* stream) {
+  if (!q) return QPL_ERR_NULL;
+  qpl::RopeArgs r;
+  qpl_status s = rope_of(rope, tokens, head_dim, norm, eps, r);
+  if (s != QPL_OK) return s;
+  qpl::RopeSide side[2];
+  if ((s = sides_of(q, k, true, tokens, head_dim, norm, side)) != QPL_OK) return s;
+  if (side[0].dweight || side[1].dweight) {
+    if (!ws) return QPL_ERR_NULL;
+    if (!aligned16(ws)) return QPL_ERR_ALIGN;
+    if (ws_bytes < qpl::qk_backward_bytes(tokens, (int)head_dim)) return QPL_ERR_WORKSPACE;
+  }
+  if ((s = check_device()) != QPL_OK) return s;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launched(Timed(QPL_KERNEL_QK_NORM_ROPE, st)(
+      qpl::launch_qk_norm_rope_backward(side, tokens, (int)head_dim, r, static_cast<float*>(ws), st)));
+}
+
+// pi, to the last bit of a double
+static constexpr double kPi = 0x1.921fb54442d18p+1;
+
+QPL_EXPORT qpl_status qpl_rope_frequencies(int64_t rotary_dim, double base, const qpl_rope_scaling* scaling,
+                                           float* inv_freq, float* scale) {
+  if (!inv_freq || !scale) return QPL_ERR_NULL;
+  if (rotary_dim < 16 || rotary_dim > kMaxHeadDim || rotary_dim % 16 != 0) return QPL_ERR_SHAPE;
+  if (!std::isfinite(base) || base <= 1.0) return QPL_ERR_ARG;
+  const int kind = scaling ? (int)scaling->kind : (int)QPL_ROPE_PLAIN;
+  const double factor = kind == QPL_ROPE_PLAIN ? 1.0 : scaling->factor;
+  if (kind < QPL_ROPE_PLAIN || kind > QPL_ROPE_YARN || !std::isfinite(factor) || factor < 1.0) return QPL_ERR_ARG;
+  double low = 0.0, high = 0.0, trained = 0.0;
+  if (kind == QPL_ROPE_YARN) {
+    trained = scaling->trained_tokens;
+    low = scaling->low_turns;
+    high = scaling->high_turns;
+    if (!std::isfinite(trained) || trained < 1.0 || !std::isfinite(low) || !std::isfinite(high) || low < 0.0 || high <= low)
+      return QPL_ERR_ARG;
+  }
+  const double d = (double)rotary_dim;
+  if (kind == QPL_ROPE_NTK) base *= std::pow(factor, d / (d - 2.0));
+  for (int64_t i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * (double)i / d);
+    if (kind == QPL_ROPE_LINEAR) f /= factor;
+    if (kind == QPL_ROPE_YARN) {
+      const double turns = trained * f / (2.0 * kPi);
+      double keep = (turns - low) / (high - low);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      f = (1.0 - keep) * f / factor + keep * f;
+    }
+    inv_freq[i] = (float)f;
+  }
+  *scale = kind == QPL_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return QPL_OK;
 }
 
 QPL_EXPORT qpl_status dequant_weight(qpl_scheme scheme, const uint8_t* weight, const void* weight_scale,

@@ -155,4 +155,65 @@ hipError_t launch_expert_plan(const int32_t* ids, int64_t n, int64_t topk, int64
 hipError_t launch_expert_combine(const uint16_t* y, int64_t R, int64_t N, const int32_t* slot, const float* weights,
                                  int64_t T, int64_t topk, uint16_t* out, hipStream_t stream);
 
+// Block-scaled fp8 linears.  Quantizers: codes [M, K], rows `pitch` apart, and scales [M, K / 128], or (slab) [K / 128,
+// M], as the products take them; a weight [N, K] in blocks of 128 x 128; and a quantized weight turned over.
+struct Fp8bWeight {
+  const uint8_t* codes;
+  const float* scales;
+};
+constexpr int64_t fp8b_pitch(int64_t K) { return K < 512 ? K : (K + 127) / 128 * 128; }
+hipError_t launch_quant_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t pitch, bool slab, uint8_t* xq, float* xs,
+                             hipStream_t stream);
+hipError_t launch_quant_weight_fp8b(const uint16_t* w, int64_t N, int64_t K, uint8_t* wq, float* ws,
+                                    hipStream_t stream);
+hipError_t launch_transpose_fp8b(const uint8_t* w, const float* ws, int64_t N, int64_t K, uint8_t* wt, float* wst,
+                                 hipStream_t stream);
+// Product of the codes of x (rows fp8b_pitch(K) apart, scales slab-major), or, for so few rows that one launch
+// quantizes and multiplies them (fp8b_one_launch), of x itself.
+bool fp8b_one_launch(int64_t M, int64_t K);
+hipError_t launch_fp8b_token(const uint16_t* x, const Fp8bWeight& w, int64_t M, int64_t K, int64_t N,
+                             const Epilogue& ep, uint16_t* y, hipStream_t stream);
+hipError_t launch_gemm_fp8b(const uint8_t* xq, const float* xs, const Fp8bWeight& w, int64_t M, int64_t K, int64_t N,
+                            const Epilogue& ep, uint16_t* y, hipStream_t stream);
+// h [M, H] = act(x Wg^T) (x Wu^T) of the weights {gate, up} [H, K]; save: both projections in bf16 (or nullptrs).
+// Takes x where one launch does it all, else its codes.
+hipError_t launch_fp8b_gated(const uint16_t* x, const uint8_t* xq, const float* xs, const Fp8bWeight (&w)[2], int64_t M,
+                             int64_t K, int64_t H, bool silu, uint16_t* h, uint16_t* const (&save)[2],
+                             hipStream_t stream);
+// Its backward: dg and du [M, H] in bf16 (nullptrs: not written), their codes q [M, 2 (H rounded up to 128)] and
+// scales s [2 ceil(H / 128), M]; then y [M, N] = (q's first half) w[0]^T + (second half) w[1]^T, weights [N, K].
+hipError_t launch_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M, int64_t H,
+                                 bool silu, uint16_t* dg, uint16_t* du, uint8_t* q, float* s, hipStream_t stream);
+hipError_t launch_gemm_fp8b_pair(const uint8_t* xq, const float* xs, const Fp8bWeight (&w)[2], int64_t M, int64_t K,
+                                 int64_t N, uint16_t* y, hipStream_t stream);
+// dw [N, K] (fp32) = dy^T x of bf16 dy [M, N] and x [M, K].
+hipError_t launch_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t M, int64_t N, int64_t K, float* dw,
+                              hipStream_t stream);
+
+// Norm and rotation of heads.  One tensor's heads: element (head, token, channel) at
+// head * head_stride + token * token_stride + channel.
+struct HeadView {
+  uint16_t* p = nullptr;
+  int64_t head_stride = 0, token_stride = 0;
+};
+struct RopeArgs {
+  const int32_t* positions;  // [tokens, axes]
+  const float* inv_freq;     // [rotary / 2]
+  int rotary, axes, bound[3];  // pairs from bound[i] on belong to axis i + 1 or later
+  bool interleaved, norm;
+  float scale, eps;
+};
+struct RopeSide {
+  HeadView x, y;            // input and output; backward: the saved input and dy
+  HeadView dx;              // backward
+  int64_t heads = 0;
+  const uint16_t* weight = nullptr;  // [head_dim] or nullptr
+  float* dweight = nullptr;          // backward: [head_dim] or nullptr
+};
+hipError_t launch_qk_norm_rope(const RopeSide (&side)[2], int64_t tokens, int head_dim, const RopeArgs& r,
+                               hipStream_t stream);
+size_t qk_backward_bytes(int64_t tokens, int head_dim);
+hipError_t launch_qk_norm_rope_backward(const RopeSide (&side)[2], int64_t tokens, int head_dim, const RopeArgs& r,
+                                        float* ws, hipStream_t stream);
+
 }  // namespace qpl
