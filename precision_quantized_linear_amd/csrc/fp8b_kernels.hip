@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void k_quant_fp8b(const uint16_t* __restrict__
   for (int i = 0; i < QV; ++i) {
     const int64_t j = j0 + 64 * i;
     const RowDiv d = row_div(absmax_value(block_absmax(vec_absmax(v[i], 0u))));
-    if (j < nv) {
+    if (j < (SLAB ? 16 * nb : nv)) {  // the products' rows end with a whole block, zeros behind K
       reinterpret_cast<u32x2*>(xq + row * pitch)[j] = fp8_vec(v[i], d);
       if ((lane & 15) == 0) xs[SLAB ? (j >> 4) * M + row : row * nb + (j >> 4)] = d.s;
     }
@@ -207,10 +207,10 @@ __global__ __launch_bounds__(256) void k_gated_backward(const uint16_t* __restri
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const RowDiv d = row_div(absmax_value(block_absmax(vec_absmax(o[w], 0u))));
-      if (j < nv) {
+      if (j < 16 * nb) {  // zeros behind H
         reinterpret_cast<u32x2*>(q + row * pitch + w * nb * 128)[j] = fp8_vec(o[w], d);
         if ((lane & 15) == 0) s[(w * nb + (j >> 4)) * M + row] = d.s;
-        if (dg) reinterpret_cast<u32x4*>(w == 0 ? dg : du)[row * nv + j] = o[w];
+        if (dg && j < nv) reinterpret_cast<u32x4*>(w == 0 ? dg : du)[row * nv + j] = o[w];
       }
     }
   }
@@ -474,88 +474,176 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_fp8b_token(const uint16_t* __r
 }
 
 // ---------------------------------------------------------------------------
-// The product through LDS, for enough rows to reuse the weight.  A workgroup of WM x WN wavefronts owns 32 WM NJM
-// rows of x by 32 WN NI rows of the weight; a wavefront owns 32 NJ x 32 NI of them (two
-// V_MFMA_SCALE_F32_32X32X64_F8F6F4 per block and 32 x 32 tile, from a zero accumulator, and 16 fmas that fold the
-// sum, so the accumulators stay in vector registers).  Gated: half of a wavefront's NI column tiles belong to the
-// gate, the other half to the same columns of up, so that both projections of an output meet in one lane.
+// The product through LDS, for enough rows to reuse the weight.  A workgroup of WM x WN wavefronts owns 16 WM NJM
+// rows of x by 16 WN NI rows of the weight; a wavefront 16 NJ x 16 NI of them: one V_MFMA_SCALE_F32_16X16X128_F8F6F4
+// per block and 16 x 16 tile, from a zero accumulator, and four fmas that fold its sums, so the accumulators stay in
+// vector registers.  Gated: half of a wavefront's NI column tiles belong to the gate, the other half to the same
+// columns of up, so that both projections of an output meet in one lane.
 //
 // Workgroups are persistent; K is walked in pieces of 128 bytes (a block) of both operands, S stages of them in
-// LDS, filled by buffer_load_dwordx4 ... lds together with the piece's scales: piece P + S - 1's loads are issued
-// between piece P's MFMAs.  The pieces of all of a workgroup's tiles form one stream.  A tile with at most half (a
-// quarter) of its rows present runs with NJ = NJM / 2 (/ 4); the tiles of a last round that is at most half (a
-// quarter) full are cut into such parts, one for each workgroup.
+// LDS, filled by buffer_load_dwordx4 ... lds together with the piece's scales.  The pieces of all of a workgroup's
+// tiles form one stream.  A tile with at most half (a quarter) of its rows present runs with NJ = NJM / 2 (/ 4); the
+// tiles of a last round that is at most half (a quarter) full are cut into such parts, one for each workgroup.
 //
-// Top of a piece: wait for its loads, then a barrier: the piece is in LDS for every wavefront, and every wavefront
-// is done with the piece before, whose stage the next loads fill.  A wavefront's vector memory operations retire in
-// issue order, so the wait names how many later ones may be in flight: the loads of the pieces behind it and the
-// output stores of an epilogue issued after its loads.  A smaller number than that only waits longer.
+// A piece is multiplied row tile by row tile; a tile's sums are folded two MFMAs later.  The sync stands before its
+// last row tile, when all of its operands are in registers: every wavefront waits for its own loads of the next
+// piece, then all meet; the next piece is then in LDS and this piece's stage is free.  Behind it the loads of piece
+// P + S are issued between MFMAs, into the first half of the next piece's, and the next piece's first operands are
+// read, each column tile's as soon as the last row tile is done with the register.  A wavefront's vector memory operations retire in issue order, so the sync's wait names how many later
+// ones may be in flight: the loads of the pieces behind the next and the output stores of an epilogue issued
+// after its loads.  A smaller number than that only waits longer.
 // ---------------------------------------------------------------------------
 struct Fp8bStagedArgs {
   Fp8bArgs g;
   int tiles_m, tiles_n, nwg;
+  uint16_t* y;
+  EpiArgs e;
 };
 
 template <int WM, int WN, int NI, int NJM, int S>
 struct StagedShape {
-  static constexpr int W = WM * WN, XR = 32 * WM * NJM, WR = 32 * WN * NI;
-  static constexpr int SC = (XR + WR) * PR_ROW;       // scales of a stage: XR of x, 64 of each weight
-  static constexpr int STAGE = SC + 4 * XR + 512;
+  static constexpr int W = WM * WN, XR = 16 * WM * NJM, WR = 16 * WN * NI;
+  // a stage: scales (XR of x, 64 of each weight), rows of x, rows of W
+  static constexpr int XB = 4 * XR + 512, WB = XB + XR * PR_ROW, STAGE = WB + WR * PR_ROW;
   static constexpr int LDS = S * STAGE + 256;         // and a spare area
-  static constexpr int per_cu() { return (160 << 10) / LDS; }
+  static constexpr int per_cu() { return (160 << 10) / LDS < 16 / W ? (160 << 10) / LDS : 16 / W; }
   static constexpr int per_simd() { return per_cu() * W / 4; }
 };
+
+// Epilogue of a wavefront's tile: y = bf16 of the accumulators (EPI_GELU: of their GELU).  acc[i][j] holds y^T:
+// element r at lane l is row m0 + 16 j + l % 16, column n0 + 16 i + 4 (l / 16) + r.  Lanes of neighbouring rows of 16
+// exchange words of column tiles i and i + 1 (V_PERMLANE16_SWAP), so that each holds eight consecutive columns: 8 (l /
+// 32) .. of tile i + (l / 16) % 2.  Returns the number of stores left in flight (0 on the edge path, which checks
+// every element and drains its stores).
+template <int NJ, int NI, int EPI, bool ANY, bool FAST, class Acc>
+__device__ __forceinline__ void store16_path(const Acc& acc, int lane, int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                             uint16_t* __restrict__ y, const EpiArgs& e) {
+  const int q = lane >> 4;
+  // loops expanded at compile time, as in store_tile; values, because a choice among an array's elements would become an
+  // index into memory
+  uint16_t *const oq = e.qkv[0], *const ok = e.qkv[1], *const ov = e.qkv[2];
+  const int64_t d = e.d, tokens = e.tokens, off = e.off;
+  const int lg_hd = e.lg_hd;
+  static_for<0, NJ>([&](auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
+    const int64_t m = m0 + 16 * j + (lane & 15);
+    static_for<0, NI / 2>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = 2 * decltype(ic)::value;
+      uint32_t w[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float o[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = (EPI & EPI_GELU) != 0 ? gelu_tanh(acc[i + t][j][r]) : acc[i + t][j][r];
+        w[t][0] = pack_bf16(o[0], o[1]);
+        w[t][1] = pack_bf16(o[2], o[3]);
+      }
+      const auto a = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
+      const auto b = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
+      const u32x4 v{a[0], b[0], a[1], b[1]};
+      const int64_t n = n0 + 16 * (i + (q & 1)) + 8 * (q >> 1);
+      uint16_t* dst = y + m * N + n;
+      if constexpr ((EPI & EPI_QKV) != 0) {  // as out_ptr, without an array indexed by the part; eight columns are of one head
+        const bool k = n >= d, v2 = n >= 2 * d;
+        const int64_t c = n - (v2 ? 2 * d : k ? d : 0), hd = c >> lg_hd;
+        dst = (v2 ? ov : k ? ok : oq) + (((hd * tokens + off + m) << lg_hd) + (c & ((int64_t{1} << lg_hd) - 1)));
+      }
+      if constexpr (FAST && !ANY) {
+        *reinterpret_cast<u32x4*>(dst) = v;
+      } else if constexpr (FAST) {
+        reinterpret_cast<Segment*>(dst)->v = v;
+      } else if (m < M) {
+        if (n + 8 <= N) {
+          reinterpret_cast<Segment*>(dst)->v = v;
+        } else {
+          const uint32_t el[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (n + c < N) dst[c] = (uint16_t)(el[c >> 1] >> (16 * (c & 1)));
+        }
+      }
+    });
+    __builtin_amdgcn_sched_barrier(0);  // a row tile at a time: registers
+  });
+}
+
+template <int NJ, int NI, int EPI, bool ANY, class Acc>
+__device__ __forceinline__ int store16(const Acc& acc, int lane_, int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                       uint16_t* __restrict__ y, const EpiArgs& e) {
+  int lane = lane_;
+  asm volatile("" : "+v"(lane));  // what follows is not to be computed before the products, where registers are scarce
+  if (m0 + 16 * NJ <= M && n0 + 16 * NI <= N) {
+    store16_path<NJ, NI, EPI, ANY, true>(acc, lane, m0, n0, M, N, y, e);
+    return NJ * NI / 2;
+  }
+  store16_path<NJ, NI, EPI, ANY, false>(acc, lane, m0, n0, M, N, y, e);
+  QPL_WAIT_VMCNT(0);
+  return 0;
+}
 
 template <int WM, int WN, int NI, int NJM, int S, bool GATED, int EPI>
 __global__ __launch_bounds__(64 * WM * WN)
 __attribute__((amdgpu_waves_per_eu((StagedShape<WM, WN, NI, NJM, S>::per_simd()),
                                    (StagedShape<WM, WN, NI, NJM, S>::per_simd())))) void
-k_fp8b_staged(Fp8bStagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
+k_fp8b_staged(Fp8bStagedArgs) {
   using C = StagedShape<WM, WN, NI, NJM, S>;
-  constexpr int W = C::W, XR = C::XR, WR = C::WR, SC = C::SC, STAGE = C::STAGE;
+  constexpr int W = C::W, XR = C::XR, WR = C::WR, XB = C::XB, WB = C::WB, STAGE = C::STAGE;
   constexpr int NO = GATED ? NI / 2 : NI;              // column tiles of outputs per wavefront
-  constexpr int COLS = 32 * WN * NO;                   // output columns of a tile
+  constexpr int COLS = 16 * WN * NO;                   // output columns of a tile
   constexpr int XL = XR / 8 / W, WL = WR / 8 / W;      // loads per wavefront per piece: x, W
   constexpr int LOADS = XL + WL + 1;                   // and one of scales
   static_assert(XR / 64 + 2 <= W, "one load of scales per wavefront");
   static_assert((XR / W) % 16 == 0 && (WR / W) % 16 == 0, "the swizzle of a load's rows");
+  static_assert(!GATED || (WM == 2 && NO % 2 == 0), "a wavefront loads rows of one weight");
   __shared__ __attribute__((aligned(16))) uint8_t lds[C::LDS];
-  const Fp8bArgs& p = a.g;
+  // The arguments are read where they are needed, from the kernel's argument block: held in scalar registers through
+  // the loop over K they would push its own values out of them.
+  using Args = const __attribute__((address_space(4))) Fp8bStagedArgs;
+  auto args = []() {
+    Args* p = (Args*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+  };
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wm = wv / WN, wn = wv % WN;
-  const int h = lane >> 5, r32 = lane & 31;
-  const int b = blockIdx.x;
+  const int q = lane >> 4, r16 = lane & 15;
   const uint32_t lbase = lds_address(lds);
-  const int ntiles = a.tiles_m * a.tiles_n;
-  const int np = p.pieces * p.segs;
+  const int pieces = args()->g.pieces, np = pieces * args()->g.segs;
 
   struct Tile {
     int64_t m0, n0;
     int rows;
   };
-  const int full = ntiles - ntiles % a.nwg, tail = ntiles - full;
-  const int parts = NJM >= 4 && 4 * tail <= a.nwg ? 4 : NJM >= 2 && 2 * tail <= a.nwg ? 2 : 1;
-  const int units = full + tail * parts;
-  // This workgroup's i-th unit (units: none).  Workgroups are dealt to the 8 XCDs in turn; in every round, the
-  // last and shorter one too, an XCD's workgroups take a contiguous run of units.
-  auto position = [&](int i) {
-    const int base = i * a.nwg, left = min(units - base, a.nwg);
-    if (left <= 0) return units;
-    const int each = (left + 7) >> 3, at = (b & 7) * each + (b >> 3);
-    if ((a.nwg & 7) != 0) return b < left ? base + b : units;
-    return (b >> 3) < each && at < left ? base + at : units;
-  };
+  // This workgroup's i-th unit: a tile, or a part of one of the last round's; rows <= 0 if there is none.
+  // Workgroups are dealt to the 8 XCDs in turn; in every round, the last and shorter one too, an XCD's workgroups
+  // take a contiguous run of units.
   auto tile = [&](int i) {
-    Tile t;
+    Args* a = args();
+    const int nwg = a->nwg, ntiles = a->tiles_m * a->tiles_n, b = blockIdx.x;
+    const int full = ntiles - ntiles % nwg, tail = ntiles - full;
+    const int parts = NJM >= 8 && 4 * tail <= nwg ? 4 : NJM >= 4 && 2 * tail <= nwg ? 2 : 1;
+    const int units = full + tail * parts;
+    const int base = i * nwg, left = min(units - base, nwg);
+    const int each = (left + 7) >> 3, at = (b & 7) * each + (b >> 3);
+    int u = -1;
+    if (left > 0) {
+      if ((nwg & 7) != 0) {
+        u = b < left ? base + b : -1;
+      } else {
+        u = (b >> 3) < each && at < left ? base + at : -1;
+      }
+    }
+    Tile t{0, 0, 0};
+    if (u < 0) return t;
     int tm, tn;
-    const int u = position(i);
     const bool whole = u < full;
     const int cut = whole ? 0 : (u - full) % parts;
-    walk(whole ? u : full + (u - full) / parts, a.tiles_m, a.tiles_n, tm, tn);
+    walk(whole ? u : full + (u - full) / parts, a->tiles_m, a->tiles_n, tm, tn);
     t.n0 = (int64_t)tn * COLS;
     t.m0 = (int64_t)tm * XR;
-    t.rows = (int)(p.M - t.m0 < XR ? p.M - t.m0 : XR);
+    const int64_t M = a->g.M;
+    t.rows = (int)(M - t.m0 < XR ? M - t.m0 : XR);
     if (!whole && parts > 1) {
       const int first = XR / parts * cut;
       t.m0 += first;
@@ -563,124 +651,117 @@ k_fp8b_staged(Fp8bStagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     }
     return t;
   };
-  int nt = 0;
-  while (position(nt) < units) ++nt;
-  if (nt > 0 && tile(nt - 1).rows <= 0) --nt;  // a part behind its tile's last row
 
-  // load q of an operand: stage rows (rows / W) wv + 8 q .. + 7; lane l fills row + l / 8, stage chunk l % 8, with
-  // the row's chunk (l % 8) ^ ((row / 2) % 8) = lc ^ 4 (q % 2)
+  // load n of an operand: stage rows (rows / W) wv + 8 n .. + 7; lane l fills row + l / 8, stage chunk l % 8, with
+  // the row's chunk (l % 8) ^ ((row / 2) % 8) = lc ^ 4 (n % 2).  Gated: the rows of a wavefront's share all belong to
+  // the gate (even wavefronts) or to up.
   const int lc = (lane & 7) ^ (lane >> 4);
-
-  // The stream of pieces.
-  struct Piece {
-    int kx, kw, stage;
-    bool valid, second;
-  };
-  int s_i = 0, s_k = 0, s_stage = 0;
-  Tile st_tile{};
-  u32x4 dx{}, dwa{}, dwb{}, ds{};  // dwa, dwb: of the two weights
+  uint32_t vx, vw;
+  {
+    const int wrow = GATED ? (wv >> 1) * (WR / W) : wv * (WR / W);
+    vx = (uint32_t)((XR / W * wv + (lane >> 3)) * args()->g.px + 16 * lc);
+    vw = (uint32_t)((wrow + (lane >> 3)) * args()->g.K + 16 * lc);
+  }
   const int job = wv < XR / 64 ? 0 : wv - XR / 64 + 1;  // scales: of x, of the first weight, of the second
-  auto enter = [&](int i) {
-    st_tile = tile(i);
-    const int rn = (int)(p.N - st_tile.n0 < COLS ? p.N - st_tile.n0 : COLS);
-    dx = make_desc(p.x + st_tile.m0 * p.px, (int64_t)st_tile.rows * p.px);
-    dwa = make_desc(p.w[0] + st_tile.n0 * p.K, (int64_t)rn * p.K);
-    dwb = make_desc(p.w[1] + st_tile.n0 * p.K, (int64_t)rn * p.K);
+  const bool scales = job <= (GATED ? 2 : 1);
+  uint32_t vs = kOutOfRange;
+  if (job == 0) vs = (uint32_t)((64 * wv + lane) * 4);
+  if (job != 0 && scales && lane < (COLS + 127) / 128) vs = (uint32_t)(lane * pieces * 4);
+
+  // The stream of pieces: what the loads of the next one need.  Past the last tile the operands have no rows, and
+  // zeros are loaded.
+  int s_i = 0, s_k = 0, s_stage = 0;  // tile, piece, stage
+  const uint8_t *xp = nullptr, *wp = nullptr;
+  const float* sp = nullptr;
+  int x_bytes = 0, w_bytes = 0, sp_bytes = 0, sp_step = 0, kx = 0, kw = 0;
+  int64_t s_n0 = 0;
+  auto weight = [&](int which) {  // rows and scales of the tile in one of the weights
+    Args* a = args();
+    const int rn = (int)(a->g.N - s_n0 < COLS ? a->g.N - s_n0 : COLS);
+    const int row_part = GATED ? wv & 1 : which;
+    wp = (row_part ? a->g.w[1] : a->g.w[0]) + s_n0 * a->g.K;
+    w_bytes = rn * a->g.K;
+    if (job == 0) return;
+    // one scale for every 128 rows of the weight, whose rows of scales are `pieces` long
+    const int scale_part = GATED ? job - 1 : which;
+    const int64_t nb0 = s_n0 >> 7, left = ((a->g.N + 127) >> 7) - nb0;
+    const int nb = (int)(left < (COLS + 127) / 128 ? left : (COLS + 127) / 128);
+    sp = (scale_part ? a->g.ws[1] : a->g.ws[0]) + nb0 * pieces;
+    sp_bytes = ((nb - 1) * pieces + 1) * 4;
+    sp_step = 1;
   };
-  // the piece to load next; its loads have to be issued before the following call
+  // moves the stream to the piece to load next; its loads have to be issued before the following call
+  int l_stage = 0;
   auto next_piece = [&]() {
-    Piece r;
-    r.valid = s_i < nt;
-    if (s_k == 0 && r.valid) enter(s_i);
-    r.stage = s_stage;
-    r.second = s_k >= p.pieces;  // of two segments
-    r.kx = s_k * PR_ROW;
-    r.kw = (r.second ? s_k - p.pieces : s_k) * PR_ROW;
-    if (r.valid) {
-      if (job == 0) {
-        ds = make_desc(p.xs + (int64_t)s_k * p.M + st_tile.m0, st_tile.rows * 4);
-      } else {
-        // one scale for every 128 rows of the weight, whose rows of scales are `pieces` long
-        const bool which = GATED ? job == 2 : r.second;
-        const int64_t nb0 = st_tile.n0 >> 7, left = ((p.N + 127) >> 7) - nb0;
-        const int nb = (int)(left < (COLS + 127) / 128 ? left : (COLS + 127) / 128);
-        const int c = r.second ? s_k - p.pieces : s_k;
-        ds = make_desc((which ? p.ws[1] : p.ws[0]) + nb0 * p.pieces + c, ((int64_t)(nb - 1) * p.pieces + 1) * 4);
-      }
-    }
+    l_stage = s_stage;
     s_stage = s_stage == S - 1 ? 0 : s_stage + 1;
+    kx += PR_ROW;
+    kw += PR_ROW;
+    sp += sp_step;
+    if (s_k == 0 || s_k == pieces) {  // a tile, or the second of two segments
+      if (s_k == 0) {
+        const Tile t = tile(s_i);
+        kx = 0;
+        x_bytes = w_bytes = sp_bytes = 0;
+        if (t.rows > 0) {
+          Args* a = args();
+          s_n0 = t.n0;
+          xp = a->g.x + t.m0 * a->g.px;
+          x_bytes = t.rows * a->g.px;
+          weight(0);
+          if (job == 0) {
+            sp = a->g.xs + t.m0;
+            sp_bytes = t.rows * 4;
+            sp_step = (int)a->g.M;
+          }
+        }
+      } else if (x_bytes > 0) {
+        weight(1);
+      }
+      kw = 0;
+    }
     if (++s_k == np) {
       s_k = 0;
       ++s_i;
     }
-    return r;
   };
-  auto issue = [&](const Piece& s, int d) {
-    const uint32_t st = lbase + s.stage * STAGE;
-    if (d < XL + WL) {
-      const bool isx = d < XL;
-      const int q = isx ? d : d - XL;
-      const int byte = 16 * (lc ^ (4 * (q & 1)));
-      const bool in = s.valid && s.kw + byte < p.K;
-      const int row = (isx ? XR : WR) / W * wv + 8 * q;  // of the stage
-      int from = row, which = s.second ? 1 : 0;          // of the operand
-      if (!isx && GATED) {
-        const int in_wave = row % (32 * NI);
-        from = row / (32 * NI) * (16 * NI) + in_wave % (16 * NI);
-        which = in_wave / (16 * NI);
-      }
-      const int pitch = isx ? p.px : p.K;
-      const uint32_t vo = in ? (uint32_t)((from + (lane >> 3)) * pitch + byte) : kOutOfRange;
-      u32x4 desc = dx;
-      if (!isx) {
-        // chosen part by part: a select of whole descriptors ends in vector registers
-#pragma unroll
-        for (int i = 0; i < 4; ++i) desc[i] = __builtin_amdgcn_readfirstlane(which ? dwb[i] : dwa[i]);
-      }
-      dma16(st + (isx ? row : XR + row) * PR_ROW, vo, desc, isx ? s.kx : s.kw);
+  auto issue = [&](int d, int px, int pw) {  // px, pw: pitches of x and W
+    const uint32_t st = lbase + l_stage * STAGE;
+    if (d < XL) {
+      dma16(st + XB + (XR / W * wv + 8 * d) * PR_ROW, d & 1 ? vx ^ 64 : vx, make_desc(xp, x_bytes), kx + 8 * d * px);
+    } else if (d < XL + WL) {
+      const int n = d - XL;
+      dma16(st + WB + (WR / W * wv + 8 * n) * PR_ROW, n & 1 ? vw + (lane & 4 ? -64 : 64) : vw, make_desc(wp, w_bytes), kw + 8 * n * pw);
     } else {
-      const bool real = s.valid && (job == 0 || job == 1 || (GATED && job == 2));
-      uint32_t vo = kOutOfRange;
-      if (real) vo = job == 0 ? (uint32_t)((64 * wv + lane) * 4) : (uint32_t)lane < (COLS + 127) / 128 ? (uint32_t)(lane * p.pieces * 4) : kOutOfRange;
-      dma4(real ? st + SC + (job == 0 ? 256 * wv : 4 * XR + 256 * (job - 1)) : lbase + S * STAGE, vo, ds, 0);
+      dma4(scales ? st + (job == 0 ? 256 * wv : 4 * XR + 256 * (job - 1)) : lbase + S * STAGE, vs,
+           make_desc(sp, sp_bytes), 0);
     }
   };
 
-  struct Frag {
-    i32x8 lo, hi;
+  // fragment of 16 rows: lane l has chunks l / 16 and 4 + l / 16 of row l % 16
+  const int at0 = r16 * PR_ROW + ((q ^ (r16 >> 1)) << 4), at1 = at0 ^ 64;
+  auto frag = [&](const uint8_t* a, const uint8_t* b) {
+    return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(a), *reinterpret_cast<const i32x4*>(b), 0, 1, 2, 3, 4,
+                                   5, 6, 7);
   };
-  auto frag = [&](const uint8_t* st, int row) {
-    i32x4 c[4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) c[2 * u + t] = *reinterpret_cast<const i32x4*>(st + chunk_at(row, 4 * u + 2 * h + t));
-    return Frag{__builtin_shufflevector(c[0], c[1], 0, 1, 2, 3, 4, 5, 6, 7),
-                __builtin_shufflevector(c[2], c[3], 0, 1, 2, 3, 4, 5, 6, 7)};
-  };
-  auto mma = [&](const i32x8& w, const i32x8& x, const f32x16& c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 0, 127, 0, 127);
+  auto mma = [&](const i32x8& w, const i32x8& x) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{}, 0, 0, 0, 127, 0, 127);
   };
 
-#pragma unroll
-  for (int ahead = 0; ahead < S - 1; ++ahead) {
-    const Piece s = next_piece();
-#pragma unroll
-    for (int d = 0; d < LOADS; ++d) issue(s, d);
-  }
-  constexpr int LATER = (S - 2) * LOADS;                    // loads of the pieces behind the current one
-  constexpr int STORES = 2 * NO * NJM;                      // output stores of a whole tile
+  constexpr int LATER = (S - 2) * LOADS;        // loads of the pieces behind the next
+  constexpr int STORES = NO * NJM / 2;          // output stores of a whole tile
   static_assert(LATER + STORES < 64, "vmcnt holds 63");
-  int st[S - 1] = {};  // stores issued by the epilogue after each of the last S - 1 pieces
-  int cur = 0;         // stage of the piece being multiplied
-  auto piece = [&](auto& acc, auto nj) {
-    constexpr int NJ = decltype(nj)::value;
-    constexpr int T = NI * NJ;  // tiles of 32 x 32 per wavefront
-    int stores = 0;
+  int stores[S - 1] = {};  // left in flight by the epilogue after each of the last S - 1 pieces
+  int cur = 0;             // stage of the piece being multiplied
+  i32x8 fw[NI], fx[2];     // operands: the weight's column tiles, row tile j in fx[j % 2]
+  float sw[2], sx[2];      // their scales
+
+  auto sync = [&]() {
+    QPL_WAIT_LGKM0();
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) stores += st[i];
-    QPL_WAIT_LGKM0();  // this wavefront is done with the stage that the next loads fill
-    if (stores >= STORES) {
+    for (int i = 0; i < S - 1; ++i) n += stores[i];
+    if (n >= STORES) {
       QPL_WAIT_VMCNT(LATER + STORES);
     } else {
       QPL_WAIT_VMCNT(LATER);
@@ -688,79 +769,166 @@ k_fp8b_staged(Fp8bStagedArgs a, uint16_t* __restrict__ Y, EpiArgs e) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = S - 2; i > 0; --i) st[i] = st[i - 1];
-    st[0] = 0;
-    const Piece s = next_piece();
-    const uint8_t* cs = lds + cur * STAGE;
-    const uint8_t* cw = cs + XR * PR_ROW;
-    cur = cur == S - 1 ? 0 : cur + 1;
-    const float* lx = reinterpret_cast<const float*>(cs + SC);
-    const float* lw = lx + XR;
-    Frag fw[NI], fx[2];
+    for (int i = S - 2; i > 0; --i) stores[i] = stores[i - 1];
+    stores[0] = 0;
+  };
+  // where a wavefront that owns nj row tiles finds its operands in stage st
+  struct Source {
+    const uint8_t *x0, *x1, *w0, *w1;
+    const float *sx, *sw;
+  };
+  auto source = [&](int st, int nj) {
+    const uint8_t* s = lds + st * STAGE;
+    const uint8_t* x = s + XB + wm * 16 * nj * PR_ROW;
+    const uint8_t* w = s + WB + wn * 16 * NI * PR_ROW;
+    const float* f = reinterpret_cast<const float*>(s);
+    return Source{x + at0, x + at1, w + at0, w + at1, f + wm * 16 * nj + r16, f + XR + ((wn * 16 * NO) >> 7)};
+  };
+  auto read_x = [&](const Source& s, int j) {
+    fx[j & 1] = frag(s.x0 + 16 * PR_ROW * j, s.x1 + 16 * PR_ROW * j);
+    sx[j & 1] = s.sx[16 * j];
+  };
+  auto read_w = [&](const Source& s, int i) { fw[i] = frag(s.w0 + 16 * PR_ROW * i, s.w1 + 16 * PR_ROW * i); };
+  auto read_scales = [&](const Source& s) {
+    sw[0] = s.sw[0];
+    sw[1] = GATED ? s.sw[64] : sw[0];
+  };
+
 #pragma unroll
-    for (int i = 0; i < NI; ++i) fw[i] = frag(cw, wn * 32 * NI + i * 32 + r32);
-    fx[0] = frag(cs, wm * 32 * NJ + r32);
-    float sx[NJ], sw[2];
+  for (int ahead = 0; ahead < S; ++ahead) {
+    next_piece();
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) sx[j] = lx[wm * 32 * NJ + j * 32 + r32];
-    sw[0] = lw[(wn * 32 * NO) >> 7];
-    sw[1] = GATED ? lw[64 + ((wn * 32 * NO) >> 7)] : sw[0];
-    f32x16 pr[2];
+    for (int d = 0; d < LOADS; ++d) issue(d, args()->g.px, args()->g.K);
+  }
+  QPL_WAIT_VMCNT((S - 1) * LOADS);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  // loads issued behind the sync, one after each of a piece's last MFMAs; the others follow between the first half of
+  // the next piece's
+  constexpr int EARLY = (LOADS + 2) / 3, LATE = LOADS - EARLY;
+  // One piece, its first operands in registers.  first: of a tile, whose loads have been issued; last: of a tile, whose
+  // next piece's operands are read when the accumulators have been stored and the registers are free.
+  auto piece = [&](auto& acc, auto nj, auto first, auto last, int px, int pw) {
+    constexpr int NJ = decltype(nj)::value, T = NI * NJ;
+    constexpr bool FIRST = decltype(first)::value, LAST = decltype(last)::value;
+    constexpr int LAG = 2;  // MFMAs between a tile's own and the fold of its sums
+    const int nxt = cur == S - 1 ? 0 : cur + 1;
+    const Source now = source(cur, NJ);
+    // a load's offset is made when it is issued: kept for all loads they would not fit the registers, and a reload
+    // from memory would wait for every load in flight
+    asm volatile("" : "+s"(px), "+s"(pw));
+    f32x4 pr[3];
+    float f[2][2];  // scales of row tile j and of either weight's column tiles
     auto fold = [&](auto tc) __attribute__((always_inline)) {
       constexpr int t = decltype(tc)::value, i = t % NI, j = t / NI;
-      const float f = sx[j] * sw[i >= NO ? 1 : 0];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(pr[t & 1][r], f, acc[i][j][r]);
+      fold4(acc[i][j], pr[t % 3], f[j & 1][i >= NO ? 1 : 0]);
+      // kept where it stands: the compiler would move all folds behind the sync's branches, and keep every sum till then
+      asm volatile("" : "+v"(acc[i][j]));
     };
-    static_for<0, T>([&](auto tc) __attribute__((always_inline)) {
-      constexpr int t = decltype(tc)::value, i = t % NI, j = t / NI;
-      pr[t & 1] = mma(fw[i].lo, fx[j & 1].lo, f32x16{});
-      pr[t & 1] = mma(fw[i].hi, fx[j & 1].hi, pr[t & 1]);
-      if constexpr (i == 0 && j + 1 < NJ) fx[(j + 1) & 1] = frag(cs, wm * 32 * NJ + (j + 1) * 32 + r32);
-      if constexpr (t > 0) fold(std::integral_constant<int, t - 1>{});
+    static_for<0, NJ>([&](auto jc) __attribute__((always_inline)) {
+      constexpr int j = decltype(jc)::value;
+      f[j & 1][0] = sx[j & 1] * sw[0];
+      f[j & 1][1] = GATED ? sx[j & 1] * sw[1] : f[j & 1][0];
+      Source next;
+      if constexpr (j + 1 < NJ) {
+        read_x(now, j + 1);
+      } else {
+        sync();
+        next_piece();
+        if constexpr (!LAST) {
+          next = source(nxt, NJ);
+          read_x(next, 0);
+          read_scales(next);
+        }
+      }
+      static_for<0, NI>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value, t = NI * j + i;
+        pr[t % 3] = mma(fw[i], fx[j & 1]);
+        if constexpr (t >= LAG) fold(std::integral_constant<int, t - LAG>{});
+        if constexpr (j + 1 == NJ) {
+          if constexpr (!LAST) read_w(next, i);
 #pragma unroll
-      for (int d = 0; d < LOADS; ++d)
-        if (t == (d * T) / LOADS) issue(s, d);
-      __builtin_amdgcn_sched_barrier(0);
+          for (int d = 0; d < EARLY; ++d)
+            if (d * NI / EARLY == i) issue(d, px, pw);
+        } else if constexpr (!FIRST) {
+#pragma unroll
+          for (int d = 0; d < LATE; ++d)
+            if (d * (T / 2) / LATE == t) issue(EARLY + d, px, pw);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
     });
-    fold(std::integral_constant<int, T - 1>{});
+    static_for<T - LAG, T>(fold);
+    cur = nxt;
   };
+  using Yes = std::integral_constant<bool, true>;
+  using No = std::integral_constant<bool, false>;
   auto run_tile = [&](const Tile& t, auto nj) {
     constexpr int NJ = decltype(nj)::value;
-    f32x16 acc[NI][NJ];
+    f32x4 acc[NI][NJ];
 #pragma unroll
     for (int x = 0; x < NI; ++x)
 #pragma unroll
-      for (int y = 0; y < NJ; ++y) acc[x][y] = f32x16{};
-    for (int k = 0; k < np; ++k) piece(acc, nj);
-    const auto one = [](int) { return 1.0f; };
-    const auto ones = [](int) { return f32x4{1.0f, 1.0f, 1.0f, 1.0f}; };
+      for (int y = 0; y < NJ; ++y) acc[x][y] = f32x4{};
+    const int px = args()->g.px, pw = args()->g.K;
+    const Source s = source(cur, NJ);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) read_w(s, i);
+    read_x(s, 0);
+    read_scales(s);
+    if (np == 1) {
+      piece(acc, nj, Yes{}, Yes{}, px, pw);
+    } else {
+      piece(acc, nj, Yes{}, No{}, px, pw);
+      for (int k = 2; k < np; ++k) piece(acc, nj, No{}, No{}, px, pw);
+      piece(acc, nj, No{}, Yes{}, px, pw);
+    }
+    // before the output stores, because a load behind them could not be waited for without them
+#pragma unroll
+    for (int d = EARLY; d < LOADS; ++d) issue(d, px, pw);
+    Args* a = args();
+    const int64_t m0 = t.m0 + wm * 16 * NJ, n0 = t.n0 + wn * 16 * NO, m1 = t.m0 + t.rows, N = a->g.N;
+    EpiArgs e{};
+    if constexpr ((EPI & EPI_QKV) != 0) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) e.qkv[i] = a->e.qkv[i];
+      e.d = a->e.d;
+      e.tokens = a->e.tokens;
+      e.off = a->e.off;
+      e.lg_hd = a->e.lg_hd;
+    }
+    uint16_t* y = a->y;
     int left = 0;
     if constexpr (GATED) {
-      if (p.save[0]) {
-        left += store_tile<NJ, NO>(acc, wm, wn, lane, t.m0, t.n0, t.m0 + t.rows, p.N, p.save[0], one, ones);
-        left += store_tile<NJ, NO>(acc + NO, wm, wn, lane, t.m0, t.n0, t.m0 + t.rows, p.N, p.save[1], one, ones);
+      uint16_t *g = a->g.save[0], *u = a->g.save[1];
+      if (g) {
+        left += store16<NJ, NO, 0, false>(acc, lane, m0, n0, m1, N, g, e);
+        left += store16<NJ, NO, 0, false>(acc + NO, lane, m0, n0, m1, N, u, e);
       }
 #pragma unroll
       for (int i = 0; i < NO; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] = gate_act<EPI>(acc[i][j][r]) * acc[i + NO][j][r];
-      left += store_tile<NJ, NO>(acc, wm, wn, lane, t.m0, t.n0, t.m0 + t.rows, p.N, Y, one, ones);
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = gate_act<EPI>(acc[i][j][r]) * acc[i + NO][j][r];
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      left += store16<NJ, NO, 0, false>(acc, lane, m0, n0, m1, N, y, e);
     } else {
-      left = store_tile<NJ, NO, EPI, true>(acc, wm, wn, lane, t.m0, t.n0, t.m0 + t.rows, p.N, Y, one, ones, e);
+      left = store16<NJ, NO, EPI, true>(acc, lane, m0, n0, m1, N, y, e);
     }
-    st[0] = __builtin_amdgcn_readfirstlane(left);
+    stores[0] = __builtin_amdgcn_readfirstlane(left);
   };
-  for (int i = 0; i < nt; ++i) {
+  for (int i = 0;; ++i) {
     const Tile t = tile(i);
-    if (NJM == 1 || t.rows > XR / 2) {
+    if (t.rows <= 0) break;  // none, or a part behind its tile's last row
+    if (NJM <= 2 || t.rows > XR / 2) {
       run_tile(t, std::integral_constant<int, NJM>{});
-    } else if (NJM == 2 || t.rows > XR / 4) {
-      if constexpr (NJM >= 2) run_tile(t, std::integral_constant<int, NJM / 2>{});
+    } else if (NJM <= 4 || t.rows > XR / 4) {
+      if constexpr (NJM >= 4) run_tile(t, std::integral_constant<int, NJM / 2>{});
     } else {
-      if constexpr (NJM >= 4) run_tile(t, std::integral_constant<int, NJM / 4>{});
+      if constexpr (NJM >= 8) run_tile(t, std::integral_constant<int, NJM / 4>{});
     }
   }
   QPL_WAIT_VMCNT(0);
@@ -826,7 +994,7 @@ struct Staged {
   hipStream_t stream;
   template <bool GATED, int EPI>
   hipError_t run() const {
-    if constexpr (GATED && NI == 1) {
+    if constexpr (GATED && NI == 2) {
       return hipErrorInvalidValue;
     } else {
       constexpr int COLS = GATED ? C::WR / 2 : C::WR;
@@ -834,10 +1002,12 @@ struct Staged {
       a.g = p;
       a.tiles_m = (int)((p.M + C::XR - 1) / C::XR);
       a.tiles_n = (int)((p.N + COLS - 1) / COLS);
-      const int64_t n = (int64_t)a.tiles_m * a.tiles_n * NJM, most = 256 * C::per_cu();
+      const int64_t n = (int64_t)a.tiles_m * a.tiles_n * (NJM / 2), most = 256 * C::per_cu();
       a.nwg = (int)(n < most ? n : most);
+      a.y = y;
+      a.e = e;
       hipLaunchKernelGGL((k_fp8b_staged<WM, WN, NI, NJM, S, GATED, EPI>), dim3((unsigned)a.nwg), dim3(64 * C::W), 0, stream,
-                         a, y, e);
+                         a);
       return hipGetLastError();
     }
   }
@@ -847,10 +1017,10 @@ hipError_t launch_product(const Fp8bArgs& p, bool gated, int kind, uint16_t* y, 
   switch (fp8b_shape(p.M, (int64_t)p.pieces * p.segs, gated ? 2 * p.N : p.N, gated)) {
     case 0: return with_epilogue(Direct<1, 2, 8, 2>{p, y, e, stream}, gated, kind);
     case 1: return with_epilogue(Direct<2, 2, 8, 2>{p, y, e, stream}, gated, kind);
-    case 2: return with_epilogue(Staged<2, 2, 1, 1, 4>{p, y, e, stream}, gated, kind);
-    case 3: return with_epilogue(Staged<2, 2, 2, 1, 3>{p, y, e, stream}, gated, kind);
-    case 4: return with_epilogue(Staged<2, 2, 2, 2, 2>{p, y, e, stream}, gated, kind);
-    default: return with_epilogue(Staged<2, 4, 2, 4, 2>{p, y, e, stream}, gated, kind);
+    case 2: return with_epilogue(Staged<2, 2, 2, 2, 4>{p, y, e, stream}, gated, kind);
+    case 3: return with_epilogue(Staged<2, 2, 4, 2, 3>{p, y, e, stream}, gated, kind);
+    case 4: return with_epilogue(Staged<2, 2, 4, 4, 2>{p, y, e, stream}, gated, kind);
+    default: return with_epilogue(Staged<2, 4, 4, 8, 2>{p, y, e, stream}, gated, kind);
   }
 }
 
@@ -872,7 +1042,7 @@ Fp8bArgs product_args(const Fp8bWeight* w, int n, int64_t M, int64_t K, int64_t 
 
 hipError_t launch_quant_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t pitch, bool slab, uint8_t* xq, float* xs,
                              hipStream_t stream) {
-  const int64_t chunks = (K / 8 + 64 * QV - 1) / (64 * QV);
+  const int64_t chunks = (pitch / 8 + 64 * QV - 1) / (64 * QV);
   const dim3 grid((unsigned)((M + 3) / 4 * chunks)), block(256);
   if (slab) {
     hipLaunchKernelGGL(k_quant_fp8b<true>, grid, block, 0, stream, x, M, K, pitch, (uint32_t)chunks, xq, xs);
@@ -900,7 +1070,7 @@ hipError_t launch_transpose_fp8b(const uint8_t* w, const float* ws, int64_t N, i
 
 hipError_t launch_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M, int64_t H,
                                  bool silu, uint16_t* dg, uint16_t* du, uint8_t* q, float* s, hipStream_t stream) {
-  const int64_t chunks = (H / 8 + 64 * GV - 1) / (64 * GV), pitch = 2 * ((H + 127) / 128 * 128);
+  const int64_t chunks = ((H + 127) / 128 * 16 + 64 * GV - 1) / (64 * GV), pitch = 2 * ((H + 127) / 128 * 128);
   const dim3 grid((unsigned)((M + 3) / 4 * chunks)), block(256);
   if (silu) {
     hipLaunchKernelGGL(k_gated_backward<true>, grid, block, 0, stream, dh, g, u, M, H, pitch, (uint32_t)chunks, dg, du, q, s);

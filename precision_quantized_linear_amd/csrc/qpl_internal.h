@@ -161,14 +161,14 @@ struct Fp8bWeight {
   const uint8_t* codes;
   const float* scales;
 };
-constexpr int64_t fp8b_pitch(int64_t K) { return K < 512 ? K : (K + 127) / 128 * 128; }
+constexpr int64_t fp8b_pitch(int64_t K) { return (K + 127) / 128 * 128; }
 hipError_t launch_quant_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t pitch, bool slab, uint8_t* xq, float* xs,
                              hipStream_t stream);
 hipError_t launch_quant_weight_fp8b(const uint16_t* w, int64_t N, int64_t K, uint8_t* wq, float* ws,
                                     hipStream_t stream);
 hipError_t launch_transpose_fp8b(const uint8_t* w, const float* ws, int64_t N, int64_t K, uint8_t* wt, float* wst,
                                  hipStream_t stream);
-// Product of the codes of x (rows fp8b_pitch(K) apart, scales slab-major), or, for so few rows that one launch
+// Product of the codes of x (rows fp8b_pitch(K) apart, zeros behind K, scales slab-major), or, for so few rows that one launch
 // quantizes and multiplies them (fp8b_one_launch), of x itself.
 bool fp8b_one_launch(int64_t M, int64_t K);
 hipError_t launch_fp8b_token(const uint16_t* x, const Fp8bWeight& w, int64_t M, int64_t K, int64_t N,
@@ -180,7 +180,7 @@ hipError_t launch_gemm_fp8b(const uint8_t* xq, const float* xs, const Fp8bWeight
 hipError_t launch_fp8b_gated(const uint16_t* x, const uint8_t* xq, const float* xs, const Fp8bWeight (&w)[2], int64_t M,
                              int64_t K, int64_t H, bool silu, uint16_t* h, uint16_t* const (&save)[2],
                              hipStream_t stream);
-// Its backward: dg and du [M, H] in bf16 (nullptrs: not written), their codes q [M, 2 (H rounded up to 128)] and
+// Its backward: dg and du [M, H] in bf16 (nullptrs: not written), their codes q [M, 2 (H rounded up to 128)], zeros behind H, and
 // scales s [2 ceil(H / 128), M]; then y [M, N] = (q's first half) w[0]^T + (second half) w[1]^T, weights [N, K].
 hipError_t launch_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M, int64_t H,
                                  bool silu, uint16_t* dg, uint16_t* du, uint8_t* q, float* s, hipStream_t stream);
