@@ -961,6 +961,7 @@ struct Direct {
   hipStream_t stream;
   template <bool GATED, int EPI>
   hipError_t run() const {
+    if constexpr (GATED && NT == 1) return hipErrorInvalidValue;
     constexpr int N_T = GATED && NT > 1 ? NT / 2 : NT;
     const int64_t tn = (p.N + 16 * N_T - 1) / (16 * N_T), tm = (p.M + 16 * MT - 1) / (16 * MT);
     const dim3 grid((unsigned)(tn < kDirectColumns ? tn : kDirectColumns), (unsigned)(tm < kDirectRows ? tm : kDirectRows));
@@ -1015,11 +1016,12 @@ struct Staged {
 
 hipError_t launch_product(const Fp8bArgs& p, bool gated, int kind, uint16_t* y, const EpiArgs& e, hipStream_t stream) {
   switch (fp8b_shape(p.M, (int64_t)p.pieces * p.segs, gated ? 2 * p.N : p.N, gated)) {
-    case 0: return with_epilogue(Direct<1, 2, 8, 2>{p, y, e, stream}, gated, kind);
-    case 1: return with_epilogue(Direct<2, 2, 8, 2>{p, y, e, stream}, gated, kind);
-    case 2: return with_epilogue(Staged<2, 2, 2, 2, 4>{p, y, e, stream}, gated, kind);
-    case 3: return with_epilogue(Staged<2, 2, 4, 2, 3>{p, y, e, stream}, gated, kind);
-    case 4: return with_epilogue(Staged<2, 2, 4, 4, 2>{p, y, e, stream}, gated, kind);
+    case 0: return with_epilogue(Direct<1, 1, 16, 2>{p, y, e, stream}, gated, kind);
+    case 1: return with_epilogue(Direct<1, 2, 8, 2>{p, y, e, stream}, gated, kind);
+    case 2: return with_epilogue(Direct<2, 2, 8, 2>{p, y, e, stream}, gated, kind);
+    case 3: return with_epilogue(Staged<2, 2, 2, 2, 4>{p, y, e, stream}, gated, kind);
+    case 4: return with_epilogue(Staged<2, 2, 4, 2, 3>{p, y, e, stream}, gated, kind);
+    case 5: return with_epilogue(Staged<2, 4, 4, 4, 3>{p, y, e, stream}, gated, kind);
     default: return with_epilogue(Staged<2, 4, 4, 8, 2>{p, y, e, stream}, gated, kind);
   }
 }

@@ -12,7 +12,7 @@ SHIM = """
 #include "qpl_fp8b_shape.h"
 using namespace qpl;
 extern "C" int shapes() { return kFp8bShapeCount; }
-extern "C" int ungated() { return FP8B_UNGATED; }
+extern "C" int ungated(int v) { return !fp8b_gated_shape(v); }
 extern "C" int shape(int64_t M, int64_t K, int64_t N, int segs, int gated) {
   return segs == 1 && fp8b_token_fits(M, K) ? -1 : fp8b_shape(M, (K + 127) / 128 * segs, N, gated != 0);
 }
@@ -46,4 +46,4 @@ def pair(M, H, K):
 
 
 def every(gated=False):
-    return set(range(rule().shapes())) - ({rule().ungated()} if gated else set())
+    return {v for v in range(rule().shapes()) if not (gated and rule().ungated(v))}
