@@ -7,6 +7,7 @@ fallback: a missing library or a non-OK status raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -598,6 +599,13 @@ def qlinear_moe_int8(x, expert_ids, expert_weights, fc1, fc2, y=None, workspace=
     return y
 
 
+# qpl_heads, qpl_rope and qpl_fp8b_weight as bytes (the layouts of Heads, Rope and Fp8bWeight): packing them takes a tenth of the
+# time of building ctypes objects, which counts in calls that take a few microseconds.
+_PACK_HEADS = struct.Struct("@PPqqqqqPPqqP").pack
+_PACK_ROPE = struct.Struct("@PPqqqqqqif").pack
+_PACK_WEIGHT = struct.Struct("@PP").pack
+
+
 def _blocks(n):
     return (n + 127) // 128
 
@@ -674,10 +682,11 @@ def _gated_act(act):
 
 
 def _fp8b_weight(layer, N, K, dev, name):
-    """Fp8bWeight of a dict with weight uint8 [N,K] and weight_scale float32 [ceil(N/128), ceil(K/128)]."""
-    return Fp8bWeight(_addr(layer["weight"], torch.uint8, (N, K), dev, name + ".weight"),
-                      _addr(layer["weight_scale"], torch.float32, (_blocks(N), _blocks(K)), dev,
-                            name + ".weight_scale"))
+    """qpl_fp8b_weight, as bytes, of a dict with weight uint8 [N,K] and weight_scale float32 [ceil(N/128),
+    ceil(K/128)]."""
+    return _PACK_WEIGHT(_addr(layer["weight"], torch.uint8, (N, K), dev, name + ".weight"),
+                        _addr(layer["weight_scale"], torch.float32, (_blocks(N), _blocks(K)), dev,
+                              name + ".weight_scale"))
 
 
 def qlinear_gated_fp8b_workspace_bytes(M, K, H):
@@ -699,7 +708,7 @@ def qlinear_gated_fp8b(x, gate, up, act="silu", h=None, save=False, workspace=No
     g, u = save if save else (None, None)
     ws, wa, nbytes = _scratch(workspace, qlinear_gated_fp8b_workspace_bytes(M, K, H), x, dev, stream)
     _check("qlinear_gated_fp8b", load().qlinear_gated_fp8b(
-        _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, H, ctypes.byref(wg), ctypes.byref(wu), code,
+        _addr(x, torch.bfloat16, (M, K), dev, "x"), M, K, H, wg, wu, code,
         _addr(h, torch.bfloat16, (M, H), dev, "h"), _addr(g, torch.bfloat16, (M, H), dev, "g"),
         _addr(u, torch.bfloat16, (M, H), dev, "u"), wa, nbytes, _queue(stream, dev)))
     return (h, g, u) if save else h
@@ -726,7 +735,7 @@ def qlinear_gated_fp8b_backward(dh, g, u, gate_t, up_t, act="silu", dx=None, dg=
     ws, wa, nbytes = _scratch(workspace, qlinear_gated_fp8b_backward_workspace_bytes(M, K, H), dh, dev, stream)
     _check("qlinear_gated_fp8b_backward", load().qlinear_gated_fp8b_backward(
         _addr(dh, torch.bfloat16, (M, H), dev, "dh"), _addr(g, torch.bfloat16, (M, H), dev, "g"),
-        _addr(u, torch.bfloat16, (M, H), dev, "u"), M, K, H, ctypes.byref(wg), ctypes.byref(wu), code,
+        _addr(u, torch.bfloat16, (M, H), dev, "u"), M, K, H, wg, wu, code,
         _addr(dx, torch.bfloat16, (M, K), dev, "dx"), _addr(dg, torch.bfloat16, (M, H), dev, "dg"),
         _addr(du, torch.bfloat16, (M, H), dev, "du"), wa, nbytes, _queue(stream, dev)))
     return dx, dg, du
@@ -744,24 +753,30 @@ def qlinear_weight_grad(dy, x, dw=None, stream=None):
     return dw
 
 
-def _head_view(t, shape, dev, name):
+def _head_view(t, heads, tokens, dim, dev, name):
     """(address, head stride, token stride) of bf16 heads [heads, tokens, head_dim] whose channels are contiguous."""
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != dev or (shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name}: expected torch.bfloat16 {tuple(shape)} with contiguous channels on the current GPU "
-                         f"({dev}), got {t.dtype} {tuple(t.shape)} strides={t.stride()} device={t.device}")
+    hs, ts, cs = t.stride()
+    if t.dtype != torch.bfloat16 or t.shape != (heads, tokens, dim) or t.get_device() != dev or (cs != 1 and dim > 1):
+        raise ValueError(f"{name}: expected torch.bfloat16 {(heads, tokens, dim)} with contiguous channels on the current "
+                         f"GPU ({dev}), got {t.dtype} {tuple(t.shape)} strides={t.stride()} device={t.device}")
     # the stride of a single head or token is never used
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0
+    return t.data_ptr(), hs if heads > 1 else 0, ts if tokens > 1 else 0
 
 
 def _new_heads(like, stream):
     """New heads in the order of `like`'s (token-major heads stay token-major)."""
     heads, tokens, dim = like.shape
-    if tokens > 1 and heads > 1 and like.stride(0) < like.stride(1):
-        return _new((tokens, heads, dim), torch.bfloat16, like, stream).transpose(0, 1)
+    hs, ts, _ = like.stride()
+    if tokens > 1 and heads > 1 and hs < ts:
+        if stream is None:
+            return like.new_empty_strided((heads, tokens, dim), (dim, heads * dim, 1))
+        with torch.cuda.stream(stream):
+            return like.new_empty_strided((heads, tokens, dim), (dim, heads * dim, 1))
     return _new((heads, tokens, dim), torch.bfloat16, like, stream)
 
 
 def _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev):
+    """qpl_rope as bytes, or None for the norm alone."""
     if inv_freq is None:
         return None
     n = _dims(inv_freq, 1, "inv_freq")[0]
@@ -770,15 +785,13 @@ def _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev):
     axes = 1 if sections is None else len(sections)
     if sections is not None and not 1 <= axes <= 4:
         raise ValueError(f"sections: expected one to four numbers of pairs, got {axes}")
-    shape = (tokens, axes) if positions.dim() == 2 else (tokens,)
     if axes > 1 and positions.dim() != 2:
         raise ValueError(f"positions: expected [tokens, {axes}] for {axes} sections, got {tuple(positions.shape)}")
-    r = Rope(_addr(positions, torch.int32, shape, dev, "positions"), _addr(inv_freq, torch.float32, (n,), dev, "inv_freq"),
-             2 * n, axes)
-    for i, v in enumerate(sections or (n,)):
-        r.sections[i] = int(v)
-    r.interleaved, r.scale = int(bool(interleaved)), float(scale)
-    return r
+    shape = (tokens, axes) if positions.dim() == 2 else (tokens,)
+    parts = (n, 0, 0, 0) if sections is None else (tuple(int(v) for v in sections) + (0, 0, 0))[:4]
+    return _PACK_ROPE(_addr(positions, torch.int32, shape, dev, "positions"),
+                      _addr(inv_freq, torch.float32, (n,), dev, "inv_freq"), 2 * n, axes, *parts,
+                      1 if interleaved else 0, scale)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, norm=True, interleaved=False,
@@ -790,23 +803,22 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     (2 i, 2 i + 1), times scale.  positions int32 [tokens], or [tokens, len(sections)] with sections pairs for each
     axis; inv_freq float32 (rope_frequencies), or None for the norm alone.  q_out and k_out may be q and k."""
     dev = _current(q, 3, "q")
-    tokens, dim = q.shape[1], q.shape[2]
+    _, tokens, dim = q.shape
     r = _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev)
-    outs, sides = [], []
-    for t, w, o, name in ((q, q_weight, q_out, "q"), (k, k_weight, k_out, "k")):
-        if t is None:
-            outs.append(None)
-            sides.append(None)
-            continue
-        shape = (_dims(t, 3, name)[0], tokens, dim)
-        xa, xh, xt = _head_view(t, shape, dev, name)
-        o = _new_heads(t, stream) if o is None else o
-        ya, yh, yt = _head_view(o, shape, dev, name + "_out")
-        sides.append(Heads(xa, ya, shape[0], xh, xt, yh, yt, _addr(w, torch.bfloat16, (dim,), dev, name + "_weight")))
-        outs.append(o)
-    _check("qk_norm_rope", load().qk_norm_rope(_ref(sides[0]), _ref(sides[1]), tokens, dim, int(bool(norm)), float(eps),
-                                               _ref(r), _queue(stream, dev)))
-    return tuple(outs)
+
+    def side(t, w, o, name):
+        heads = _dims(t, 3, name)[0]
+        xa, xh, xt = _head_view(t, heads, tokens, dim, dev, name)
+        if o is None:
+            o = _new_heads(t, stream)
+        ya, yh, yt = _head_view(o, heads, tokens, dim, dev, name + "_out")
+        return o, _PACK_HEADS(xa, ya, heads, xh, xt, yh, yt, _addr(w, torch.bfloat16, (dim,), dev, name + "_weight"),
+                              0, 0, 0, 0)
+
+    q_out, qs = side(q, q_weight, q_out, "q")
+    k_out, ks = (None, None) if k is None else side(k, k_weight, k_out, "k")
+    _check("qk_norm_rope", load().qk_norm_rope(qs, ks, tokens, dim, 1 if norm else 0, eps, r, _queue(stream, dev)))
+    return q_out, k_out
 
 
 def qk_norm_rope_backward_workspace_bytes(tokens, head_dim):
@@ -819,31 +831,27 @@ def qk_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_weight=None, k_we
     """Gradients (of q, of k, of q_weight, of k_weight) from those of qk_norm_rope's outputs and its inputs; the
     weights' in float32 [head_dim], None where there is no weight.  dq_out and dk_out may be dq and dk (or q and k)."""
     dev = _current(q, 3, "q")
-    tokens, dim = q.shape[1], q.shape[2]
+    _, tokens, dim = q.shape
     r = _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev)
-    outs, grads, sides = [], [], []
-    for d, t, w, o, name in ((dq, q, q_weight, dq_out, "q"), (dk, k, k_weight, dk_out, "k")):
-        if t is None:
-            outs.append(None)
-            grads.append(None)
-            sides.append(None)
-            continue
-        shape = (_dims(t, 3, name)[0], tokens, dim)
-        xa, xh, xt = _head_view(t, shape, dev, name)
-        da, dh, dt = _head_view(d, shape, dev, "d" + name)
-        o = _new_heads(d, stream) if o is None else o
-        oa, oh, ot = _head_view(o, shape, dev, "d" + name + "_out")
+
+    def side(d, t, w, o, name):
+        heads = _dims(t, 3, name)[0]
+        xa, xh, xt = _head_view(t, heads, tokens, dim, dev, name)
+        da, dh, dt = _head_view(d, heads, tokens, dim, dev, "d" + name)
+        if o is None:
+            o = _new_heads(d, stream)
+        oa, oh, ot = _head_view(o, heads, tokens, dim, dev, "d" + name + "_out")
         gw = None if w is None else _new((dim,), torch.float32, t, stream)
-        sides.append(Heads(xa, da, shape[0], xh, xt, dh, dt, _addr(w, torch.bfloat16, (dim,), dev, name + "_weight"),
-                           oa, oh, ot, _addr(gw, torch.float32, (dim,), dev, "d" + name + "_weight")))
-        outs.append(o)
-        grads.append(gw)
-    need = qk_norm_rope_backward_workspace_bytes(tokens, dim) if any(g is not None for g in grads) else 0
+        return o, gw, _PACK_HEADS(xa, da, heads, xh, xt, dh, dt, _addr(w, torch.bfloat16, (dim,), dev, name + "_weight"),
+                                  oa, oh, ot, 0 if gw is None else gw.data_ptr())
+
+    dq_out, gq, qs = side(dq, q, q_weight, dq_out, "q")
+    dk_out, gk, ks = (None, None, None) if k is None else side(dk, k, k_weight, dk_out, "k")
+    need = 0 if gq is None and gk is None else qk_norm_rope_backward_workspace_bytes(tokens, dim)
     ws, wa, nbytes = _scratch(workspace, need, q, dev, stream)
-    _check("qk_norm_rope_backward", load().qk_norm_rope_backward(
-        _ref(sides[0]), _ref(sides[1]), tokens, dim, int(bool(norm)), float(eps), _ref(r), wa, nbytes,
-        _queue(stream, dev)))
-    return (*outs, *grads)
+    _check("qk_norm_rope_backward", load().qk_norm_rope_backward(qs, ks, tokens, dim, 1 if norm else 0, eps, r, wa,
+                                                                 nbytes, _queue(stream, dev)))
+    return dq_out, dk_out, gq, gk
 
 
 _ROPE_KINDS = {"linear": 1, "ntk": 2, "yarn": 3}

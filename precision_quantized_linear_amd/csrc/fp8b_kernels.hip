@@ -462,8 +462,8 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_fp8b_token(const uint16_t* __r
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         sum[g] = red[0][g][lane];
-#pragma unroll
-        for (int k = 1; k < W; ++k) sum[g] += red[k][g][lane];
+#pragma unroll 3
+        for (int k = 1; k < W; ++k) sum[g] += red[k][g][lane];  // a few at a time: next to the weight in flight
       }
       store_four<GATED, EPI>(p, Y, r16, M, n0 + 4 * q, sum[0], sum[1], e);
     }

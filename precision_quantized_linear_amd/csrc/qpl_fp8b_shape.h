@@ -13,7 +13,7 @@ inline bool fp8b_token_fits(int64_t M, int64_t K) { return M <= 16 && M * ((K + 
 // Which kernel multiplies otherwise.  A workgroup's time is about
 //   (pieces of 128 channels) * piece + tile   microseconds
 // with the constants below, and the 256 CUs take the tiles in rounds; the shape with the least time is taken.
-// The direct kernel's piece is its bytes at 35 KB/us, and several of its workgroups share a CU, so its rounds need
+// The direct kernel's piece is its bytes at 40 KB/us, and several of its workgroups share a CU, so its rounds need
 // not be whole.  Measured, us in a graph with the quantizer's launch (4 to 5 us):
 //   M    K    N      16x16 16x32 32x32 64x64 64x128 128x128 128x256 256x256
 //   17   4096 4096   15.1  12.9  13.8  17.4  20.8   24.5
@@ -30,7 +30,11 @@ inline bool fp8b_token_fits(int64_t M, int64_t K) { return M <= 16 && M * ((K + 
 //   515  2048 5632         69.2  50.3        19.4   23.2    19.6    26.3
 //   1024 4096 8192                           53.9   46.9    43.9    47.1
 //   4096 4096 21504                          472    392     368     343
-// Of 98 sizes, dense and gated, most of them random, the shape taken was within 9 % of the best for 97.  A 128 x 128
+// two segments (the gated backward, with its first launch), K of both:
+//   16   21504 4096  28.4  36.8  39.4  61.4  76.8
+//   130  5472 1040   22.4  18.6  15.7  23.0  27.4           37.9    53.4
+//   515  11264 2048  199   143   106   51.7  50.4           63.0    100
+// Of 108 such sizes, most of them random, the shape taken was within 9 % of the best for 107.  A 128 x 128
 // shape (the table's column) was the best for one of them, by 4 %, and is not built.
 // ---------------------------------------------------------------------------
 // rows and cols: outputs of a workgroup (a gated product makes cols / 2 of them from as many rows of each weight).
@@ -38,8 +42,8 @@ struct Fp8bShape {
   int rows, cols;
   double piece, tile;
 };
-constexpr Fp8bShape kFp8bShapes[] = {{16, 16, 0, 2.0},    {16, 32, 0, 1.0},     {32, 32, 0, 0.9},     {64, 64, 0.26, 0.8},
-                                     {64, 128, 0.4, 0.9}, {128, 256, 0.87, 5.4}, {256, 256, 1.67, 5.7}};
+constexpr Fp8bShape kFp8bShapes[] = {{16, 16, 0, 1.9},    {16, 32, 0, 1.7},    {32, 32, 0, 2.0},     {64, 64, 0.3, 1.9},
+                                     {64, 128, 0.41, 2.7}, {128, 256, 1.18, 3.4}, {256, 256, 2.05, 6.3}};
 constexpr int kFp8bShapeCount = 7;
 // A gated product has no 16 x 16 shape (its 16 x 32 is as fine) and no 64 x 64 shape, where a wavefront has too few
 // column tiles for two weights.
@@ -56,8 +60,8 @@ inline int fp8b_shape(int64_t M, int64_t pieces, int64_t N, bool gated) {
     const double tiles = (double)((M + s.rows - 1) / s.rows) * (double)((N + s.cols - 1) / s.cols) / 256;
     const double left = tiles - __builtin_floor(tiles);  // of the last round; staged tiles are cut in it
     const double last = left == 0 ? 0 : s.rows >= 256 && left <= 0.25 ? 0.6 : s.rows >= 128 && left <= 0.5 ? 0.8 : 1;
-    const double rounds = direct ? (tiles > 1 ? tiles : 1) : tiles - left + last;
-    const double piece = direct ? ((M < s.rows ? M : s.rows) + s.cols) * 128 / 35e3 : s.piece;
+    const double rounds = direct ? (tiles > 1 ? tiles + 0.2 : 1) : tiles - left + last;
+    const double piece = direct ? ((M < s.rows ? M : s.rows) + s.cols) * 128 / 40e3 : s.piece;
     const double t = rounds * (double)pieces * piece + (rounds > 1 ? rounds : 1) * s.tile;
     if (best < 0 || t < least) {
       best = v;

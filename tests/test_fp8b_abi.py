@@ -263,7 +263,8 @@ def test_binding_names_the_wrong_tensor():
 LINEAR = [(1, 16, 1), (1, 4096, 257), (2, 48, 16), (16, 1024, 33), (16, 1040, 40), (3, 2000, 20000), (15, 80, 33),
           (17, 144, 63), (20, 2064, 100), (31, 400, 65), (33, 64, 8), (64, 400, 65), (65, 272, 1000), (127, 1040, 129),
           (129, 128, 256), (255, 512, 300), (300, 192, 513), (513, 336, 264), (515, 1040, 2001), (1025, 1200, 1032),
-          (2100, 256, 2050), (2049, 528, 4103), (4500, 96, 5000), (2300, 400, 6000), (260, 20000, 40), (40, 8192, 24), (1500, 640, 6000), (1030, 272, 6000), (2050, 144, 6000)]
+          (2100, 256, 2050), (2049, 528, 4103), (4500, 96, 5000), (2300, 400, 6000), (260, 20000, 40), (40, 8192, 24), (1500, 640, 6000), (1030, 272, 6000), (2050, 144, 6000), (300, 400, 1500),
+          (64, 1040, 4112)]
 GATED = [(1, 64, 16), (4, 2048, 272), (16, 1024, 64), (17, 144, 48), (33, 272, 400), (40, 4096, 16), (100, 512, 96),
          (130, 1040, 1008), (257, 384, 656), (700, 256, 1392), (1030, 400, 2064), (515, 272, 6000), (2050, 272, 3088)]
 PAIR = [(1, 64, 16), (5, 400, 48), (17, 144, 272), (64, 1008, 528), (130, 2736, 1040), (300, 272, 2064),
