@@ -395,8 +395,9 @@ qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, 
 /*
  * Block-scaled fp8 (FP8B): E4M3 codes with an fp32 scale for every 128 channels of a row of x and for every
  * 128 x 128 block of a weight, the form that block-scaled checkpoints carry.
- *   rule   a = max |v| over the block, s = a / 448 (fp32), codes E4M3(v / s) with a correctly rounded division;
- *          an all-zero block has s = 0 and signed-zero codes.  A last block holds what is left of K (or N).
+ *   rule   a = max |v| over the block, s = a * fp32(1 / 448) in fp32 (as torch evaluates a / 448 on the GPU; the
+ *          row-wise rule above divides), codes E4M3(v / s) with a correctly rounded division; an all-zero block has
+ *          s = 0 and signed-zero codes.  A last block holds what is left of K (or N).
  * quant_act_fp8b:    x bf16 [M,K] -> x_q uint8 [M,K], x_scale float [M, ceil(K/128)].
  * quant_weight_fp8b: w bf16 [N,K] -> w_q uint8 [N,K], w_scale float [ceil(N/128), ceil(K/128)].
  * transpose_fp8b:    a quantized weight turned over: weight_t [K,N], weight_t_scale [ceil(K/128), ceil(N/128)]
@@ -421,7 +422,8 @@ qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, 
  *     dx = bf16_rne(Q(dg) Wg + Q(du) Wu),  Q the rule above over blocks of 128 of H (the rounding of x to its codes
  *     passes gradients through unchanged)
  *   gate_t, up_t  the weights turned over (transpose_fp8b): [K,H], scales [ceil(K/128), ceil(H/128)]
- *   dx            bf16 [M,K] out;  dg, du  bf16 [M,H] out (for qlinear_weight_grad), or both NULL
+ *   dx            bf16 [M,K] out;  dg, du  bf16 [M,H] out (for qlinear_weight_grad), or both NULL; either may be dh, g
+ *                 or u itself
  *   ws            at least qlinear_gated_fp8b_backward_workspace_bytes(M, K, H) bytes
  * qlinear_weight_grad: dw[n,k] = sum_m dy[m,n] x[m,k] of bf16 dy [M,N] and x [M,K], fp32 [N,K], summed in fp32: the
  *   gradient of any linear's weight.  N % 16 == 0 and K % 16 == 0, both at most 2^23.

@@ -4,8 +4,8 @@
 The format and rules are this library's (each listed, with its reason, in the design notes):
 
 * a block is 128 channels of a row of x, or 128 x 128 of a weight; what is left at the end is a block too;
-* s = max |v| / 448 (fp32), codes E4M3(v / s) with a correctly rounded fp32 division; a zero block has s = 0 and
-  signed-zero codes;
+* s = max |v| times fp32(1 / 448), in fp32 (how torch divides a tensor by 448 on the GPU), codes E4M3(v / s) with a
+  correctly rounded fp32 division; a zero block has s = 0 and signed-zero codes;
 * y = bf16(sum of the products of the codes' values), defined as dequantize-then-multiply in float64;
 * gated: h = act(g) u of two such linears; its backward takes g and u in bf16, rounds dg and du to bf16, and
   multiplies their codes by the weights.
@@ -35,7 +35,7 @@ def quant_act(x_bits):
     x = bf16_bits_to_f32(x_bits)
     M, K = x.shape
     s = np.stack([np.max(np.abs(x[:, k:k + B]), axis=1) for k in range(0, K, B)], 1)
-    s = (s / F32(448.0)).astype(F32)
+    s = (s * (F32(1.0) / F32(448.0))).astype(F32)
     return _codes(x, np.repeat(s, B, axis=1)[:, :K]), s
 
 
@@ -44,7 +44,7 @@ def quant_weight(w_bits):
     w = bf16_bits_to_f32(w_bits)
     N, K = w.shape
     s = np.array([[np.max(np.abs(w[n:n + B, k:k + B])) for k in range(0, K, B)] for n in range(0, N, B)], F32)
-    s = (s / F32(448.0)).astype(F32)
+    s = (s * (F32(1.0) / F32(448.0))).astype(F32)
     return _codes(w, spread(s, N, K)), s
 
 

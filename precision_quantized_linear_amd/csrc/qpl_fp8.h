@@ -1,4 +1,4 @@
-// E4M3 codes of bf16 values under a scale s = amax / 448 (fp32): what the fp8 quantizers, by row and by
+// E4M3 codes of bf16 values under a scale s, amax / 448 up to its rounding to fp32: what the fp8 quantizers, by row and by
 // block of 128, share.
 #pragma once
 
@@ -19,14 +19,22 @@ struct RowDiv {
   bool zero, tiny;
 };
 
-__device__ __forceinline__ RowDiv row_div(float amax) {
+__device__ __forceinline__ RowDiv scale_div(float s) {
   RowDiv d;
-  d.s = amax / 448.0f;
+  d.s = s;
   d.zero = !(d.s > 0.0f);
   d.tiny = !div_rn_ok(d.s);
   d.r = 1.0f / d.s;
   return d;
 }
+
+// By row: the correctly rounded quotient.
+__device__ __forceinline__ RowDiv row_div(float amax) { return scale_div(amax / 448.0f); }
+
+// By block: the product with fp32(1 / 448), 0.375 * 2^-23 of itself above it before its rounding.  torch divides a
+// tensor on the GPU by a number like that, so codes made here are those that a program in torch makes there: a value
+// of bf16 over s often lies on the border between two codes, and one step of s decides for either.
+__device__ __forceinline__ RowDiv block_div(float amax) { return scale_div(amax * (1.0f / 448.0f)); }
 
 // |x| <= amax, so |x / s| stays at 448 up to rounding: no overflow, and no clamp
 // needed before the converter.

@@ -62,6 +62,16 @@ def test_quantizer_rows(M):
     assert np.array_equal(host(q), wq) and np.array_equal(host(s), ws)
 
 
+def test_quantizer_gives_the_codes_of_torch_on_the_gpu():
+    # the rule written down in torch, its division by 448 on the GPU: many quotients lie on a border between two codes
+    x = to_dev_bf16(activation(np.random.default_rng(11), 200, 2048))
+    q, s = qpl.quant_act_fp8b(x)
+    b = x.float().reshape(200, 16, 128)
+    want_s = b.abs().amax(2, keepdim=True) / 448.0
+    want = (b.double() / want_s.double()).float().to(torch.float8_e4m3fn)
+    assert torch.equal(s, want_s[..., 0]) and torch.equal(q.reshape(200, 16, 128), want.view(torch.uint8))
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (130, 272), (10, 2048), (1000, 400)])
 def test_weight_quantizer(N, K):
     w = adversarial_rows(K, seed=N)
@@ -255,7 +265,21 @@ def test_gated_backward_extremes(act):
     assert np.isfinite(dx).all()
 
 
-def test_gated_backward_without_projections_gradients(lib=None):
+@pytest.mark.parametrize("M", [3, 300])
+def test_gated_backward_in_place(M):
+    rng = np.random.default_rng(M)
+    H, K = 2064, 48
+    dh, g, u = (to_dev_bf16(activation(rng, M, H)) for _ in range(3))
+    w = [layer(weight(rng, K, H)) for _ in range(2)]
+    want = qpl.qlinear_gated_fp8b_backward(dh, g, u, *w)
+    for dg, du in (("g", "u"), ("dh", "g"), ("u", "dh")):
+        t = dict(dh=dh.clone(), g=g.clone(), u=u.clone())
+        got = qpl.qlinear_gated_fp8b_backward(t["dh"], t["g"], t["u"], *w, dg=t[dg], du=t[du])
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), (dg, du)
+
+
+def test_gated_backward_without_projections_gradients():
     import ctypes
     rng = np.random.default_rng(0)
     M, H, K = 40, 144, 48

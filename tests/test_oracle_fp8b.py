@@ -6,7 +6,7 @@ import pytest
 
 from helpers import adversarial_rows
 from oracle import fp8b
-from oracle.formats import bf16_bits_to_f32, e4m3_decode, f32_to_bf16_bits
+from oracle.formats import bf16_bits_to_f32, e4m3_decode, e4m3_encode, f32_to_bf16_bits
 from oracle.quant import quant_fp8_row
 
 
@@ -15,13 +15,37 @@ def bits(a):
 
 
 @pytest.mark.parametrize("K", [16, 128, 144, 400])
-def test_row_blocks_are_rows_of_the_row_scheme(K):
-    # each block by itself is a row of the fp8 row scheme, which has pins of its own
+def test_row_blocks_against_the_row_scheme(K):
+    # each block by itself is a row of the fp8 row scheme, which has pins of its own, but for how the scale is rounded:
+    # one step up at most, and codes move where the quotient lies next to a border between two
     x = adversarial_rows(K, seed=K)
     q, s = fp8b.quant_act(x)
     for b in range(0, K, 128):
         wq, ws = quant_fp8_row(x[:, b:b + 128])
-        assert np.array_equal(q[:, b:b + 128], wq) and np.array_equal(s[:, b // 128], ws)
+        up = s[:, b // 128].view(np.int32).astype(np.int64) - ws.view(np.int32)
+        assert ((up >= 0) & (up <= 1)).all()
+        same, moved = q[:, b:b + 128][up == 0], np.abs(q[:, b:b + 128].astype(int) - wq)[up == 1]
+        assert np.array_equal(same, wq[up == 0]) and (moved <= 1).all()
+
+
+def test_scale_against_rationals():
+    # every significand of bf16: the product with the fp32 number next to 1 / 448, rounded to nearest
+    c = Fraction(float(np.float32(1) / np.float32(448)))
+    assert abs(c - Fraction(1, 448)) * 448 < Fraction(1, 2 ** 24)
+    x = np.zeros((128, 128), np.uint16)
+    x[:, 3] = 0x3F80 + np.arange(128)
+    s = fp8b.quant_act(x)[1][:, 0]
+    for m, got in zip(range(128, 256), s):
+        want = Fraction(m, 128) * c
+        step = Fraction(float(np.spacing(got)))
+        assert abs(Fraction(float(got)) - want) * 2 <= step
+
+
+@pytest.mark.parametrize("p", [-120, -8, 0, 30, 119])
+def test_scale_of_a_largest_code_is_exact(p):
+    x = np.zeros((1, 128), np.uint16)
+    x[0, 0] = bits(448.0 * 2.0 ** p)
+    assert fp8b.quant_act(x)[1][0, 0] == np.float32(2.0 ** p)
 
 
 def test_weight_blocks_share_one_scale():
@@ -32,8 +56,10 @@ def test_weight_blocks_share_one_scale():
     for i in range(3):
         for j in range(3):
             blk = w[128 * i:128 * i + 128, 128 * j:128 * j + 128]
-            wq, ws = quant_fp8_row(blk.reshape(1, -1))
-            assert np.array_equal(q[128 * i:128 * i + 128, 128 * j:128 * j + 128].ravel(), wq[0]) and s[i, j] == ws[0]
+            top = np.abs(bf16_bits_to_f32(blk)).max()
+            assert s[i, j] == top * (np.float32(1) / np.float32(448))
+            want = e4m3_encode((bf16_bits_to_f32(blk) / s[i, j]).astype(np.float32))
+            assert np.array_equal(q[128 * i:128 * i + 128, 128 * j:128 * j + 128], want)
 
 
 def test_zero_block_and_largest_code():
@@ -42,7 +68,7 @@ def test_zero_block_and_largest_code():
     x[1, 5] = bits(-3.0)
     q, s = fp8b.quant_act(x)
     assert s[0].tolist() == [0, 0] and set(q[0, :128].tolist()) == {0, 0x80} and not q[0, 128:].any()
-    assert s[1, 0] == np.float32(3.0 / 448) and q[1, 5] == 0xFE and s[1, 1] == 0
+    assert s[1, 0] == np.float32(3) * (np.float32(1) / np.float32(448)) and q[1, 5] == 0xFE and s[1, 1] == 0
 
 
 def test_linear_against_rationals():
