@@ -384,30 +384,30 @@ int64_t even_blocks(int64_t n, int64_t most) {
   return (n + each - 1) / each;
 }
 
-// Threads that the heads need together: below this many, every head gets a group of its own, because the chip is not
-// full otherwise (16 tokens of 40 heads: one pass of two workgroups per token).
-constexpr int64_t kFewThreads = 256 * 1024;
+// Workgroups that fill the chip: below them heads are spread further.  32 and 8 heads of 128, head-major, us at 256, 768
+// and 1024: forward of 1024 tokens 8.3, 6.7 and 6.6, of 1536 9.4, 8.8 and 9.2, of 2048 13.9, 11.3 and 11.3 (never
+// spread: 12.2, 12.8 and 13.8); backward, where each workgroup ends with its sums, of 512 tokens 9.1, 10.2 and 10.2, of
+// 1024 11.2, 16.8 and 16.8, of 2048 17.9, 23.4 and 23.5 (never spread: 12.0, 13.8 and 18.2).  Single tokens of 40
+// heads take 3.4 us spread, 10.3 not.
+constexpr int64_t kFill = 768, kFillBackward = 256;
 
-// Groups that share a token, a power of two: with few tokens one for each head; else so many that they walk four heads
-// or more (the next head's loads run under the work on this one) and the fewest stand idle at the end.  Head-major
-// tensors are contiguous along the tokens, so there neighbouring groups take tokens, at least eight of them.
-void place_groups(RopeKernelArgs& p, int heads, int lanes, bool few) {
+// Groups that share a token, a power of two: so many that they walk four heads or more (the next head's loads run
+// under the work on this one) and the fewest stand idle at the end.  Head-major tensors are contiguous along the
+// tokens, so there neighbouring groups take tokens, at least eight of them.  With few tokens more groups share one,
+// until the workgroups fill the chip or every head has a group.
+void place_groups(RopeKernelArgs& p, int heads, int lanes, int64_t fill) {
   const int groups = 256 / lanes;
-  int best = 1;
-  if (few) {
-    while (best < groups && best < heads) best *= 2;
-  } else {
-    int least = heads;
-    for (int s = 1; s <= groups && (s == 1 || 4 * s <= heads); s *= 2) {
-      const int padded = (heads + s - 1) / s * s;
-      if (padded <= least) {
-        least = padded;
-        best = s;
-      }
+  int best = 1, least = heads;
+  for (int s = 1; s <= groups && (s == 1 || 4 * s <= heads); s *= 2) {
+    const int padded = (heads + s - 1) / s * s;
+    if (padded <= least) {
+      least = padded;
+      best = s;
     }
   }
   p.by_token = p.side[0].xt < p.side[0].xh;
-  while (!few && p.by_token && best > 1 && groups / best < 8) best /= 2;
+  while (p.by_token && best > 1 && groups / best < 8) best /= 2;
+  while (best < groups && best < heads && p.tokens * best < fill * groups) best *= 2;
   p.lg_slots = log2_of(best);
   p.lg_per = log2_of(groups / best);
 }
@@ -433,10 +433,11 @@ hipError_t launch_qk_norm_rope(const RopeSide (&side)[2], int64_t tokens, int he
                                hipStream_t stream) {
   RopeKernelArgs p = kernel_args(side, tokens, head_dim, r);
   const int lanes = lanes_of(head_dim);
-  const bool few = tokens * lanes * p.heads < kFewThreads;
-  place_groups(p, p.heads, lanes, few);
+  place_groups(p, p.heads, lanes, kFill);
+  // where that does not fill the chip, a token's heads go to several workgroups
   const int64_t per = int64_t(1) << p.lg_per, slots = int64_t(1) << p.lg_slots;
-  const dim3 grid((unsigned)((tokens + per - 1) / per), (unsigned)(few ? (p.heads + slots - 1) / slots : 1));
+  const int64_t n = (tokens + per - 1) / per, turns = (p.heads + slots - 1) / slots, parts = (kFill + n - 1) / n;
+  const dim3 grid((unsigned)n, (unsigned)(parts < turns ? parts : turns));
   const size_t lds = angle_bytes(p);
   return by_lanes(lanes, [&](auto lp) {
     if (r.norm) {
@@ -457,7 +458,7 @@ hipError_t launch_qk_norm_rope_backward(const RopeSide (&side)[2], int64_t token
                                         float* ws, hipStream_t stream) {
   RopeKernelArgs p = kernel_args(side, tokens, head_dim, r);
   const int lanes = lanes_of(head_dim);
-  place_groups(p, p.heads0, lanes, tokens * lanes * p.heads < kFewThreads);
+  place_groups(p, p.heads0, lanes, kFillBackward);
   const bool sums = side[0].dweight || side[1].dweight;
   p.partial = sums ? ws : nullptr;
   // the sides' shares of the workgroups are as their heads; one of a side takes at least one token

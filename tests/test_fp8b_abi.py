@@ -45,7 +45,7 @@ def test_workspace_sizes():
     assert b(33, 48, 40) == b(33, 40, 48) == b(0, 48, 48) == 0
     assert b(1, 16, (1 << 21) - 128) > 0 and b(1, 16, (1 << 21) - 112) == 0
     q = qpl.qk_norm_rope_backward_workspace_bytes
-    assert q(5, 128) == 5 * 8 * 128 and q(10 ** 6, 64) == 1024 * 8 * 64
+    assert q(5, 128) == 5 * 8 * 128 and q(10 ** 6, 64) == 2048 * 8 * 64
     assert q(0, 64) == q(5, 24) == q(5, 528) == 0
 
 

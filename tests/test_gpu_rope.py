@@ -75,7 +75,8 @@ CASES = [dict(heads=1, kv=1, T=1, D=16, R=16), dict(heads=3, kv=1, T=5, D=32, R=
          dict(heads=8, kv=2, T=33, D=64, R=64), dict(heads=5, kv=5, T=19, D=80, R=16), dict(heads=12, kv=4, T=70, D=96, R=64),
          dict(heads=32, kv=8, T=1, D=128, R=128), dict(heads=32, kv=8, T=300, D=128, R=128), dict(heads=20, kv=20, T=77, D=128, R=32),
          dict(heads=6, kv=3, T=41, D=192, R=192), dict(heads=4, kv=1, T=130, D=256, R=64), dict(heads=3, kv=2, T=9, D=512, R=512),
-         dict(heads=2, kv=2, T=3000, D=64, R=48), dict(heads=1, kv=70, T=40, D=16, R=16), dict(heads=32, kv=8, T=1500, D=128, R=128)]
+         dict(heads=2, kv=2, T=3000, D=64, R=48), dict(heads=1, kv=70, T=40, D=16, R=16), dict(heads=5, kv=1, T=9001, D=32, R=32),
+         dict(heads=32, kv=8, T=1500, D=128, R=128)]
 
 
 @pytest.mark.parametrize("major", ["token", "head"])
