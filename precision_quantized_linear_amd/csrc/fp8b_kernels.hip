@@ -18,7 +18,7 @@ constexpr int EPI_SILU = 4;  // gated: SiLU of the gate (else EPI_GELU)
 // ---------------------------------------------------------------------------
 // Row quantizer.  16 lanes hold a block, 8 channels each; a wavefront takes one row's 2048 channels, all its
 // loads in flight together.  Scales [M, blocks], or (SLAB) [blocks, M], where a piece of a product finds those
-// of consecutive rows in one run.
+// of consecutive rows in one run.  HBM: 4096 x 4096 in 10.7 us, 4096 x 10752 in 26.8 (4.9 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int QV = 4;  // vectors of 8 channels per lane
 
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void k_quant_fp8b(const uint16_t* __restrict__
   }
 }
 
-// Weight quantizer: a workgroup per 128 x 128 block.
+// Weight quantizer: a workgroup per 128 x 128 block.  HBM: 10752 x 4096 in 23.6 us (5.6 TB/s, part of it from caches).
 __global__ __launch_bounds__(256) void k_quant_weight_fp8b(const uint16_t* __restrict__ w, int64_t N, int64_t K,
                                                            uint8_t* __restrict__ wq, float* __restrict__ ws) {
   __shared__ float part[4];
@@ -86,7 +86,8 @@ __global__ __launch_bounds__(256) void k_quant_weight_fp8b(const uint16_t* __res
 }
 
 // Transposed codes [K, N] and scales [K / 128, N / 128] of a weight [N, K]: a workgroup per 128 x 128 block, its
-// bytes turned over in LDS.  A thread reads 16 channels of four rows and writes 16 rows of four channels.
+// bytes turned over in LDS.  A thread reads 16 channels of four rows and writes 16 rows of four channels.  HBM:
+// 10752 x 4096 in 18.3 us (4.8 TB/s).
 __global__ __launch_bounds__(256) void k_transpose_fp8b(const uint8_t* __restrict__ w, const float* __restrict__ ws,
                                                         int64_t N, int64_t K, uint8_t* __restrict__ wt,
                                                         float* __restrict__ wst) {
@@ -128,6 +129,7 @@ __global__ __launch_bounds__(256) void k_transpose_fp8b(const uint8_t* __restric
 // weights' gradients), and the codes of both, side by side in a row: dg's blocks, then du's, as one product
 // multiplies them by the two transposed weights.  One pass: 6 bytes read and 2 to 6 written per element.
 // The products run in 8 bits like the forward's; the scheme's rule keeps 4 significant bits of each gradient.
+// HBM and the vector unit alike: 4096 x 10752 with dg and du kept in 85 us (528 MB, 6.2 TB/s, part of it from caches).
 // ---------------------------------------------------------------------------
 constexpr float GELU_LINEAR = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float GELU_CUBE = 0.134145f;              // 3 * 0.044715
@@ -287,6 +289,8 @@ __device__ __forceinline__ void store_four(const Fp8bArgs& p, uint16_t* __restri
 // operands (V_MFMA_SCALE_F32_16X16X128_F8F6F4, 32 bytes per lane) straight from memory, and their sums meet in
 // LDS, in the order of the wavefronts.  Operands are swapped (the MFMA computes y^T): a lane holds four
 // consecutive columns of one row.  Lane l has bytes 16 (l / 16) and 64 + 16 (l / 16) of the piece of row l % 16.
+// Bound by the latency of its loads, about 40 KB/us for a workgroup: 130 x 5472 x 1040 in two segments 10.0 to 11.2 us
+// (32 x 32); 17 x 4096 x 4096 12.9 us with the quantizer's launch (16 x 32).
 // ---------------------------------------------------------------------------
 template <int MT, int NT, int W, int U, bool GATED, int EPI>
 __global__ __launch_bounds__(64 * W) void k_fp8b_direct(Fp8bArgs p, uint16_t* __restrict__ Y, EpiArgs e) {
@@ -376,7 +380,8 @@ __global__ __launch_bounds__(64 * W) void k_fp8b_direct(Fp8bArgs p, uint16_t* __
 // ---------------------------------------------------------------------------
 // A few rows (single tokens) in one launch: as the direct kernel, but every workgroup quantizes the M <= 16 rows
 // itself, into LDS, while its first weight bytes are on their way.  A row is parts of 512 channels (four blocks);
-// wavefront w takes the parts w, w + 16, ... of all rows.
+// wavefront w takes the parts w, w + 16, ... of all rows.  1 x 4096 x 4096 in 4.7 us (3.6 TB/s: latency, 64 KB of
+// weight per CU), gated 4 x 4096 x 10752 in 18.5 us (4.8 TB/s: HBM).
 // ---------------------------------------------------------------------------
 constexpr int TOKEN_W = 16, TOKEN_SLOTS = FP8B_TOKEN_PARTS / TOKEN_W;
 constexpr int TOKEN_BYTES = FP8B_TOKEN_PARTS * 512 + 16 * 16;  // rows 16 bytes further apart than they are long
@@ -488,9 +493,15 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_fp8b_token(const uint16_t* __r
 // last row tile, when all of its operands are in registers: every wavefront waits for its own loads of the next
 // piece, then all meet; the next piece is then in LDS and this piece's stage is free.  Behind it the loads of piece
 // P + S are issued between MFMAs, into the first half of the next piece's, and the next piece's first operands are
-// read, each column tile's as soon as the last row tile is done with the register.  A wavefront's vector memory operations retire in issue order, so the sync's wait names how many later
-// ones may be in flight: the loads of the pieces behind the next and the output stores of an epilogue issued
-// after its loads.  A smaller number than that only waits longer.
+// read, each column tile's as soon as the last row tile is done with the register.  A wavefront's vector memory
+// operations retire in issue order, so the sync's wait names how many later ones may be in flight: the loads of the
+// pieces behind the next and the output stores of an epilogue issued after its loads.  A smaller number than that only
+// waits longer.
+//
+// Bound by power and the matrix unit together (1.9 to 2.1 GHz under load): 4096 x 4096 x 12288 to q, k, v 210 us of 221
+// with the quantizer's (2.0 PFLOP/s), gated 4096 x 4096 x 2 * 10752 with both projections kept 358 of 368 (2.0
+// PFLOP/s), two segments 4096 x 21504 x 4096 303 us (2.4 PFLOP/s: few tile ends).  The same on 32 x 32 x 64 tiles, two
+// of them and sixteen fmas for a block, with the sync at a piece's end took 246, 425 and 370 us.
 // ---------------------------------------------------------------------------
 struct Fp8bStagedArgs {
   Fp8bArgs g;

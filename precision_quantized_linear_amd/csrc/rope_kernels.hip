@@ -11,7 +11,8 @@
 // such a group walks heads of one token.  The vectors are chosen so that every pair lies inside a lane: j and j +
 // rotary / 16 where pairs are half a rotary part apart, any two where they are neighbours.  A workgroup makes its
 // tokens' cosines and sines once, in LDS, for all heads: made by each group for itself, 8192 tokens of 40 heads of 128
-// channels took 88 us.
+// channels took 88 us.  They take 28.6 us now (168 MB, 5.9 TB/s, part of it from caches; 36 us with inputs from HBM, 4.6
+// TB/s), their backward 46 us (252 MB; 58 us with inputs from HBM, 4.3 TB/s, of which 4 are the sums' launch).
 #include <type_traits>
 
 #include "qpl_device.h"
