@@ -406,7 +406,8 @@ qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, 
  * qlinear_fp8b:      y[m,n] = bf16_rne(sum_b x_scale[m,b] weight_scale[n/128,b] sum_{k in b} q_x q_w), with q_x and
  *                    x_scale from quant_act_fp8b(x).  A block's sum comes from the FP8 matrix instructions (which
  *                    cut each product below 2^-13 of the largest of its group of eight) and is folded into fp32
- *                    accumulators.  The product of two scales must not overflow fp32.
+ *                    accumulators.  The product of two scales must not overflow fp32; below 2^-126 it
+ *                    loses bits.
  * qlinear_fp8b_ex:   the same with an epilogue (see qlinear_fp8r_ex).
  *   ws   at least qlinear_workspace_bytes(QPL_FP8B, M, K, N, 0) bytes, which is 0 for a few rows (they are quantized
  *        inside the product's kernel; ws may then be NULL).
