@@ -63,12 +63,17 @@ __device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
   return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
 }
 
-// cos and sin, times the scale, of the angles of `per` tokens from t0 on: cs [per, 8 rot pairs].
+// cos and sin, times the scale, of the angles of `per` tokens from t0 on: cs [per, 8 rot pairs].  Zeros for tokens past
+// the last: the groups without a token read them too, and the weights' gradients add up their products with zeros,
+// which are NaNs where LDS is left as the kernel before left it.
 __device__ __forceinline__ void make_angles(const RopeKernelArgs& p, int64_t t0, float2* cs) {
   const int pairs = 8 * p.rot, n = pairs << p.lg_per;
   for (int k = threadIdx.x; k < n; k += 256) {
     const int tt = k / pairs, i = k - tt * pairs;
-    if (t0 + tt >= p.tokens) break;
+    if (t0 + tt >= p.tokens) {
+      cs[k] = float2{0.0f, 0.0f};
+      continue;
+    }
     const int axis = (i >= p.bound[0]) + (i >= p.bound[1]) + (i >= p.bound[2]);
     const double turns = (double)p.positions[(t0 + tt) * p.axes + axis] * ((double)p.inv_freq[i] * 0.15915494309189535);
     float s, c;
