@@ -735,16 +735,23 @@ k_fp8b_staged(Fp8bStagedArgs) {
       ++s_i;
     }
   };
-  auto issue = [&](int d, int px, int pw) {  // px, pw: pitches of x and W
+  // px, pw: pitches of x and W.  What a load is ahead of the operand's start (its rows, and K) moves the descriptor's
+  // start, whose size shrinks by as much: rows past the operand's last, and everything where there is no tile, are past
+  // its end.  The same in the lanes' offsets takes a register, which the 256 x 256 shape does not have in its loop.
+  auto rest = [](const uint8_t* at, int bytes, int ahead) {
+    return make_desc(at + ahead, bytes > ahead ? bytes - ahead : 0);
+  };
+  auto issue = [&](int d, int px, int pw) {
     const uint32_t st = lbase + l_stage * STAGE;
     if (d < XL) {
-      dma16(st + XB + (XR / W * wv + 8 * d) * PR_ROW, d & 1 ? vx ^ 64 : vx, make_desc(xp, x_bytes), kx + 8 * d * px);
+      dma16(st + XB + (XR / W * wv + 8 * d) * PR_ROW, d & 1 ? vx ^ 64 : vx, rest(xp, x_bytes, kx + 8 * d * px));
     } else if (d < XL + WL) {
       const int n = d - XL;
-      dma16(st + WB + (WR / W * wv + 8 * n) * PR_ROW, n & 1 ? vw + (lane & 4 ? -64 : 64) : vw, make_desc(wp, w_bytes), kw + 8 * n * pw);
+      dma16(st + WB + (WR / W * wv + 8 * n) * PR_ROW, n & 1 ? vw + (lane & 4 ? -64 : 64) : vw,
+            rest(wp, w_bytes, kw + 8 * n * pw));
     } else {
       dma4(scales ? st + (job == 0 ? 256 * wv : 4 * XR + 256 * (job - 1)) : lbase + S * STAGE, vs,
-           make_desc(sp, sp_bytes), 0);
+           make_desc(sp, sp_bytes));
     }
   };
 

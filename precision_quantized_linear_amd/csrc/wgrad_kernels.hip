@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void k_weight_grad(GradArgs p) {
     return make_desc((isx ? p.x : p.dy) + (rows > 0 ? m * width : 0), rows * width * 2);
   };
   auto issue = [&](int stage, int d, const u32x4& desc) {
-    dma16(lbase + stage * STAGE + (d < L ? 0 : OP) + 1024 * (L * wv + (d < L ? d : d - L)), vo[d], desc, 0);
+    dma16(lbase + stage * STAGE + (d < L ? 0 : OP) + 1024 * (L * wv + (d < L ? d : d - L)), vo[d], desc);
   };
   // Fragment of 32 channels, tokens 16 u .. 16 u + 15 (lane l: channel l % 32, tokens 8 (l / 32) ..), in two reads.
   // The swizzle moves whole fragments, so each has an address of its own, and the tokens are offsets from it.
