@@ -399,9 +399,9 @@ qpl_status qlinear_moe_int8(const uint16_t* x, int64_t T, int64_t K, int64_t H, 
  *          row-wise rule above divides), codes E4M3(v / s) with a correctly rounded division; an all-zero block has
  *          s = 0 and signed-zero codes.  A last block holds what is left of K (or N).
  * quant_act_fp8b:    x bf16 [M,K] -> x_q uint8 [M,K], x_scale float [M, ceil(K/128)].
- * quant_weight_fp8b: w bf16 [N,K] -> w_q uint8 [N,K], w_scale float [ceil(N/128), ceil(K/128)].
+ * quant_weight_fp8b: w bf16 [N,K] -> w_q uint8 [N,K], w_scale float [ceil(N/128), ceil(K/128)]; K <= 2^31 - 128.
  * transpose_fp8b:    a quantized weight turned over: weight_t [K,N], weight_t_scale [ceil(K/128), ceil(N/128)]
- *                    (N % 16 == 0), the same values.  With it the gradient of a linear's input is a linear:
+ *                    (N % 16 == 0, K <= 2^31 - 128), the same values.  With it the gradient of a linear's input is a linear:
  *                    dx = qlinear_fp8b(dy, weight_t).
  * qlinear_fp8b:      y[m,n] = bf16_rne(sum_b x_scale[m,b] weight_scale[n/128,b] sum_{k in b} q_x q_w), with q_x and
  *                    x_scale from quant_act_fp8b(x).  A block's sum comes from the FP8 matrix instructions (which

@@ -18,7 +18,8 @@ constexpr int EPI_SILU = 4;  // gated: SiLU of the gate (else EPI_GELU)
 // ---------------------------------------------------------------------------
 // Row quantizer.  16 lanes hold a block, 8 channels each; a wavefront takes one row's 2048 channels, all its
 // loads in flight together.  Scales [M, blocks], or (SLAB) [blocks, M], where a piece of a product finds those
-// of consecutive rows in one run.  HBM: 4096 x 4096 in 10.7 us, 4096 x 10752 in 26.8 (4.9 TB/s).
+// of consecutive rows in one run.  Takes `rows` of the M rows (row_slices).  HBM: 4096 x 4096 in 10.7 us, 4096 x
+// 10752 in 26.8 (4.9 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int QV = 4;  // vectors of 8 channels per lane
 
@@ -31,12 +32,12 @@ __device__ __forceinline__ uint32_t block_absmax(uint32_t m) {
 }
 
 template <bool SLAB>
-__global__ __launch_bounds__(256) void k_quant_fp8b(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+__global__ __launch_bounds__(256) void k_quant_fp8b(const uint16_t* __restrict__ x, int64_t rows, int64_t M, int64_t K,
                                                     int64_t pitch, uint32_t chunks, uint8_t* __restrict__ xq,
                                                     float* __restrict__ xs) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)(blockIdx.x / chunks) * 4 + (threadIdx.x >> 6);
-  if (row >= M) return;
+  if (row >= rows) return;
   const int64_t nv = K >> 3, nb = (K + 127) >> 7;
   const int64_t j0 = (int64_t)(blockIdx.x % chunks) * (64 * QV) + lane;
   const u32x4* xr = reinterpret_cast<const u32x4*>(x + row * K);
@@ -175,13 +176,14 @@ __device__ __forceinline__ void gate_gradients(uint32_t dh, uint32_t g, uint32_t
 constexpr int GV = 2;  // vectors of 8 channels per lane
 
 template <bool SILU>
-__global__ __launch_bounds__(256) void k_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M,
-                                                        int64_t H, int64_t pitch, uint32_t chunks, uint16_t* dg,
-                                                        uint16_t* du, uint8_t* __restrict__ q, float* __restrict__ s) {
+__global__ __launch_bounds__(256) void k_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
+                                                        int64_t rows, int64_t M, int64_t H, int64_t pitch, uint32_t chunks,
+                                                        uint16_t* dg, uint16_t* du, uint8_t* __restrict__ q,
+                                                        float* __restrict__ s) {
   // a lane has read all of its vectors before it writes the first: dg and du may be dh, g or u themselves
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)(blockIdx.x / chunks) * 4 + (threadIdx.x >> 6);
-  if (row >= M) return;
+  if (row >= rows) return;
   const int64_t nv = H >> 3, nb = (H + 127) >> 7;
   const int64_t j0 = (int64_t)(blockIdx.x % chunks) * (64 * GV) + lane;
   u32x4 v[GV][3];
@@ -1060,18 +1062,36 @@ Fp8bArgs product_args(const Fp8bWeight* w, int n, int64_t M, int64_t K, int64_t 
   return p;
 }
 
+// A grid's threads are counted in 32 bits, and the runtime launches what is left of more without an error: kernels with
+// a workgroup for every four rows and chunk run on slices of so many rows, f(first row, rows, grid).
+constexpr int64_t kMostBlocks = int64_t(1) << 23;
+
+template <class F>
+hipError_t row_slices(int64_t M, int64_t chunks, const F& f) {
+  const int64_t each = kMostBlocks / chunks * 4;  // chunks: at most 2^20, of rows below 2^31
+  for (int64_t r0 = 0; r0 < M; r0 += each) {
+    const int64_t rows = M - r0 < each ? M - r0 : each;
+    f(r0, rows, dim3((unsigned)((rows + 3) / 4 * chunks)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_quant_fp8b(const uint16_t* x, int64_t M, int64_t K, int64_t pitch, bool slab, uint8_t* xq, float* xs,
                              hipStream_t stream) {
   const int64_t chunks = (pitch / 8 + 64 * QV - 1) / (64 * QV);
-  const dim3 grid((unsigned)((M + 3) / 4 * chunks)), block(256);
-  if (slab) {
-    hipLaunchKernelGGL(k_quant_fp8b<true>, grid, block, 0, stream, x, M, K, pitch, (uint32_t)chunks, xq, xs);
-  } else {
-    hipLaunchKernelGGL(k_quant_fp8b<false>, grid, block, 0, stream, x, M, K, pitch, (uint32_t)chunks, xq, xs);
-  }
-  return hipGetLastError();
+  return row_slices(M, chunks, [&](int64_t r0, int64_t rows, dim3 grid) {
+    if (slab) {
+      hipLaunchKernelGGL(k_quant_fp8b<true>, grid, dim3(256), 0, stream, x + r0 * K, rows, M, K, pitch, (uint32_t)chunks,
+                         xq + r0 * pitch, xs + r0);
+    } else {
+      hipLaunchKernelGGL(k_quant_fp8b<false>, grid, dim3(256), 0, stream, x + r0 * K, rows, M, K, pitch,
+                         (uint32_t)chunks, xq + r0 * pitch, xs + r0 * ((K + 127) / 128));
+    }
+  });
 }
 
 hipError_t launch_quant_weight_fp8b(const uint16_t* w, int64_t N, int64_t K, uint8_t* wq, float* ws,
@@ -1093,13 +1113,18 @@ hipError_t launch_transpose_fp8b(const uint8_t* w, const float* ws, int64_t N, i
 hipError_t launch_gated_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t M, int64_t H,
                                  bool silu, uint16_t* dg, uint16_t* du, uint8_t* q, float* s, hipStream_t stream) {
   const int64_t chunks = ((H + 127) / 128 * 16 + 64 * GV - 1) / (64 * GV), pitch = 2 * ((H + 127) / 128 * 128);
-  const dim3 grid((unsigned)((M + 3) / 4 * chunks)), block(256);
-  if (silu) {
-    hipLaunchKernelGGL(k_gated_backward<true>, grid, block, 0, stream, dh, g, u, M, H, pitch, (uint32_t)chunks, dg, du, q, s);
-  } else {
-    hipLaunchKernelGGL(k_gated_backward<false>, grid, block, 0, stream, dh, g, u, M, H, pitch, (uint32_t)chunks, dg, du, q, s);
-  }
-  return hipGetLastError();
+  return row_slices(M, chunks, [&](int64_t r0, int64_t rows, dim3 grid) {
+    const int64_t at = r0 * H;
+    uint16_t* const og = dg ? dg + at : nullptr;
+    uint16_t* const ou = du ? du + at : nullptr;
+    if (silu) {
+      hipLaunchKernelGGL(k_gated_backward<true>, grid, dim3(256), 0, stream, dh + at, g + at, u + at, rows, M, H, pitch,
+                         (uint32_t)chunks, og, ou, q + r0 * pitch, s + r0);
+    } else {
+      hipLaunchKernelGGL(k_gated_backward<false>, grid, dim3(256), 0, stream, dh + at, g + at, u + at, rows, M, H, pitch,
+                         (uint32_t)chunks, og, ou, q + r0 * pitch, s + r0);
+    }
+  });
 }
 
 bool fp8b_one_launch(int64_t M, int64_t K) { return fp8b_token_fits(M, K); }

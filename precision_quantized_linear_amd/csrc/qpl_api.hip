@@ -951,6 +951,13 @@ qpl_status check_fp8b_weight(const qpl_fp8b_weight* w) {
   return QPL_OK;
 }
 
+// A weight that is taken block by block, a workgroup for each block of K: a grid has fewer than 2^32 threads.
+qpl_status check_fp8b_blocks(int64_t N, int64_t K) {
+  const qpl_status s = check_dims(N, K);
+  if (s != QPL_OK) return s;
+  return blocks128(K) < int64_t(1) << 24 ? QPL_OK : QPL_ERR_SHAPE;
+}
+
 qpl_status fp8b_linear(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* weight,
                        const float* weight_scale, const qpl_epilogue* epi, uint16_t* y, void* ws, size_t ws_bytes,
                        void* stream) {
@@ -1016,7 +1023,7 @@ QPL_EXPORT qpl_status quant_weight_fp8b(const uint16_t* w, int64_t N, int64_t K,
                                         void* stream) {
   if (!w || !w_q || !w_scale) return QPL_ERR_NULL;
   if (!aligned16(w) || !aligned16(w_q) || !aligned4(w_scale)) return QPL_ERR_ALIGN;
-  qpl_status s = check_dims(N, K);
+  qpl_status s = check_fp8b_blocks(N, K);
   if (s != QPL_OK) return s;
   if ((s = check_device()) != QPL_OK) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -1028,7 +1035,7 @@ QPL_EXPORT qpl_status transpose_fp8b(const uint8_t* weight, const float* weight_
   if (!weight || !weight_scale || !weight_t || !weight_t_scale) return QPL_ERR_NULL;
   if (!aligned16(weight) || !aligned4(weight_scale) || !aligned16(weight_t) || !aligned4(weight_t_scale))
     return QPL_ERR_ALIGN;
-  qpl_status s = check_dims(N, K);
+  qpl_status s = check_fp8b_blocks(N, K);
   if (s != QPL_OK) return s;
   if ((s = check_dims(K, N)) != QPL_OK) return s;
   if ((s = check_device()) != QPL_OK) return s;

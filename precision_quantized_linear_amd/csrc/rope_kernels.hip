@@ -435,6 +435,8 @@ hipError_t by_lanes(int lanes, const F& f) {
 
 }  // namespace
 
+constexpr int64_t kMostBlocks = int64_t(1) << 23;
+
 hipError_t launch_qk_norm_rope(const RopeSide (&side)[2], int64_t tokens, int head_dim, const RopeArgs& r,
                                hipStream_t stream) {
   RopeKernelArgs p = kernel_args(side, tokens, head_dim, r);
@@ -443,15 +445,30 @@ hipError_t launch_qk_norm_rope(const RopeSide (&side)[2], int64_t tokens, int he
   // where that does not fill the chip, a token's heads go to several workgroups
   const int64_t per = int64_t(1) << p.lg_per, slots = int64_t(1) << p.lg_slots;
   const int64_t n = (tokens + per - 1) / per, turns = (p.heads + slots - 1) / slots, parts = (kFill + n - 1) / n;
-  const dim3 grid((unsigned)n, (unsigned)(parts < turns ? parts : turns));
   const size_t lds = angle_bytes(p);
+  // A grid's threads are counted in 32 bits, and the runtime launches what is left of more without an error: so many
+  // tokens go in slices.
+  const int64_t each = kMostBlocks << p.lg_per;
   return by_lanes(lanes, [&](auto lp) {
-    if (r.norm) {
-      hipLaunchKernelGGL((k_qk_norm_rope<decltype(lp)::value, true>), grid, dim3(256), lds, stream, p);
-    } else {
-      hipLaunchKernelGGL((k_qk_norm_rope<decltype(lp)::value, false>), grid, dim3(256), lds, stream, p);
+    for (int64_t t0 = 0; t0 < tokens; t0 += each) {
+      if (t0 > 0) {
+        for (Side& s : p.side) {
+          s.x += each * s.xt;
+          s.y += each * s.yt;
+        }
+        p.positions += each * p.axes;
+      }
+      p.tokens = tokens - t0 < each ? tokens - t0 : each;
+      const dim3 grid((unsigned)((p.tokens + per - 1) / per), (unsigned)(parts < turns ? parts : turns));
+      if (r.norm) {
+        hipLaunchKernelGGL((k_qk_norm_rope<decltype(lp)::value, true>), grid, dim3(256), lds, stream, p);
+      } else {
+        hipLaunchKernelGGL((k_qk_norm_rope<decltype(lp)::value, false>), grid, dim3(256), lds, stream, p);
+      }
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
   });
 }
 
