@@ -478,8 +478,8 @@ qpl_status qlinear_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t M,
  *   dweight (out, float [head_dim], or NULL) the weight's, summed over heads and tokens in a fixed order.  dx may be x
  *   or y itself.  ws at least qk_norm_rope_backward_workspace_bytes(tokens, head_dim) bytes (may be NULL without any
  *   dweight).
- * Errors: QPL_ERR_ARG for eps or scale not finite and > 0, a weight without norm, a dweight without weight, neither
- * norm nor rotation.
+ * Errors: QPL_ERR_ARG for eps or scale not finite and > 0, eps below 2^-126 (subnormal), a weight without norm, a
+ * dweight without weight, neither norm nor rotation.
  * qpl_rope_frequencies (host): base^(-2 i / rotary_dim), scaled for contexts longer than the trained ones:
  *   LINEAR  divided by factor;   NTK  with base * factor^(rotary_dim / (rotary_dim - 2));
  *   YARN    channels that turn at most low_turns times over trained_tokens are divided by factor, those that turn at

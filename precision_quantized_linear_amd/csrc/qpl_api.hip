@@ -1157,7 +1157,8 @@ qpl_status rope_of(const qpl_rope* rope, int64_t tokens, int64_t head_dim, int n
   r = qpl::RopeArgs{};
   if (tokens < 1 || tokens >= kMaxDim || head_dim < 16 || head_dim > kMaxHeadDim || head_dim % 16 != 0)
     return QPL_ERR_SHAPE;
-  if (norm && !positive_finite(eps)) return QPL_ERR_ARG;
+  // the reciprocal root instruction takes a subnormal number for zero, and a zero head would become 0 times infinity
+  if (norm && !(positive_finite(eps) && std::isnormal(eps))) return QPL_ERR_ARG;
   r.norm = norm != 0;
   r.eps = eps;
   r.scale = 1.0f;

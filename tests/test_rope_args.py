@@ -1,0 +1,34 @@
+"""Arguments of the norm and rotation of heads that no result could be right for."""
+import ctypes
+
+import pytest
+import torch
+
+import precision_quantized_linear_amd as qpl
+
+ARG = 4
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_subnormal_eps(backward):
+    lib = qpl.load()
+    h = qpl.Heads(1 << 20, 1 << 21, 3, 640, 128, 640, 128, None, 1 << 22, 640, 128)
+
+    def call(eps):
+        args = (ctypes.byref(h), None, 5, 128, 1, eps, None)
+        return lib.qk_norm_rope_backward(*args, None, 0, None) if backward else lib.qk_norm_rope(*args, None)
+    for eps in (1e-38, 2.0 ** -127, 1e-40, 2.0 ** -149):
+        assert call(eps) == ARG, eps
+    if not torch.cuda.is_available():
+        assert call(2.0 ** -126) not in (0, ARG)
+
+
+@pytest.mark.gpu
+def test_zero_heads_with_the_smallest_eps():
+    x = torch.zeros((2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    for eps in (2.0 ** -126, 1e-30):
+        y, _ = qpl.qk_norm_rope(x, None, None, None, eps=eps)
+        dx, _, _, _ = qpl.qk_norm_rope_backward(torch.zeros_like(x), None, x, None, None, None, eps=eps)
+        assert not y.any() and not dx.any()
+    with pytest.raises(qpl.QPLError):
+        qpl.qk_norm_rope(x, None, None, None, eps=1e-38)
