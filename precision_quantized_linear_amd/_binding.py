@@ -868,7 +868,7 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
     s = None
     if scaling is not None:
         s = RopeScaling(_ROPE_KINDS[scaling], factor, trained_tokens, low_turns, high_turns)
-    out = torch.empty((max(rotary_dim // 2, 1),), dtype=torch.float32)
+    out = torch.empty((max(rotary_dim // 2, 1),), dtype=torch.float32, device="cpu")
     scale = ctypes.c_float()
     _check("qpl_rope_frequencies", load().qpl_rope_frequencies(rotary_dim, base, _ref(s), _ptr(out),
                                                                ctypes.byref(scale)))

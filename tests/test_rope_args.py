@@ -1,4 +1,5 @@
-"""Arguments of the norm and rotation of heads that no result could be right for."""
+"""Arguments of the norm and rotation of heads that no result could be right for, and the frequencies where torch's
+default device is not the host."""
 import ctypes
 
 import pytest
@@ -21,6 +22,14 @@ def test_subnormal_eps(backward):
         assert call(eps) == ARG, eps
     if not torch.cuda.is_available():
         assert call(2.0 ** -126) not in (0, ARG)
+
+
+def test_frequencies_under_another_default_device():
+    # the library writes them on the host, wherever torch would put a new tensor
+    want, scale = qpl.rope_frequencies(64, scaling="yarn", factor=4.0, trained_tokens=4096)
+    with torch.device("meta"):
+        got, s = qpl.rope_frequencies(64, scaling="yarn", factor=4.0, trained_tokens=4096)
+    assert got.device.type == "cpu" and torch.equal(got, want) and s == scale
 
 
 @pytest.mark.gpu
