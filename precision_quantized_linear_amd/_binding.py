@@ -785,6 +785,8 @@ def _rope(positions, inv_freq, tokens, interleaved, sections, scale, dev):
     axes = 1 if sections is None else len(sections)
     if sections is not None and not 1 <= axes <= 4:
         raise ValueError(f"sections: expected one to four numbers of pairs, got {axes}")
+    if sections is not None and axes == 1 and sections[0] != n:
+        raise ValueError(f"sections: expected {n} pairs in all, got {tuple(sections)}")
     if axes > 1 and positions.dim() != 2:
         raise ValueError(f"positions: expected [tokens, {axes}] for {axes} sections, got {tuple(positions.shape)}")
     shape = (tokens, axes) if positions.dim() == 2 else (tokens,)

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import precision_quantized_linear_amd as qpl
+from precision_quantized_linear_amd import _binding as binding
 
 ARG = 4
 
@@ -30,6 +31,14 @@ def test_frequencies_under_another_default_device():
     with torch.device("meta"):
         got, s = qpl.rope_frequencies(64, scaling="yarn", factor=4.0, trained_tokens=4096)
     assert got.device.type == "cpu" and torch.equal(got, want) and s == scale
+
+
+@pytest.mark.parametrize("sections", [(5,), (9,), (0,)])
+def test_one_section_that_is_not_all_pairs(sections):
+    pos, freq = torch.zeros((4, 1), dtype=torch.int32), torch.ones(8)
+    assert binding._rope(pos, freq, 4, False, (8,), 1.0, -1) == binding._rope(pos[:, 0], freq, 4, False, None, 1.0, -1)
+    with pytest.raises(ValueError, match="^sections:"):
+        binding._rope(pos, freq, 4, False, sections, 1.0, -1)
 
 
 @pytest.mark.gpu
