@@ -579,11 +579,17 @@ __device__ __forceinline__ void store16_path(const Acc& acc, int lane, int64_t m
   });
 }
 
+// This lane's number in its wavefront, made anew at each call: one that is kept costs a register all along.
+__device__ __forceinline__ int lane_id() {
+  int lane;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(lane));
+  return lane;
+}
+
 template <int NJ, int NI, int EPI, bool ANY, class Acc>
-__device__ __forceinline__ int store16(const Acc& acc, int lane_, int64_t m0, int64_t n0, int64_t M, int64_t N,
+__device__ __forceinline__ int store16(const Acc& acc, int64_t m0, int64_t n0, int64_t M, int64_t N,
                                        uint16_t* __restrict__ y, const EpiArgs& e) {
-  int lane = lane_;
-  asm volatile("" : "+v"(lane));  // what follows is not to be computed before the products, where registers are scarce
+  const int lane = lane_id();  // what follows is not to be computed before the products, where registers are scarce
   if (m0 + 16 * NJ <= M && n0 + 16 * NI <= N) {
     store16_path<NJ, NI, EPI, ANY, true>(acc, lane, m0, n0, M, N, y, e);
     return NJ * NI / 2;
@@ -624,8 +630,7 @@ k_fp8b_staged(Fp8bStagedArgs) {
   const int pieces = args()->g.pieces, np = pieces * args()->g.segs;
 
   struct Tile {
-    int64_t m0, n0;
-    int rows;
+    int m0, n0, rows;
   };
   // This workgroup's i-th unit: a tile, or a part of one of the last round's; rows <= 0 if there is none.
   // Workgroups are dealt to the 8 XCDs in turn; in every round, the last and shorter one too, an XCD's workgroups
@@ -652,10 +657,9 @@ k_fp8b_staged(Fp8bStagedArgs) {
     const bool whole = u < full;
     const int cut = whole ? 0 : (u - full) % parts;
     walk(whole ? u : full + (u - full) / parts, a->tiles_m, a->tiles_n, tm, tn);
-    t.n0 = (int64_t)tn * COLS;
-    t.m0 = (int64_t)tm * XR;
-    const int64_t M = a->g.M;
-    t.rows = (int)(M - t.m0 < XR ? M - t.m0 : XR);
+    t.n0 = tn * COLS;  // M and N are below 2^31
+    t.m0 = tm * XR;
+    t.rows = min((int)a->g.M - t.m0, XR);
     if (!whole && parts > 1) {
       const int first = XR / parts * cut;
       t.m0 += first;
@@ -676,9 +680,8 @@ k_fp8b_staged(Fp8bStagedArgs) {
   }
   const int job = wv < XR / 64 ? 0 : wv - XR / 64 + 1;  // scales: of x, of the first weight, of the second
   const bool scales = job <= (GATED ? 2 : 1);
-  uint32_t vs = kOutOfRange;
-  if (job == 0) vs = (uint32_t)((64 * wv + lane) * 4);
-  if (job != 0 && scales && lane < (COLS + 127) / 128) vs = (uint32_t)(lane * pieces * 4);
+  // a lane's scale lies vs_step bytes behind the lane's before it: the next row's of x, the next 128 rows' of a weight
+  const uint32_t vs_step = job == 0 ? 4 : (uint32_t)pieces * 4, vs0 = !scales ? kOutOfRange : job == 0 ? 256u * wv : 0;
 
   // The stream of pieces: what the loads of the next one need.  Past the last tile the operands have no rows, and
   // zeros are loaded.
@@ -686,19 +689,18 @@ k_fp8b_staged(Fp8bStagedArgs) {
   const uint8_t *xp = nullptr, *wp = nullptr;
   const float* sp = nullptr;
   int x_bytes = 0, w_bytes = 0, sp_bytes = 0, sp_step = 0, kx = 0, kw = 0;
-  int64_t s_n0 = 0;
+  int s_n0 = 0;
   auto weight = [&](int which) {  // rows and scales of the tile in one of the weights
     Args* a = args();
-    const int rn = (int)(a->g.N - s_n0 < COLS ? a->g.N - s_n0 : COLS);
+    const int rn = min((int)a->g.N - s_n0, COLS);
     const int row_part = GATED ? wv & 1 : which;
-    wp = (row_part ? a->g.w[1] : a->g.w[0]) + s_n0 * a->g.K;
+    wp = (row_part ? a->g.w[1] : a->g.w[0]) + (int64_t)s_n0 * a->g.K;
     w_bytes = rn * a->g.K;
     if (job == 0) return;
     // one scale for every 128 rows of the weight, whose rows of scales are `pieces` long
     const int scale_part = GATED ? job - 1 : which;
-    const int64_t nb0 = s_n0 >> 7, left = ((a->g.N + 127) >> 7) - nb0;
-    const int nb = (int)(left < (COLS + 127) / 128 ? left : (COLS + 127) / 128);
-    sp = (scale_part ? a->g.ws[1] : a->g.ws[0]) + nb0 * pieces;
+    const int nb0 = s_n0 >> 7, nb = min((int)((a->g.N + 127) >> 7) - nb0, (COLS + 127) / 128);
+    sp = (scale_part ? a->g.ws[1] : a->g.ws[0]) + (int64_t)nb0 * pieces;
     sp_bytes = ((nb - 1) * pieces + 1) * 4;
     sp_step = 1;
   };
@@ -718,7 +720,7 @@ k_fp8b_staged(Fp8bStagedArgs) {
         if (t.rows > 0) {
           Args* a = args();
           s_n0 = t.n0;
-          xp = a->g.x + t.m0 * a->g.px;
+          xp = a->g.x + (int64_t)t.m0 * a->g.px;
           x_bytes = t.rows * a->g.px;
           weight(0);
           if (job == 0) {
@@ -737,23 +739,21 @@ k_fp8b_staged(Fp8bStagedArgs) {
       ++s_i;
     }
   };
-  // px, pw: pitches of x and W.  What a load is ahead of the operand's start (its rows, and K) moves the descriptor's
-  // start, whose size shrinks by as much: rows past the operand's last, and everything where there is no tile, are past
-  // its end.  The same in the lanes' offsets takes a register, which the 256 x 256 shape does not have in its loop.
-  auto rest = [](const uint8_t* at, int bytes, int ahead) {
-    return make_desc(at + ahead, bytes > ahead ? bytes - ahead : 0);
-  };
+  // px, pw: pitches of x and W.  A lane's whole offset is in voff: rows past the operand's last, and everything where
+  // there is no tile, are past the descriptor's end by it.  With the rows' and K's part moving the descriptor's start
+  // and size instead (five scalar instructions a load) the gated 4096 x 4096 x 2 * 10752 took 375 us for 369.
   auto issue = [&](int d, int px, int pw) {
     const uint32_t st = lbase + l_stage * STAGE;
     if (d < XL) {
-      dma16(st + XB + (XR / W * wv + 8 * d) * PR_ROW, d & 1 ? vx ^ 64 : vx, rest(xp, x_bytes, kx + 8 * d * px));
+      dma16(st + XB + (XR / W * wv + 8 * d) * PR_ROW, (d & 1 ? vx ^ 64 : vx) + (uint32_t)(kx + 8 * d * px),
+            make_desc(xp, x_bytes));
     } else if (d < XL + WL) {
       const int n = d - XL;
-      dma16(st + WB + (WR / W * wv + 8 * n) * PR_ROW, n & 1 ? vw + (lane & 4 ? -64 : 64) : vw,
-            rest(wp, w_bytes, kw + 8 * n * pw));
+      dma16(st + WB + (WR / W * wv + 8 * n) * PR_ROW,
+            (n & 1 ? vw + (lane & 4 ? -64 : 64) : vw) + (uint32_t)(kw + 8 * n * pw), make_desc(wp, w_bytes));
     } else {
-      dma4(scales ? st + (job == 0 ? 256 * wv : 4 * XR + 256 * (job - 1)) : lbase + S * STAGE, vs,
-           make_desc(sp, sp_bytes));
+      dma4(scales ? st + (job == 0 ? 256 * wv : 4 * XR + 256 * (job - 1)) : lbase + S * STAGE,
+           __umul24((uint32_t)lane_id(), vs_step) + vs0, make_desc(sp, sp_bytes));
     }
   };
 
@@ -910,7 +910,8 @@ k_fp8b_staged(Fp8bStagedArgs) {
 #pragma unroll
     for (int d = EARLY; d < LOADS; ++d) issue(d, px, pw);
     Args* a = args();
-    const int64_t m0 = t.m0 + wm * 16 * NJ, n0 = t.n0 + wn * 16 * NO, m1 = t.m0 + t.rows, N = a->g.N;
+    const int64_t m0 = (int64_t)t.m0 + wm * 16 * NJ, n0 = (int64_t)t.n0 + wn * 16 * NO, m1 = (int64_t)t.m0 + t.rows,
+                  N = a->g.N;
     EpiArgs e{};
     if constexpr ((EPI & EPI_QKV) != 0) {
 #pragma unroll
@@ -925,8 +926,8 @@ k_fp8b_staged(Fp8bStagedArgs) {
     if constexpr (GATED) {
       uint16_t *g = a->g.save[0], *u = a->g.save[1];
       if (g) {
-        left += store16<NJ, NO, 0, false>(acc, lane, m0, n0, m1, N, g, e);
-        left += store16<NJ, NO, 0, false>(acc + NO, lane, m0, n0, m1, N, u, e);
+        left += store16<NJ, NO, 0, false>(acc, m0, n0, m1, N, g, e);
+        left += store16<NJ, NO, 0, false>(acc + NO, m0, n0, m1, N, u, e);
       }
 #pragma unroll
       for (int i = 0; i < NO; ++i)
@@ -936,9 +937,9 @@ k_fp8b_staged(Fp8bStagedArgs) {
           for (int r = 0; r < 4; ++r) acc[i][j][r] = gate_act<EPI>(acc[i][j][r]) * acc[i + NO][j][r];
           __builtin_amdgcn_sched_barrier(0);
         }
-      left += store16<NJ, NO, 0, false>(acc, lane, m0, n0, m1, N, y, e);
+      left += store16<NJ, NO, 0, false>(acc, m0, n0, m1, N, y, e);
     } else {
-      left = store16<NJ, NO, EPI, true>(acc, lane, m0, n0, m1, N, y, e);
+      left = store16<NJ, NO, EPI, true>(acc, m0, n0, m1, N, y, e);
     }
     stores[0] = __builtin_amdgcn_readfirstlane(left);
   };
