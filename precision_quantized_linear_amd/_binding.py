@@ -864,7 +864,8 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
     """(inv_freq float32 [rotary_dim / 2], scale) for qk_norm_rope: base^(-2 i / rotary_dim), scaled for longer
     contexts by scaling "linear" (divided by factor), "ntk" (a larger base) or "yarn" (channels that turn at most
     low_turns times over trained_tokens are divided by factor, those that turn at least high_turns times are kept,
-    and scale = 0.1 ln(factor) + 1)."""
+    in between mixed linearly in the number of turns, not in the channel's index, and scale = 0.1 ln(factor) + 1).
+    Without device on the host."""
     if scaling is not None and scaling not in _ROPE_KINDS:
         raise ValueError(f"scaling: expected one of {sorted(_ROPE_KINDS)}, got {scaling!r}")
     s = None

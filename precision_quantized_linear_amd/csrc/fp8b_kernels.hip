@@ -2,9 +2,10 @@
 // codes, a scale for every 128 channels of a row of x and for every 128 x 128 block of the weight.
 //
 // A block's scale is s = max |v| times fp32(1 / 448), its codes E4M3(v / s) of the correctly rounded quotient; a zero
-// block has s = 0 and codes 0.  A block's products are summed by the FP8 matrix instructions, which cut each
-// product of a group of eight below 2^-13 of the group's largest (no FP8 form of this chip does otherwise), and
-// each sum is folded into fp32 accumulators as acc += P (s_x s_w): one product and one fma per output and block.
+// block has s = 0 and signed-zero codes.  A block's products are summed by the FP8 matrix instructions, which cut each
+// product of a group of eight below 2^-13 of the group's largest (measured with constructed operands for this form,
+// the 32 x 32 x 64 one and the unscaled one), and each sum is folded into fp32 accumulators as acc += P (s_x s_w): one product and one fma per output and block.
+#include "qpl_dma_lane.h"
 #include "qpl_fp8b_shape.h"
 #include "qpl_fp8.h"
 #include "qpl_piece.h"
@@ -500,9 +501,12 @@ __global__ __launch_bounds__(64 * TOKEN_W) void k_fp8b_token(const uint16_t* __r
 // pieces behind the next and the output stores of an epilogue issued after its loads.  A smaller number than that only
 // waits longer.
 //
-// Bound by power and the matrix unit together (1.9 to 2.1 GHz under load): 4096 x 4096 x 12288 to q, k, v 210 us of 221
-// with the quantizer's (2.0 PFLOP/s), gated 4096 x 4096 x 2 * 10752 with both projections kept 358 of 368 (2.0
-// PFLOP/s), two segments 4096 x 21504 x 4096 303 us (2.4 PFLOP/s: few tile ends).  The same on 32 x 32 x 64 tiles, two
+// Bound by the matrix unit and the instructions beside it, power and the tile ends: 4096 x 4096 x 12288 to q, k, v 208
+// us of 219 with the quantizer's (2.0 PFLOP/s), gated 4096 x 4096 x 2 * 10752 with both projections kept 355 of 366 (2.0
+// PFLOP/s), two segments 4096 x 21504 x 4096 310 us (2.3 PFLOP/s: few tile ends).  4096 x K x 12288, three tiles for
+// each workgroup, takes 43, 104, 188, 361 and 704 us at K = 512, 2048, 4096, 8192 and 16384: 1.7 to 1.8 us a piece and
+// 20 us for the launch and the three tiles' first pieces and ends.  To q, k, v it takes 17 to 32 us more at any of
+// them: the stores' addresses, of three tensors in 64 bits.  The same on 32 x 32 x 64 tiles, two
 // of them and sixteen fmas for a block, with the sync at a piece's end took 246, 425 and 370 us.
 // ---------------------------------------------------------------------------
 struct Fp8bStagedArgs {

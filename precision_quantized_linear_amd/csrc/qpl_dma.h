@@ -35,23 +35,11 @@ __device__ __forceinline__ u32x4 make_desc(const void* base, int64_t bytes) {
 // LDS read: the pipelines count them themselves (QPL_WAIT_VMCNT).
 // The LDS address and soffset are wave-uniform; readfirstlane makes them scalar
 // operands even where the compiler keeps a uniform value in a vector register.
-// Whether a lane reads or gets zeros has to follow from voff alone: documents differ
-// on whether soffset counts in the comparison with the descriptor's size, and on what
-// happens where it exceeds that size.  So soffset only moves a lane along its own row;
-// a lane whose row or columns are not there has kOutOfRange in voff.  The forms without
-// soffset leave it all to voff and to the descriptor's start and size.
 __device__ __forceinline__ void dma16(uint32_t lds_addr, uint32_t voff, u32x4 desc, int soffset) {
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(desc),
                  "s"(__builtin_amdgcn_readfirstlane(soffset))
-               : "memory");
-}
-
-__device__ __forceinline__ void dma16(uint32_t lds_addr, uint32_t voff, u32x4 desc) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(desc)
                : "memory");
 }
 
@@ -63,13 +51,6 @@ __device__ __forceinline__ void dma4(uint32_t lds_addr, uint32_t voff, u32x4 des
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(desc),
                  "s"(__builtin_amdgcn_readfirstlane(soffset))
-               : "memory");
-}
-
-__device__ __forceinline__ void dma4(uint32_t lds_addr, uint32_t voff, u32x4 desc) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(desc)
                : "memory");
 }
 

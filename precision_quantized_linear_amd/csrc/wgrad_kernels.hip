@@ -1,5 +1,5 @@
 // Gradient of a linear's weight for gfx950: dW [N, K] (fp32) = dy^T x of bf16 dy [M, N] and x [M, K].
-#include "qpl_dma.h"
+#include "qpl_dma_lane.h"
 #include "qpl_internal.h"
 
 namespace qpl {
