@@ -464,8 +464,8 @@ qpl_status qlinear_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t M,
  *     n = x w / sqrt(mean over the head of x^2 + eps)      (norm != 0; w bf16 [head_dim], or NULL for ones)
  *     (a, b) -> scale (a cos t - b sin t, a sin t + b cos t),  t = position * inv_freq[i]
  *   for pair i of the first rotary_dim channels: channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
- *   interleaved.  The other channels are not rotated.  All in fp32 up to the one rounding of the result; angles in
- *   fp64, so that far positions keep theirs.
+ *   interleaved.  The other channels are not rotated.  All in fp32 up to the one rounding of the result (the sum of a
+ *   head's squares too: it overflows where values pass 2^59); angles in fp64, so that far positions keep theirs.
  * A tensor's element (head, token, channel) lies at head * head_stride + token * token_stride + channel; strides are
  * multiples of 8 elements.  heads up to 65536, head_dim a multiple of 16 up to 512.  The output may be the input
  * itself (same pointer and strides); other overlaps are not allowed, and a written view may not hold two elements in
@@ -483,7 +483,9 @@ qpl_status qlinear_weight_grad(const uint16_t* dy, const uint16_t* x, int64_t M,
  * qpl_rope_frequencies (host): base^(-2 i / rotary_dim), scaled for contexts longer than the trained ones:
  *   LINEAR  divided by factor;   NTK  with base * factor^(rotary_dim / (rotary_dim - 2));
  *   YARN    channels that turn at most low_turns times over trained_tokens are divided by factor, those that turn at
- *           least high_turns times are kept, in between linearly mixed, and *scale = 0.1 ln(factor) + 1 (else 1).
+ *           least high_turns times are kept, in between both are mixed, linearly in the number of turns (a ramp that
+ *           is linear in the channel's index instead gives other frequencies), and *scale = 0.1 ln(factor) + 1 (else
+ *           1).
  */
 typedef struct {
   const uint16_t* x;
