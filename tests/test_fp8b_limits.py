@@ -12,6 +12,13 @@ SHAPE = 2
 A, B, C, D = (ctypes.c_void_p(1 << i) for i in range(20, 24))
 
 
+@pytest.fixture(autouse=True)
+def give_back():
+    yield
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
 def test_refused_weights():
     lib = qpl.load()
     for K in ((1 << 31) - 112, (1 << 31) - 16):
